@@ -15,6 +15,15 @@ is missing, every call raises.
     hc = eq.prepare_conv_weights(psi)         # p4 group convolution, psi [C_out, C_in, 4, k, k]
     y = eq.conv_forward(hc, x, b)             # x [B, H, W, C_in, 4] -> y [B, H, W, C_out, 4]
 
+The operators between the layers of a transformer stage (include/eqlin.h has their formulas):
+
+    y, s, rstd = eq.rmsnorm(x, gamma, residual=r)              # x, r: [N, C, G]; gamma: [C]
+    q, scale, s, rstd = eq.rmsnorm_quant(x, gamma, residual=r) # q: float8_e4m3fn, one scale a token
+    dx, dgamma = eq.rmsnorm_backward(dy, s, gamma, rstd, ds=ds)
+    qk = eq.rotary(qk, pos, pairs=(4, 4))                      # qk: [N, H, dc, G]; pos: int32 [N, axes]
+    o, lse = eq.attention(q, k, v, cu_q, cu_k, causal=False)   # q: [T, H, D] or [T, H, dc, G]
+    dq, dk, dv = eq.attention_backward(do, q, k, v, o, lse, cu_q, cu_k, causal=False)
+
 Method: "Flash EQ-Linear: Accelerating Equivariant Linear Layers via Group-wise Discrete Fourier
 Transform" (explainer page, gist.science/es/paper/2607.21271).
 """
@@ -41,6 +50,8 @@ EQLIN_PREPARE_BACKWARD = 2
 EQLIN_PREPARE_D4 = 4
 EQLIN_PREPARE_FIXED_KERNEL = 8
 GROUPS = ("cyclic", "d4")
+EQLIN_ROTARY_INVERSE = 1
+EQLIN_ROTARY_D4 = 4
 EQLIN_ACT_NONE = 0
 EQLIN_ACT_GELU = 1
 _ACTS = {None: EQLIN_ACT_NONE, "none": EQLIN_ACT_NONE, "gelu": EQLIN_ACT_GELU}
@@ -53,9 +64,31 @@ EXPORTED = (
     "eqlin_export_spectral_weights", "eqlin_export_expanded_weight", "eqlin_describe",
     "eqlin_status_string", "eqlin_last_error", "eqlin_version",
     "eqlin_prepare_conv_weights", "eqlin_conv_forward", "eqlin_conv_forward_expanded",
+    "eqlin_rmsnorm", "eqlin_rmsnorm_quant", "eqlin_rmsnorm_backward_workspace", "eqlin_rmsnorm_backward",
+    "eqlin_rotary", "eqlin_attention_workspace", "eqlin_attention", "eqlin_attention_backward_workspace",
+    "eqlin_attention_backward",
 )
 
 _lib = None
+
+_vp, _i32, _i64, _f32 = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_float
+
+
+class AttentionArgs(ctypes.Structure):
+    """eqlin_attention_args."""
+    _fields_ = [("q", _vp), ("k", _vp), ("v", _vp), ("o", _vp), ("lse", _vp),
+                ("q_token_stride", _i64), ("q_head_stride", _i64), ("k_token_stride", _i64), ("k_head_stride", _i64),
+                ("v_token_stride", _i64), ("v_head_stride", _i64), ("o_token_stride", _i64), ("o_head_stride", _i64),
+                ("cu_q", _vp), ("cu_k", _vp), ("len_k", _vp), ("total_q", _i64), ("total_k", _i64),
+                ("batch", _i32), ("heads_q", _i32), ("heads_kv", _i32), ("dim", _i32),
+                ("scale", _f32), ("causal", _i32), ("dtype", _i32)]
+
+
+class AttentionGrads(ctypes.Structure):
+    """eqlin_attention_grads."""
+    _fields_ = [("d_o", _vp), ("dq", _vp), ("dk", _vp), ("dv", _vp),
+                ("do_token_stride", _i64), ("do_head_stride", _i64), ("dq_token_stride", _i64), ("dq_head_stride", _i64),
+                ("dk_token_stride", _i64), ("dk_head_stride", _i64), ("dv_token_stride", _i64), ("dv_head_stride", _i64)]
 
 
 class EqlinError(RuntimeError):
@@ -107,6 +140,22 @@ def load_library() -> ctypes.CDLL:
                  "eqlin_conv_forward_expanded",
                  "eqlin_export_spectral_weights", "eqlin_export_expanded_weight"):
         getattr(lib, name).restype = i32
+    szt, f32, args, grads = ctypes.c_size_t, ctypes.c_float, ctypes.POINTER(AttentionArgs), ctypes.POINTER(AttentionGrads)
+    lib.eqlin_rmsnorm.argtypes = [vp, vp, vp, vp, vp, vp, i64, i32, i32, f32, i32, vp]
+    lib.eqlin_rmsnorm_quant.argtypes = [vp, vp, vp, vp, vp, vp, vp, i64, i32, i32, f32, i32, vp]
+    lib.eqlin_rmsnorm_backward.argtypes = [vp, vp, vp, vp, vp, vp, vp, i64, i32, i32, i32, vp, szt, vp]
+    lib.eqlin_rmsnorm_backward_workspace.argtypes = [i64, i32, i32]
+    lib.eqlin_rotary.argtypes = [vp, i64, i64, vp, i64, i64, vp, i64, i32, i32, i32, i32, ctypes.POINTER(i32),
+                                 ctypes.c_double, u32, i32, vp]
+    lib.eqlin_attention_workspace.argtypes = [args]
+    lib.eqlin_attention.argtypes = [args, vp, szt, vp]
+    lib.eqlin_attention_backward_workspace.argtypes = [args]
+    lib.eqlin_attention_backward.argtypes = [args, grads, vp, szt, vp]
+    for name in ("eqlin_rmsnorm", "eqlin_rmsnorm_quant", "eqlin_rmsnorm_backward", "eqlin_rotary", "eqlin_attention",
+                 "eqlin_attention_backward"):
+        getattr(lib, name).restype = i32
+    for name in ("eqlin_rmsnorm_backward_workspace", "eqlin_attention_workspace", "eqlin_attention_backward_workspace"):
+        getattr(lib, name).restype = szt
     _lib = lib
     return lib
 
@@ -383,6 +432,242 @@ def conv_forward_expanded(h: Handle, x: torch.Tensor, b: torch.Tensor | None = N
     if not h.expanded:
         raise ValueError("handle was prepared without expanded=True")
     return _conv(load_library().eqlin_conv_forward_expanded, "eqlin_conv_forward_expanded", h, x, b, y)
+
+
+# ---- the operators between the layers of a transformer stage ----
+
+
+def _on(device, fn, *args):
+    """fn(*args, current stream) with ``device`` current: the launch goes where the tensors are."""
+    stream = torch.cuda.current_stream(device).cuda_stream
+    if torch.cuda.current_device() == device.index:
+        return fn(*args, stream)
+    with torch.cuda.device(device):
+        return fn(*args, stream)
+
+
+def _ptr(t: torch.Tensor | None):
+    return None if t is None else t.data_ptr()
+
+
+def _same(t: torch.Tensor, like: torch.Tensor, name: str, shape=None):
+    """t: contiguous, on like's device, of its dtype and shape (or ``shape``)."""
+    _need_cuda(t, name)
+    if t.dtype != like.dtype or t.device != like.device or tuple(t.shape) != tuple(like.shape if shape is None else shape):
+        raise ValueError(f"{name} must be {tuple(like.shape if shape is None else shape)} of {like.dtype} on {like.device}, "
+                         f"got {tuple(t.shape)} {t.dtype} on {t.device}")
+
+
+def _f32_out(t: torch.Tensor | None, shape, device, name: str):
+    if t is None:
+        return torch.empty(shape, dtype=torch.float32, device=device)
+    _need_cuda(t, name)
+    if t.dtype != torch.float32 or tuple(t.shape) != tuple(shape) or t.device != device:
+        raise ValueError(f"{name} must be {tuple(shape)} of float32 on {device}")
+    return t
+
+
+def _norm_args(x, gamma, residual):
+    _need_cuda(x, "x")
+    code = _dtype_code(x.dtype)
+    if x.dim() != 3:
+        raise ValueError(f"x must be [N, C, G], got {tuple(x.shape)}")
+    if residual is not None:
+        _same(residual, x, "residual")
+    if gamma is not None:
+        _same(gamma, x, "gamma", (x.shape[1],))
+    return code
+
+
+def rmsnorm(x: torch.Tensor, gamma: torch.Tensor | None = None, residual: torch.Tensor | None = None, eps: float = 1e-6,
+            y: torch.Tensor | None = None):
+    """eqlin_rmsnorm -> (y, s, rstd): s = x + residual (x itself without one), rstd [N] float32 over a token's
+    C * G values, y = s rstd gamma[c]. x: [N, C, G]; gamma: [C] of x's dtype or None."""
+    code = _norm_args(x, gamma, residual)
+    N, C, G = x.shape
+    if y is None:
+        y = torch.empty_like(x)
+    else:
+        _same(y, x, "y")
+    s = x if residual is None else torch.empty_like(x)
+    rstd = torch.empty((N,), dtype=torch.float32, device=x.device)
+    st = _on(x.device, load_library().eqlin_rmsnorm, x.data_ptr(), _ptr(residual), _ptr(gamma),
+             None if residual is None else s.data_ptr(), y.data_ptr(), rstd.data_ptr(), N, C, G, eps, code)
+    _check(st, "eqlin_rmsnorm")
+    return y, s, rstd
+
+
+def rmsnorm_quant(x: torch.Tensor, gamma: torch.Tensor | None = None, residual: torch.Tensor | None = None,
+                  eps: float = 1e-6):
+    """eqlin_rmsnorm_quant -> (q, scale, s, rstd): rmsnorm's y as q float8_e4m3fn [N, C, G] times scale [N]
+    float32 (the row's largest magnitude / 448)."""
+    code = _norm_args(x, gamma, residual)
+    N, C, G = x.shape
+    q = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=x.device)
+    s = x if residual is None else torch.empty_like(x)
+    rstd = torch.empty((N,), dtype=torch.float32, device=x.device)
+    scale = torch.empty((N,), dtype=torch.float32, device=x.device)
+    st = _on(x.device, load_library().eqlin_rmsnorm_quant, x.data_ptr(), _ptr(residual), _ptr(gamma),
+             None if residual is None else s.data_ptr(), q.data_ptr(), scale.data_ptr(), rstd.data_ptr(), N, C, G, eps, code)
+    _check(st, "eqlin_rmsnorm_quant")
+    return q, scale, s, rstd
+
+
+def rmsnorm_backward_workspace(N: int, C: int, G: int) -> int:
+    """Bytes of device scratch eqlin_rmsnorm_backward needs (0 without dgamma)."""
+    return int(load_library().eqlin_rmsnorm_backward_workspace(int(N), int(C), int(G)))
+
+
+def rmsnorm_backward(dy: torch.Tensor, s: torch.Tensor, gamma: torch.Tensor | None, rstd: torch.Tensor,
+                     ds: torch.Tensor | None = None, with_gamma: bool = True, workspace: torch.Tensor | None = None):
+    """eqlin_rmsnorm_backward -> (dx, dgamma): dx [N, C, G], the gradient of x and of the residual (ds: the
+    gradient that reaches s directly), and dgamma [C] float32 (None with with_gamma=False). s, rstd: rmsnorm's."""
+    code = _norm_args(s, gamma, None)
+    _same(dy, s, "dy")
+    if ds is not None:
+        _same(ds, s, "ds")
+    N, C, G = s.shape
+    _f32_out(rstd, (N,), s.device, "rstd")
+    dx = torch.empty_like(s)
+    dgamma = torch.empty((C,), dtype=torch.float32, device=s.device) if with_gamma else None
+    need = rmsnorm_backward_workspace(N, C, G) if with_gamma else 0
+    workspace = _workspace(workspace, need, s.device)
+    st = _on(s.device, load_library().eqlin_rmsnorm_backward, s.data_ptr(), _ptr(gamma), rstd.data_ptr(), dy.data_ptr(),
+             _ptr(ds), dx.data_ptr(), _ptr(dgamma), N, C, G, code, _ptr(workspace), need)
+    _check(st, "eqlin_rmsnorm_backward")
+    return dx, dgamma
+
+
+def _workspace(workspace: torch.Tensor | None, need: int, device):
+    """The caller's scratch where it is large enough, else a new one (torch's allocator keeps it for this stream)."""
+    if need == 0:
+        return None
+    if workspace is None or workspace.numel() * workspace.element_size() < need:
+        return torch.empty((need,), dtype=torch.uint8, device=device)
+    _need_cuda(workspace, "workspace")
+    if workspace.device != device:
+        raise ValueError(f"workspace must be on {device}")
+    return workspace
+
+
+def _heads(t: torch.Tensor, name: str):
+    """(tokens, heads, dim) of a [T, H, D] or [T, H, dc, G] view whose heads are contiguous."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA (HIP) tensor")
+    shape, strides = t.shape, t.stride()
+    if len(shape) == 4:
+        dim, ok = shape[2] * shape[3], (strides[3] == 1 or shape[3] == 1) and (strides[2] == shape[3] or shape[2] == 1)
+    elif len(shape) == 3:
+        dim, ok = shape[2], strides[2] == 1 or shape[2] == 1
+    else:
+        raise ValueError(f"{name} must be [T, H, D] or [T, H, dc, G], got {tuple(shape)}")
+    if not ok:
+        raise ValueError(f"{name}: a head's elements must be contiguous")
+    return shape[0], shape[1], dim
+
+
+def _index(t: torch.Tensor, name: str, shape, device):
+    _need_cuda(t, name)
+    if t.dtype != torch.int32 or tuple(t.shape) != tuple(shape) or t.device != device:
+        raise ValueError(f"{name} must be {tuple(shape)} of int32 on {device}, got {tuple(t.shape)} {t.dtype}")
+
+
+def rotary(x: torch.Tensor, pos: torch.Tensor, pairs, base: float = 10000.0, group: str = "cyclic", inverse: bool = False,
+           out: torch.Tensor | None = None) -> torch.Tensor:
+    """eqlin_rotary: x [N, H, dc, G] (or [N, H, D], G = 1; heads contiguous, tokens and heads strided) turned by
+    the positions pos, int32 [N, axes] ((row, column) last). pairs: channel pairs of each axis. inverse=True
+    turns back: the backward (dx from dy). out: a tensor to write to, x itself for in place."""
+    if group not in GROUPS:
+        raise ValueError(f"group must be one of {GROUPS}, got {group!r}")
+    N, H, D = _heads(x, "x")
+    G = x.shape[3] if x.dim() == 4 else 1
+    axes = len(pairs)
+    _index(pos, "pos", (N, axes), x.device)
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    elif out is not x:
+        _heads(out, "out")
+        if out.shape != x.shape or out.dtype != x.dtype or out.device != x.device:
+            raise ValueError(f"out must be {tuple(x.shape)} of {x.dtype} on {x.device}")
+    flags = (EQLIN_ROTARY_INVERSE if inverse else 0) | (EQLIN_ROTARY_D4 if group == "d4" else 0)
+    xs, ys = x.stride(), out.stride()
+    st = _on(x.device, load_library().eqlin_rotary, x.data_ptr(), xs[0], xs[1], out.data_ptr(), ys[0], ys[1],
+             pos.data_ptr(), N, H, D // G if G else 0, G, axes, (ctypes.c_int * axes)(*pairs), base, flags,
+             _dtype_code(x.dtype))
+    _check(st, "eqlin_rotary")
+    return out
+
+
+def _attention_args(q, k, v, o, lse, cu_q, cu_k, len_k, causal, scale):
+    Tq, Hq, D = _heads(q, "q")
+    Tk, Hkv, Dk = _heads(k, "k")
+    dev, dt = q.device, q.dtype
+    if _heads(v, "v") != (Tk, Hkv, Dk) or Dk != D:
+        raise ValueError(f"k and v must be [T, heads, {D}] alike, got {tuple(k.shape)} and {tuple(v.shape)}")
+    if k.dtype != dt or v.dtype != dt or k.device != dev or v.device != dev:
+        raise TypeError(f"q, k and v must be of one dtype on one device, got {dt}, {k.dtype}, {v.dtype}")
+    if _heads(o, "o") != (Tq, Hq, D) or o.dtype != dt or o.device != dev:
+        raise ValueError(f"o must be {tuple(q.shape)} of {dt} on {dev}")
+    _need_cuda(cu_q, "cu_q")
+    B = cu_q.numel() - 1
+    if B < 0:
+        raise ValueError("cu_q must hold batch + 1 entries")
+    _index(cu_q, "cu_q", (B + 1,), dev)
+    _index(cu_k, "cu_k", (B + 1,), dev)
+    if len_k is not None:
+        _index(len_k, "len_k", (B,), dev)
+    qs, ks, vs, os_ = q.stride(), k.stride(), v.stride(), o.stride()
+    return AttentionArgs(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), _ptr(lse), qs[0], qs[1], ks[0], ks[1],
+                         vs[0], vs[1], os_[0], os_[1], cu_q.data_ptr(), cu_k.data_ptr(), _ptr(len_k), Tq, Tk, B, Hq, Hkv, D,
+                         D ** -0.5 if scale is None else scale, 1 if causal else 0, _dtype_code(dt))
+
+
+def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: torch.Tensor, cu_k: torch.Tensor,
+              causal: bool = False, scale: float | None = None, len_k: torch.Tensor | None = None,
+              out: torch.Tensor | None = None, workspace: torch.Tensor | None = None):
+    """eqlin_attention -> (o, lse): attention over packed sequences. q: [T, Hq, D] or [T, Hq, dc, G] (tokens and
+    heads may be strided views, e.g. of a qkv layer's output), k and v: the same with Hkv heads, Hq a multiple
+    of Hkv. cu_q, cu_k: int32 [batch + 1], the sequences' bounds in tokens; len_k: int32 [batch], how many keys
+    of each stretch count. causal: token t of lq sees the keys j <= t + lk - lq. scale: 1/sqrt(D) if None.
+    o: like q; lse: float32 [T, Hq]."""
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
+    a = _attention_args(q, k, v, out, lse, cu_q, cu_k, len_k, causal, scale)
+    lib, pa = load_library(), ctypes.byref(a)
+    need = lib.eqlin_attention_workspace(pa)
+    workspace = _workspace(workspace, need, q.device)
+    _check(_on(q.device, lib.eqlin_attention, pa, _ptr(workspace), need), "eqlin_attention")
+    return out, lse
+
+
+def attention_backward(do: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.Tensor,
+                       lse: torch.Tensor, cu_q: torch.Tensor, cu_k: torch.Tensor, causal: bool = False,
+                       scale: float | None = None, len_k: torch.Tensor | None = None, dq: torch.Tensor | None = None,
+                       dk: torch.Tensor | None = None, dv: torch.Tensor | None = None,
+                       workspace: torch.Tensor | None = None):
+    """eqlin_attention_backward -> (dq, dk, dv) from do and the forward's tensors and arguments. dq, dk, dv:
+    tensors to write to (views of one gradient of a qkv layer's output, say), else new ones."""
+    a = _attention_args(q, k, v, o, lse, cu_q, cu_k, len_k, causal, scale)
+    _f32_out(lse, (a.total_q, a.heads_q), q.device, "lse")
+    grads = []
+    for name, t, like in (("dq", dq, q), ("dk", dk, k), ("dv", dv, v)):
+        if t is None:
+            t = torch.empty(like.shape, dtype=like.dtype, device=like.device)
+        elif _heads(t, name) != _heads(like, name) or t.dtype != like.dtype or t.device != like.device:
+            raise ValueError(f"{name} must be {tuple(like.shape)} of {like.dtype} on {like.device}")
+        grads.append(t)
+    dq, dk, dv = grads
+    if _heads(do, "do") != _heads(q, "q") or do.dtype != q.dtype or do.device != q.device:
+        raise ValueError(f"do must be {tuple(q.shape)} of {q.dtype} on {q.device}")
+    g = AttentionGrads(do.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), *do.stride()[:2], *dq.stride()[:2],
+                       *dk.stride()[:2], *dv.stride()[:2])
+    lib, pa = load_library(), ctypes.byref(a)
+    need = lib.eqlin_attention_backward_workspace(pa)
+    workspace = _workspace(workspace, need, q.device)
+    _check(_on(q.device, lib.eqlin_attention_backward, pa, ctypes.byref(g), _ptr(workspace), need),
+           "eqlin_attention_backward")
+    return dq, dk, dv
 
 
 STATIC_SCRATCH_BYTES = 64 << 20  # EQLIN_STATIC_SCRATCH_BYTES

@@ -1,0 +1,380 @@
+// attn_bwd.hip -- gradients of the packed attention. With P = exp(scale q k^T - lse) recomputed from the
+// forward's lse, dP = dO V^T and delta = sum over d of dO O:
+//
+//   dS = P (dP - delta);  dV = P^T dO;  dK = scale dS^T Q;  dQ = scale dS K
+//
+// Two passes, each owning its outputs: one over key tiles (dK, dV: every row that sees them, all heads of the
+// group, in order) and one over row tiles (dQ). S and dP are formed in both, 7 products instead of 5, and
+// nothing is added by atomics: the same bits every time, and no fp32 image of dQ in memory.
+#include "attn.h"
+#include "attn_tile.h"
+
+namespace eqlin {
+
+namespace {
+
+// delta[token][head] = sum over d of dO O: 16 lanes a row.
+template <class E>
+__global__ void __launch_bounds__(256) k_attn_delta(const AttnParams p) {
+    typedef Elem<E> EL;
+    typedef typename EL::T T;
+    const int64_t rows = p.total_q * p.Hq;
+    const int l = threadIdx.x & 15;
+    for (int64_t at0 = (int64_t)blockIdx.x * 16; at0 < rows; at0 += (int64_t)gridDim.x * 16) {
+    const int64_t at = at0 + (threadIdx.x >> 4);
+    float sum = 0.0f;
+    if (at < rows) {
+        const int64_t tok = at / p.Hq;
+        const int hq = (int)(at - tok * p.Hq);
+        const T *o = (const T *)p.o + tok * p.ot + hq * p.oh, *g = (const T *)p.dout + tok * p.dot + hq * p.doh;
+        for (int e = l * EL::V; e < p.D; e += 16 * EL::V) {
+            float a[EL::V], b[EL::V];
+            EL::unpack(*(const uint4 *)(o + e), a);
+            EL::unpack(*(const uint4 *)(g + e), b);
+#pragma unroll
+            for (int j = 0; j < EL::V; ++j) sum = fmaf(a[j], b[j], sum);
+        }
+    }
+#pragma unroll
+    for (int m = 8; m >= 1; m >>= 1) sum += __shfl_xor(sum, m);
+    if (at < rows && l == 0) p.ws[at] = sum;
+    }
+}
+
+// ---- dQ: as the forward, 32 rows a wave (columns), key tiles through LDS ----
+
+template <class E, int DP, int NKB, bool MASK>
+__device__ __forceinline__ void dq_block(f32x16 *dq, const uint4 *qf, const uint4 *gf, const char *kt, const char *vt, float c,
+                                         float lse2, float delta, int lim, int lane) {
+    typedef Tile<E, DP> TL;
+    const int h = lane >> 5, l32 = lane & 31;
+#pragma unroll
+    for (int kb = 0; kb < NKB; ++kb) {
+        f32x16 s, dp;
+#pragma unroll
+        for (int v = 0; v < 16; ++v) s[v] = 0.0f, dp[v] = 0.0f;
+#pragma unroll
+        for (int t = 0; t < TL::kSteps; ++t) {
+            s = mma_frag<E>(TL::row_frag(kt, 32 * kb + l32, t, h), qf[t], s);
+            dp = mma_frag<E>(TL::row_frag(vt, 32 * kb + l32, t, h), gf[t], dp);
+        }
+#pragma unroll
+        for (int v = 0; v < 16; ++v) {
+            const float pr = __builtin_amdgcn_exp2f(fmaf(s[v], c, -lse2));
+            s[v] = pr * (dp[v] - delta);
+            if constexpr (MASK) s[v] = 32 * kb + d_row(v, h) <= lim ? s[v] : 0.0f;
+        }
+        WFrags<E> w;
+        w.set(s);
+#pragma unroll
+        for (int f = 0; f < WFrags<E>::NF; ++f)
+#pragma unroll
+            for (int db = 0; db < DP / 32; ++db)
+                dq[db] = mma_frag<E>(TL::col_frag(kt, 32 * kb, f, db, lane), w.f[f], dq[db]);
+    }
+}
+
+template <class E, int DP>
+__global__ void __launch_bounds__(256, __is_same(E, F32) ? 1 : 2) k_attn_dq(const AttnParams p) {
+    typedef TileCfg<E, DP> C;
+    typedef Tile<E, DP> TL;
+    typedef typename ElemOf<E>::type T;
+    extern __shared__ __align__(16) char lds[];
+    const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), h = lane >> 5;
+    const int hk = blockIdx.y;
+    const int64_t slot = blockIdx.x;
+    const int i = seq_of_slot(p.cu_q, p.B, p.total_q, p.grp, C::BM, slot);
+    const Seq sq = seq_at(p, i);
+    const int64_t row_end = (int64_t)sq.lq * p.grp;
+    const int64_t row_wg = (slot - slot_start(p.cu_q, i, p.total_q, p.grp, C::BM)) * C::BM;
+    if (row_wg < 0 || row_wg >= row_end) return;
+    const int off = sq.lk - sq.lq;
+    const int64_t row = row_wg + wave * 32 + (lane & 31);
+    const bool live = row < row_end;
+    const int tok = live ? (int)((uint32_t)row / (uint32_t)p.grp) : 0;
+    const int hq = hk * p.grp + (live ? (int)((uint32_t)row - (uint32_t)tok * (uint32_t)p.grp) : 0);
+    const int64_t at = (sq.q0 + tok) * p.Hq + hq;
+    uint4 qf[TL::kSteps], gf[TL::kSteps];
+    {
+        const T *q = (const T *)p.q + (sq.q0 + tok) * p.qt + hq * p.qh;
+        const T *g = (const T *)p.dout + (sq.q0 + tok) * p.dot + hq * p.doh;
+#pragma unroll
+        for (int t = 0; t < TL::kSteps; ++t) {
+            const int col = (2 * t + h) * (16 / (int)sizeof(T));
+            const bool in = live && col < p.D;
+            qf[t] = in ? *(const uint4 *)(q + col) : make_uint4(0, 0, 0, 0);
+            gf[t] = in ? *(const uint4 *)(g + col) : make_uint4(0, 0, 0, 0);
+        }
+    }
+    const float lse2 = live ? p.lse[at] * kLog2e : INFINITY, delta = live ? p.ws[at] : 0.0f;
+    int last = live ? (p.causal ? min(tok + off, sq.lk - 1) : sq.lk - 1) : -1;
+    const int64_t row_last = (row_wg + C::BM < row_end ? row_wg + C::BM : row_end) - 1;
+    const int k_end = p.causal ? min((int)((uint32_t)row_last / (uint32_t)p.grp) + off + 1, sq.lk) : sq.lk;
+    int wave_min = live ? last : 0x7fffffff, wave_max = last;
+#pragma unroll
+    for (int x = 16; x >= 1; x >>= 1) {
+        wave_min = min(wave_min, __shfl_xor(wave_min, x));
+        wave_max = max(wave_max, __shfl_xor(wave_max, x));
+    }
+    wave_min = uniform(wave_min);
+    wave_max = uniform(wave_max);
+    f32x16 dq[DP / 32];
+#pragma unroll
+    for (int db = 0; db < DP / 32; ++db)
+#pragma unroll
+        for (int v = 0; v < 16; ++v) dq[db][v] = 0.0f;
+    const float c = p.scale * kLog2e;
+    const T *kg = (const T *)p.k + sq.k0 * p.kt + hk * p.kh;
+    const T *vg = (const T *)p.v + sq.k0 * p.vt + hk * p.vh;
+    Stage<E, DP, C::kStage, 256> sk, sv;
+    if (k_end > 0) {
+        sk.load(kg, p.kt, sq.lk, p.D, tid);
+        sv.load(vg, p.vt, sq.lk, p.D, tid);
+        sk.store(lds, tid);
+        sv.store(lds + C::kTileBytes, tid);
+    }
+    int buf = 0;
+    for (int k0 = 0; k0 < k_end; k0 += C::BN) {
+        __syncthreads();
+        const bool more = k0 + C::BN < k_end;
+        if (more) {
+            sk.load(kg + (int64_t)(k0 + C::BN) * p.kt, p.kt, sq.lk - k0 - C::BN, p.D, tid);
+            sv.load(vg + (int64_t)(k0 + C::BN) * p.vt, p.vt, sq.lk - k0 - C::BN, p.D, tid);
+        }
+        const char *kt = lds + buf * 2 * C::kTileBytes, *vt = kt + C::kTileBytes;
+        if (k0 <= wave_max) {
+            if (k0 + C::BN - 1 <= wave_min) dq_block<E, DP, C::NKB, false>(dq, qf, gf, kt, vt, c, lse2, delta, 0, lane);
+            else dq_block<E, DP, C::NKB, true>(dq, qf, gf, kt, vt, c, lse2, delta, last - k0, lane);
+        }
+        if (more) {
+            char *nt = lds + (buf ^ 1) * 2 * C::kTileBytes;
+            sk.store(nt, tid);
+            sv.store(nt + C::kTileBytes, tid);
+        }
+        buf ^= 1;
+    }
+    if (live) store_column<E, DP>(dq, p.scale, (T *)p.dq + (sq.q0 + tok) * p.dqt + hq * p.dqh, p.D, h);
+}
+
+// ---- dK, dV: 32 keys a wave (columns), tiles of packed rows (q and dO) through LDS ----
+
+// A tile of packed rows of q or dO.
+template <class E, int DP, int N>
+struct RowStage {
+    typedef Tile<E, DP> TL;
+    typedef typename ElemOf<E>::type T;
+    uint4 r[N];
+    __device__ __forceinline__ void load(const T *base, int64_t ts, int64_t hs, int64_t row0, int64_t row_end, int grp, int D,
+                                         int tid) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            const int id = tid + j * 256, c = id % TL::kChunks, col = c * (16 / (int)sizeof(T));
+            const int64_t row = row0 + id / TL::kChunks;
+            const int tok = (int)((uint32_t)row / (uint32_t)grp), hh = (int)((uint32_t)row - (uint32_t)tok * (uint32_t)grp);
+            r[j] = row < row_end && col < D ? *(const uint4 *)(base + tok * ts + hh * hs + col) : make_uint4(0, 0, 0, 0);
+        }
+    }
+    __device__ __forceinline__ void store(char *tile, int tid) const {
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            const int id = tid + j * 256;
+            *(uint4 *)(tile + TL::at(id / TL::kChunks, id % TL::kChunks)) = r[j];
+        }
+    }
+};
+
+template <class E, int DP, int NRB, bool MASK>
+__device__ __forceinline__ void dkv_block(f32x16 *dk, f32x16 *dv, const uint4 *kf, const uint4 *vf, const char *qt,
+                                          const char *gt, const float *lse2, const float *delta, const int *last, float c,
+                                          int key, int lane) {
+    typedef Tile<E, DP> TL;
+    const int h = lane >> 5, l32 = lane & 31;
+#pragma unroll
+    for (int rb = 0; rb < NRB; ++rb) {
+        f32x16 s, dp;
+#pragma unroll
+        for (int v = 0; v < 16; ++v) s[v] = 0.0f, dp[v] = 0.0f;
+#pragma unroll
+        for (int t = 0; t < TL::kSteps; ++t) {
+            s = mma_frag<E>(TL::row_frag(qt, 32 * rb + l32, t, h), kf[t], s);
+            dp = mma_frag<E>(TL::row_frag(gt, 32 * rb + l32, t, h), vf[t], dp);
+        }
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            const int row = 32 * rb + 8 * g + 4 * h;
+            const float4 ls = *(const float4 *)(lse2 + row), de = *(const float4 *)(delta + row);
+            const float l4[4] = {ls.x, ls.y, ls.z, ls.w}, d4[4] = {de.x, de.y, de.z, de.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int v = 4 * g + j;
+                float pr = __builtin_amdgcn_exp2f(fmaf(s[v], c, -l4[j]));
+                float ds = pr * (dp[v] - d4[j]);
+                if constexpr (MASK) {
+                    const bool see = key <= last[row + j];
+                    pr = see ? pr : 0.0f;
+                    ds = see ? ds : 0.0f;
+                }
+                s[v] = pr;
+                dp[v] = ds;
+            }
+        }
+        WFrags<E> w;
+        w.set(s);
+#pragma unroll
+        for (int f = 0; f < WFrags<E>::NF; ++f)
+#pragma unroll
+            for (int db = 0; db < DP / 32; ++db)
+                dv[db] = mma_frag<E>(TL::col_frag(gt, 32 * rb, f, db, lane), w.f[f], dv[db]);
+        w.set(dp);
+#pragma unroll
+        for (int f = 0; f < WFrags<E>::NF; ++f)
+#pragma unroll
+            for (int db = 0; db < DP / 32; ++db)
+                dk[db] = mma_frag<E>(TL::col_frag(qt, 32 * rb, f, db, lane), w.f[f], dk[db]);
+    }
+}
+
+template <class E, int DP>
+struct DkvCfg {
+    typedef Tile<E, DP> TL;
+    static constexpr int BK = 128;  // keys of a workgroup
+    static constexpr int NRB = __is_same(E, F32) ? 1 : 2;
+    static constexpr int BR = 32 * NRB;  // packed rows of a tile
+    static constexpr int kTileBytes = BR * TL::kRow;
+    static constexpr int kStage = kTileBytes / 16 / 256;
+    static constexpr int kBuf = 2 * kTileBytes + 3 * BR * 4;  // q, dO, lse, delta, last key
+    static constexpr int kLds = 2 * kBuf;
+};
+
+template <class E, int DP>
+__global__ void __launch_bounds__(256, __is_same(E, F32) || DP > 64 ? 1 : 2) k_attn_dkv(const AttnParams p) {
+    typedef DkvCfg<E, DP> C;
+    typedef Tile<E, DP> TL;
+    typedef typename ElemOf<E>::type T;
+    extern __shared__ __align__(16) char lds[];
+    const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), h = lane >> 5;
+    const int hk = blockIdx.y;
+    const int64_t slot = blockIdx.x;
+    const int i = seq_of_slot(p.cu_k, p.B, p.total_k, 1, C::BK, slot);
+    const Seq sq = seq_at(p, i);
+    const int64_t key_wg = (slot - slot_start(p.cu_k, i, p.total_k, 1, C::BK)) * C::BK;
+    if (key_wg < 0 || key_wg >= sq.lk_slot) return;
+    const int off = sq.lk - sq.lq;
+    const int key = (int)key_wg + wave * 32 + (lane & 31);
+    const bool live = key < sq.lk;
+    uint4 kf[TL::kSteps], vf[TL::kSteps];
+    {
+        const T *k = (const T *)p.k + (sq.k0 + key) * p.kt + hk * p.kh, *v = (const T *)p.v + (sq.k0 + key) * p.vt + hk * p.vh;
+#pragma unroll
+        for (int t = 0; t < TL::kSteps; ++t) {
+            const int col = (2 * t + h) * (16 / (int)sizeof(T));
+            const bool in = live && col < p.D;
+            kf[t] = in ? *(const uint4 *)(k + col) : make_uint4(0, 0, 0, 0);
+            vf[t] = in ? *(const uint4 *)(v + col) : make_uint4(0, 0, 0, 0);
+        }
+    }
+    f32x16 dk[DP / 32], dv[DP / 32];
+#pragma unroll
+    for (int db = 0; db < DP / 32; ++db)
+#pragma unroll
+        for (int v = 0; v < 16; ++v) dk[db][v] = 0.0f, dv[db][v] = 0.0f;
+    const float c = p.scale * kLog2e;
+    const int64_t row_end = key_wg < sq.lk ? (int64_t)sq.lq * p.grp : 0;
+    // causal: the first token that sees the workgroup's first key
+    int64_t row_beg = p.causal && key_wg > off ? (key_wg - off) * p.grp : 0;
+    row_beg -= row_beg % C::BR;
+    const T *qg = (const T *)p.q + sq.q0 * p.qt + (int64_t)hk * p.grp * p.qh;
+    const T *gg = (const T *)p.dout + sq.q0 * p.dot + (int64_t)hk * p.grp * p.doh;
+    const float *lse = p.lse + sq.q0 * p.Hq + hk * p.grp, *del = p.ws + sq.q0 * p.Hq + hk * p.grp;
+    RowStage<E, DP, C::kStage> sqs, sgs;
+    float st_lse = INFINITY, st_del = 0.0f;
+    int st_last = -1;
+    auto load = [&](int64_t r0) {
+        sqs.load(qg, p.qt, p.qh, r0, row_end, p.grp, p.D, tid);
+        sgs.load(gg, p.dot, p.doh, r0, row_end, p.grp, p.D, tid);
+        if (tid < C::BR) {
+            const int64_t row = r0 + tid;
+            const int tok = (int)((uint32_t)row / (uint32_t)p.grp), hh = (int)((uint32_t)row - (uint32_t)tok * (uint32_t)p.grp);
+            const bool in = row < row_end;
+            st_lse = in ? lse[(int64_t)tok * p.Hq + hh] * kLog2e : INFINITY;
+            st_del = in ? del[(int64_t)tok * p.Hq + hh] : 0.0f;
+            st_last = in ? (p.causal ? min(tok + off, sq.lk - 1) : sq.lk - 1) : -1;
+        }
+    };
+    auto store = [&](char *b) {
+        sqs.store(b, tid);
+        sgs.store(b + C::kTileBytes, tid);
+        if (tid < C::BR) {
+            float *f = (float *)(b + 2 * C::kTileBytes);
+            f[tid] = st_lse;
+            f[C::BR + tid] = st_del;
+            ((int *)f)[2 * C::BR + tid] = st_last;
+        }
+    };
+    if (row_beg < row_end) {
+        load(row_beg);
+        store(lds);
+    }
+    int buf = 0;
+    const int wave_last = (int)key_wg + wave * 32 + 31;  // the wave's last key
+    for (int64_t r0 = row_beg; r0 < row_end; r0 += C::BR) {
+        __syncthreads();
+        const bool more = r0 + C::BR < row_end;
+        if (more) load(r0 + C::BR);
+        const char *b = lds + buf * C::kBuf;
+        const float *f = (const float *)(b + 2 * C::kTileBytes);
+        // rows see a prefix of the keys, longer for later rows: the tile's first row decides
+        const bool whole = uniform(((const int *)f)[2 * C::BR]) >= wave_last && r0 + C::BR <= row_end;
+        if (whole)
+            dkv_block<E, DP, C::NRB, false>(dk, dv, kf, vf, b, b + C::kTileBytes, f, f + C::BR, (const int *)f + 2 * C::BR, c, key, lane);
+        else
+            dkv_block<E, DP, C::NRB, true>(dk, dv, kf, vf, b, b + C::kTileBytes, f, f + C::BR, (const int *)f + 2 * C::BR, c, key, lane);
+        if (more) store(lds + (buf ^ 1) * C::kBuf);
+        buf ^= 1;
+    }
+    if (key < sq.lk_slot) {  // keys beyond the sequence's length in its slot get zeros
+        store_column<E, DP>(dk, p.scale, (T *)p.dk + (sq.k0 + key) * p.dkt + hk * p.dkh, p.D, h);
+        store_column<E, DP>(dv, 1.0f, (T *)p.dv + (sq.k0 + key) * p.dvt + hk * p.dvh, p.D, h);
+    }
+}
+
+template <class K>
+hipError_t set_lds(K kernel, int bytes) {
+    return bytes > 64 * 1024 ? hipFuncSetAttribute((const void *)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes)
+                             : hipSuccess;
+}
+
+template <class E, int DP>
+hipError_t run_bwd(const AttnParams &p, hipStream_t s) {
+    typedef TileCfg<E, DP> CQ;
+    typedef DkvCfg<E, DP> CK;
+    hipError_t e = set_lds(k_attn_dq<E, DP>, CQ::kLds);
+    if (e == hipSuccess) e = set_lds(k_attn_dkv<E, DP>, CK::kLds);
+    if (e != hipSuccess) return e;
+    if (p.total_q > 0) {
+        hipLaunchKernelGGL((k_attn_delta<E>), dim3((unsigned)std::min<int64_t>((p.total_q * p.Hq + 15) / 16, 1 << 20)), dim3(256), 0, s, p);
+        hipLaunchKernelGGL((k_attn_dq<E, DP>), dim3((unsigned)(p.total_q * p.grp / CQ::BM + p.B), p.Hkv), dim3(256), CQ::kLds, s, p);
+    }
+    if (p.total_k > 0)
+        hipLaunchKernelGGL((k_attn_dkv<E, DP>), dim3((unsigned)(p.total_k / CK::BK + p.B), p.Hkv), dim3(256), CK::kLds, s, p);
+    return hipGetLastError();
+}
+
+template <class E>
+hipError_t run_bwd_e(const AttnParams &p, hipStream_t s) {
+    if (p.D <= 32) return run_bwd<E, 32>(p, s);
+    if (p.D <= 64) return run_bwd<E, 64>(p, s);
+    return run_bwd<E, 128>(p, s);
+}
+
+}  // namespace
+
+size_t attention_backward_workspace_bytes(const AttnParams &p) { return (size_t)p.total_q * p.Hq * sizeof(float); }
+
+hipError_t launch_attention_backward(const AttnParams &p, eqlin_dtype_t dtype, hipStream_t s) {
+    if (dtype == EQLIN_F32) return run_bwd_e<F32>(p, s);
+    if (dtype == EQLIN_F16) return run_bwd_e<F16>(p, s);
+    return run_bwd_e<BF16>(p, s);
+}
+
+}  // namespace eqlin

@@ -1,0 +1,266 @@
+// attn_fwd.hip -- attention over packed sequences: o = softmax(scale q k^T) v, one pass over the keys with
+// the running maximum and sum.
+#include "attn.h"
+#include "attn_tile.h"
+
+namespace eqlin {
+
+namespace {
+
+// ---- the tile kernel: 4 waves, each 32 packed rows (the columns of S^T), all over the same key tiles ----
+
+// Running softmax state of a lane's column and its O^T accumulators.
+template <class E, int DP>
+struct FwdState {
+    f32x16 o[DP / 32];
+    float m, l;  // m: running maximum in log2 units (scaled); l: this lane's half of the sum
+};
+
+// One 32 x 32 NKB block of keys against a wave's 32 columns. lim: last key (within the tile) the column may
+// see; MASK: some key of the tile is beyond some column's lim.
+template <class E, int DP, int NKB, bool MASK>
+__device__ __forceinline__ void fwd_block(FwdState<E, DP> &st, const uint4 *qf, const char *kt, const char *vt, float c,
+                                          int lim, int lane) {
+    typedef Tile<E, DP> TL;
+    const int h = lane >> 5, l32 = lane & 31;
+    f32x16 s[NKB];
+#pragma unroll
+    for (int kb = 0; kb < NKB; ++kb) {
+#pragma unroll
+        for (int v = 0; v < 16; ++v) s[kb][v] = 0.0f;
+#pragma unroll
+        for (int t = 0; t < TL::kSteps; ++t) s[kb] = mma_frag<E>(TL::row_frag(kt, 32 * kb + l32, t, h), qf[t], s[kb]);
+    }
+    float mx = -INFINITY;
+#pragma unroll
+    for (int kb = 0; kb < NKB; ++kb)
+#pragma unroll
+        for (int v = 0; v < 16; ++v) {
+            if constexpr (MASK) s[kb][v] = 32 * kb + d_row(v, h) <= lim ? s[kb][v] : -INFINITY;
+            mx = fmaxf(mx, s[kb][v]);
+        }
+    mx = half_max(mx) * c;
+    // The maximum is only raised when it grew by more than 8 (in log2 units): a stale one keeps every
+    // p <= 2^8, exact in the sums' fp32 and in range of fp16, and saves the pass over the accumulators.
+    if (__any(mx > st.m + 8.0f)) {
+        const float mn = fmaxf(st.m, mx);
+        const float a = mn == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(st.m - mn);
+        st.m = mn;
+        st.l *= a;
+#pragma unroll
+        for (int db = 0; db < DP / 32; ++db)
+#pragma unroll
+            for (int v = 0; v < 16; ++v) st.o[db][v] *= a;
+    }
+    const float mm = st.m == -INFINITY ? 0.0f : st.m;
+    float sum = 0.0f;
+#pragma unroll
+    for (int kb = 0; kb < NKB; ++kb) {
+#pragma unroll
+        for (int v = 0; v < 16; ++v) {
+            s[kb][v] = __builtin_amdgcn_exp2f(fmaf(s[kb][v], c, -mm));
+            sum += s[kb][v];
+        }
+        WFrags<E> w;
+        w.set(s[kb]);
+#pragma unroll
+        for (int f = 0; f < WFrags<E>::NF; ++f)
+#pragma unroll
+            for (int db = 0; db < DP / 32; ++db)
+                st.o[db] = mma_frag<E>(TL::col_frag(vt, 32 * kb, f, db, lane), w.f[f], st.o[db]);
+    }
+    st.l += sum;
+}
+
+template <class E, int DP>
+__global__ void __launch_bounds__(256, __is_same(E, F32) ? 1 : 2) k_attn_fwd(const AttnParams p) {
+    typedef TileCfg<E, DP> C;
+    typedef Tile<E, DP> TL;
+    typedef typename ElemOf<E>::type T;
+    extern __shared__ __align__(16) char lds[];
+    const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), h = lane >> 5;
+    const int hk = blockIdx.y;
+    const int64_t slot = blockIdx.x;
+    const int i = seq_of_slot(p.cu_q, p.B, p.total_q, p.grp, C::BM, slot);
+    const Seq sq = seq_at(p, i);
+    const int64_t row_end = (int64_t)sq.lq * p.grp;
+    const int64_t row_wg = (slot - slot_start(p.cu_q, i, p.total_q, p.grp, C::BM)) * C::BM;
+    if (row_wg < 0 || row_wg >= row_end) return;
+    const int off = sq.lk - sq.lq;  // causal: token t sees keys up to t + off
+
+    // this lane's row
+    const int64_t row = row_wg + wave * 32 + (lane & 31);
+    const bool live = row < row_end;
+    const int tok = live ? (int)((uint32_t)row / (uint32_t)p.grp) : 0;
+    const int hq = hk * p.grp + (live ? (int)((uint32_t)row - (uint32_t)tok * (uint32_t)p.grp) : 0);
+    uint4 qf[TL::kSteps];
+    {
+        const T *q = (const T *)p.q + (sq.q0 + tok) * p.qt + hq * p.qh;
+#pragma unroll
+        for (int t = 0; t < TL::kSteps; ++t) {
+            const int col = (2 * t + h) * (16 / (int)sizeof(T));
+            qf[t] = live && col < p.D ? *(const uint4 *)(q + col) : make_uint4(0, 0, 0, 0);
+        }
+    }
+    int last = live ? (p.causal ? min(tok + off, sq.lk - 1) : sq.lk - 1) : -1;  // last key of this row
+    // key range of the workgroup (all rows) and of this split
+    const int64_t row_last = (row_wg + C::BM < row_end ? row_wg + C::BM : row_end) - 1;
+    int k_end = p.causal ? min((int)((uint32_t)row_last / (uint32_t)p.grp) + off + 1, sq.lk) : sq.lk;
+    int k_beg = 0;
+    if (p.nsplit > 1) {
+        const int tiles = (k_end + C::BN - 1) / C::BN, z = blockIdx.z;
+        k_beg = (int)((int64_t)tiles * z / p.nsplit) * C::BN;
+        k_end = min(k_end, (int)((int64_t)tiles * (z + 1) / p.nsplit) * C::BN);
+    }
+    // smallest `last` of the wave: tiles wholly below it need no mask
+    int wave_min = live ? last : 0x7fffffff, wave_max = last;
+#pragma unroll
+    for (int x = 16; x >= 1; x >>= 1) {
+        wave_min = min(wave_min, __shfl_xor(wave_min, x));
+        wave_max = max(wave_max, __shfl_xor(wave_max, x));
+    }
+    wave_min = uniform(wave_min);
+    wave_max = uniform(wave_max);
+
+    FwdState<E, DP> st;
+#pragma unroll
+    for (int db = 0; db < DP / 32; ++db)
+#pragma unroll
+        for (int v = 0; v < 16; ++v) st.o[db][v] = 0.0f;
+    st.m = -INFINITY;
+    st.l = 0.0f;
+    const float c = p.scale * kLog2e;
+
+    const T *kg = (const T *)p.k + sq.k0 * p.kt + hk * p.kh;
+    const T *vg = (const T *)p.v + sq.k0 * p.vt + hk * p.vh;
+    Stage<E, DP, C::kStage, 256> sk, sv;
+    if (k_beg < k_end) {
+        sk.load(kg + (int64_t)k_beg * p.kt, p.kt, sq.lk - k_beg, p.D, tid);
+        sv.load(vg + (int64_t)k_beg * p.vt, p.vt, sq.lk - k_beg, p.D, tid);
+        sk.store(lds, tid);
+        sv.store(lds + C::kTileBytes, tid);
+    }
+    int buf = 0;
+    for (int k0 = k_beg; k0 < k_end; k0 += C::BN) {
+        __syncthreads();  // this tile is in LDS; the other buffer's readers are done
+        const bool more = k0 + C::BN < k_end;
+        if (more) {
+            sk.load(kg + (int64_t)(k0 + C::BN) * p.kt, p.kt, sq.lk - k0 - C::BN, p.D, tid);
+            sv.load(vg + (int64_t)(k0 + C::BN) * p.vt, p.vt, sq.lk - k0 - C::BN, p.D, tid);
+        }
+        const char *kt = lds + buf * 2 * C::kTileBytes, *vt = kt + C::kTileBytes;
+        if (k0 <= wave_max) {
+            if (k0 + C::BN - 1 <= wave_min) fwd_block<E, DP, C::NKB, false>(st, qf, kt, vt, c, 0, lane);
+            else fwd_block<E, DP, C::NKB, true>(st, qf, kt, vt, c, last - k0, lane);
+        }
+        if (more) {
+            char *nt = lds + (buf ^ 1) * 2 * C::kTileBytes;
+            sk.store(nt, tid);
+            sv.store(nt + C::kTileBytes, tid);
+        }
+        buf ^= 1;
+    }
+
+    const float l = half_sum(st.l);
+    const bool empty = last < 0;
+    const int64_t at = (sq.q0 + tok) * p.Hq + hq;
+    if (!live) return;
+    if (p.nsplit > 1) {  // partial results: unnormalised o, then (m, l), for k_attn_join
+        const int64_t rows = p.total_q * p.Hq;
+        store_column<F32, DP>(st.o, 1.0f, p.ws + ((int64_t)blockIdx.z * rows + at) * p.D, p.D, h);
+        if (h == 0) {
+            float *ml = p.ws + p.nsplit * rows * p.D + ((int64_t)blockIdx.z * rows + at) * 2;
+            ml[0] = st.m;
+            ml[1] = empty ? -1.0f : l;  // negative: a row that sees no key
+        }
+        return;
+    }
+    store_column<E, DP>(st.o, empty ? 0.0f : 1.0f / l, (T *)p.o + (sq.q0 + tok) * p.ot + hq * p.oh, p.D, h);
+    if (p.lse && h == 0) p.lse[at] = empty ? -INFINITY : st.m * kLn2 + logf(l);
+}
+
+// ---- joining the key ranges of a row: one wave a row ----
+
+template <class E>
+__global__ void __launch_bounds__(256) k_attn_join(const AttnParams p) {
+    typedef typename ElemOf<E>::type T;
+    const int lane = threadIdx.x & 63;
+    const int64_t rows = p.total_q * p.Hq;
+    for (int64_t at = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); at < rows; at += (int64_t)gridDim.x * 4) {
+    const float *ml = p.ws + p.nsplit * rows * p.D;
+    float m = -INFINITY;
+    for (int z = 0; z < p.nsplit; ++z) m = fmaxf(m, ml[(z * rows + at) * 2]);
+    const float mm = m == -INFINITY ? 0.0f : m;
+    float l = 0.0f, o0 = 0.0f, o1 = 0.0f;
+    for (int z = 0; z < p.nsplit; ++z) {
+        const float w = __builtin_amdgcn_exp2f(ml[(z * rows + at) * 2] - mm);
+        const float *o = p.ws + (z * rows + at) * p.D;
+        l = fmaf(w, ml[(z * rows + at) * 2 + 1], l);
+        if (lane < p.D) o0 = fmaf(w, o[lane], o0);
+        if (lane + 64 < p.D) o1 = fmaf(w, o[lane + 64], o1);
+    }
+    const int64_t tok = at / p.Hq;
+    const int hq = (int)(at - tok * p.Hq);
+    T *dst = (T *)p.o + tok * p.ot + hq * p.oh;
+    const bool empty = ml[at * 2 + 1] < 0.0f;  // the same in every range
+    const float inv = empty ? 0.0f : 1.0f / l;
+    if constexpr (__is_same(E, F32)) {
+        if (lane < p.D) dst[lane] = o0 * inv;
+        if (lane + 64 < p.D) dst[lane + 64] = o1 * inv;
+    } else {
+        if (lane < p.D) dst[lane] = pack1<E>(o0 * inv);
+        if (lane + 64 < p.D) dst[lane + 64] = pack1<E>(o1 * inv);
+    }
+    if (p.lse && lane == 0) p.lse[at] = empty ? -INFINITY : m * kLn2 + logf(l);
+    }
+}
+
+template <class E, int DP>
+hipError_t run_fwd(const AttnParams &p, hipStream_t s) {
+    typedef TileCfg<E, DP> C;
+    const int64_t slots = p.total_q * p.grp / C::BM + p.B;
+    if (C::kLds > 64 * 1024) {
+        hipError_t e = hipFuncSetAttribute((const void *)k_attn_fwd<E, DP>, hipFuncAttributeMaxDynamicSharedMemorySize, C::kLds);
+        if (e != hipSuccess) return e;
+    }
+    hipLaunchKernelGGL((k_attn_fwd<E, DP>), dim3((unsigned)slots, p.Hkv, p.nsplit), dim3(256), C::kLds, s, p);
+    if (p.nsplit > 1) {
+        const int64_t rows = p.total_q * p.Hq;
+        hipLaunchKernelGGL((k_attn_join<E>), dim3((unsigned)std::min<int64_t>((rows + 3) / 4, 1 << 20)), dim3(256), 0, s, p);
+    }
+    return hipGetLastError();
+}
+
+template <class E>
+hipError_t run_fwd_e(const AttnParams &p, hipStream_t s) {
+    if (p.D <= 32) return run_fwd<E, 32>(p, s);
+    if (p.D <= 64) return run_fwd<E, 64>(p, s);
+    return run_fwd<E, 128>(p, s);
+}
+
+// Key ranges a launch is split into: enough workgroups for two a compute unit where the rows alone do not
+// give them, none shorter than 256 keys on average.
+int pick_nsplit(const AttnParams &p) {
+    const int64_t wgs = (p.total_q * p.grp / 128 + p.B) * p.Hkv;
+    const int64_t want = 2 * (int64_t)device_num_cus();
+    const int64_t most = std::max<int64_t>(1, p.total_k / p.B / 256);
+    return (int)std::min<int64_t>(std::max<int64_t>(1, want / std::max<int64_t>(1, wgs)), std::min<int64_t>(most, 64));
+}
+
+}  // namespace
+
+size_t attention_workspace_bytes(const AttnParams &p, eqlin_dtype_t) {
+    if (p.total_q <= 0 || p.B <= 0) return 0;
+    const int n = pick_nsplit(p);
+    return n <= 1 ? 0 : (size_t)n * p.total_q * p.Hq * (p.D + 2) * sizeof(float);
+}
+
+hipError_t launch_attention(const AttnParams &p0, eqlin_dtype_t dtype, hipStream_t s) {
+    AttnParams p = p0;
+    p.nsplit = pick_nsplit(p);
+    if (dtype == EQLIN_F32) return run_fwd_e<F32>(p, s);
+    if (dtype == EQLIN_F16) return run_fwd_e<F16>(p, s);
+    return run_fwd_e<BF16>(p, s);
+}
+
+}  // namespace eqlin

@@ -185,6 +185,17 @@ void *g_scratch_ptr[kMaxDevices] = {};
 
 }  // namespace
 
+namespace eqlin {
+eqlin_status_t api_fail(eqlin_status_t s, const char *fmt, ...) {
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(g_err, sizeof(g_err), fmt, ap);
+    va_end(ap);
+    return s;
+}
+void api_clear() { g_err[0] = 0; }
+}  // namespace eqlin
+
 static __device__ __align__(256) unsigned char scratch[EQLIN_STATIC_SCRATCH_BYTES];
 
 // Device address of `scratch` on device `dev`, which must be the current device (looked up on the

@@ -5,6 +5,7 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <algorithm>
 #include <vector>
 
 #include "../../include/eqlin.h"
@@ -139,6 +140,73 @@ hipError_t launch_export_frag(const void *frag, bool f16, bool d4, int G, int C_
                               int frag_kind, float *out, hipStream_t s);
 hipError_t launch_export_plain_f32(const float *planes, bool d4, int G, int C_out, int C_in, float *out,
                                    hipStream_t s);
+
+// ---- eqlin_api.cpp ----
+// Records the calling thread's message and returns s (the C entry points' error path).
+eqlin_status_t api_fail(eqlin_status_t s, const char *fmt, ...);
+void api_clear();
+
+// ---- norm.hip ----
+// The root-mean-square norm over rows of C * G values; r, gamma, sum, rstd may be null. q (e4m3) and
+// scale instead of y for the 8-bit output.
+struct NormParams {
+    const void *x, *r, *gamma;
+    void *sum, *y;
+    uint8_t *q;
+    float *scale, *rstd;
+    int64_t N;
+    int C, lg;  // G = 1 << lg
+    float eps;
+};
+hipError_t launch_rmsnorm(const NormParams &p, eqlin_dtype_t dtype, hipStream_t s);
+struct NormGradParams {
+    const void *s, *gamma, *dy, *ds;
+    const float *rstd;
+    void *dx;
+    float *dgamma, *part;
+    int64_t N;
+    int C, lg;
+};
+size_t rmsnorm_backward_workspace_bytes(int64_t N, int C, int G);
+hipError_t launch_rmsnorm_backward(const NormGradParams &p, eqlin_dtype_t dtype, hipStream_t s);
+
+// ---- rotary.hip ----
+constexpr int kRotaryMaxPairs = 256, kRotaryMaxAxes = 4;
+struct RotaryParams {
+    const void *x;
+    void *y;
+    const int *pos;                 // [N][axes]
+    int64_t N, xt, xh, yt, yh;      // token and head strides in elements
+    int H, dc, lg, axes, P;         // P pairs: channels j and j + P
+    int end[kRotaryMaxAxes];        // axis a turns the pairs below end[a] that no earlier axis has
+    bool d4, inverse;
+    double freq[kRotaryMaxPairs];   // turns per position of each pair
+};
+hipError_t launch_rotary(const RotaryParams &p, eqlin_dtype_t dtype, hipStream_t s);
+
+// ---- attn_fwd.hip, attn_bwd.hip ----
+struct AttnParams {
+    const void *q, *k, *v;
+    void *o;
+    float *lse;
+    int64_t qt, qh, kt, kh, vt, vh, ot, oh;  // token and head strides in elements
+    const int *cu_q, *cu_k, *len_k;
+    int64_t total_q, total_k;
+    int B, Hq, Hkv, grp, D;
+    float scale;
+    int causal;
+    // gradients
+    const void *dout;
+    void *dq, *dk, *dv;
+    int64_t dot, doh, dqt, dqh, dkt, dkh, dvt, dvh;
+    float *ws;   // workspace
+    int chunk;   // keys a workgroup of the split kernel takes (0: not split)
+    int nsplit;  // key ranges the tile kernel's rows are split into
+};
+size_t attention_workspace_bytes(const AttnParams &p, eqlin_dtype_t dtype);
+hipError_t launch_attention(const AttnParams &p, eqlin_dtype_t dtype, hipStream_t s);
+size_t attention_backward_workspace_bytes(const AttnParams &p);
+hipError_t launch_attention_backward(const AttnParams &p, eqlin_dtype_t dtype, hipStream_t s);
 
 }  // namespace eqlin
 

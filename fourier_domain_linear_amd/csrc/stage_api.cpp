@@ -1,0 +1,307 @@
+// stage_api.cpp -- the C entry points of the operators between the layers (norm, rotary positions,
+// attention): argument checks and dispatch. Nothing here computes; every step runs in the HIP kernels.
+#include <hip/hip_runtime.h>
+#include <math.h>
+
+#include "eqlin_internal.h"
+
+using eqlin::api_fail;
+
+namespace {
+
+bool aligned(const void *p, size_t a) { return ((uintptr_t)p % a) == 0; }
+bool overlap(const void *a, size_t na, const void *b, size_t nb) {
+    const char *x = (const char *)a, *y = (const char *)b;
+    return a && b && x < y + nb && y < x + na;
+}
+size_t elem_bytes(eqlin_dtype_t d) { return d == EQLIN_F32 ? 4 : 2; }
+bool valid_dtype(eqlin_dtype_t d) { return d == EQLIN_F32 || d == EQLIN_BF16 || d == EQLIN_F16; }
+int ilog2(int g) {
+    int s = 0;
+    while ((1 << s) < g) ++s;
+    return s;
+}
+
+eqlin_status_t done(hipError_t e, const char *what) {
+    return e == hipSuccess ? EQLIN_OK : api_fail(EQLIN_ERR_HIP, "%s: %s (%d)", what, hipGetErrorString(e), (int)e);
+}
+
+eqlin_status_t check_workspace(const void *ws, size_t bytes, size_t need) {
+    if (need == 0) return EQLIN_OK;
+    if (!ws || bytes < need) return api_fail(EQLIN_ERR_INVALID_ARG, "workspace of %zu bytes needed (got %zu)", need, ws ? bytes : (size_t)0);
+    if (!aligned(ws, 256)) return api_fail(EQLIN_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
+    return EQLIN_OK;
+}
+
+// shared checks of the norm's entry points
+eqlin_status_t check_norm(int64_t N, int C, int G, eqlin_dtype_t dtype) {
+    if (N < 0) return api_fail(EQLIN_ERR_INVALID_ARG, "N = %lld < 0", (long long)N);
+    if (C < 1) return api_fail(EQLIN_ERR_INVALID_ARG, "C = %d must be >= 1", C);
+    if (!(G == 1 || G == 2 || G == 4 || G == 8)) return api_fail(EQLIN_ERR_INVALID_ARG, "G = %d not in {1, 2, 4, 8}", G);
+    if (!valid_dtype(dtype)) return api_fail(EQLIN_ERR_INVALID_ARG, "bad dtype %d", (int)dtype);
+    if ((int64_t)C * G > (1 << 20)) return api_fail(EQLIN_ERR_UNSUPPORTED, "C * G = %lld beyond 2^20", (long long)C * G);
+    if (N > (INT64_C(1) << 60) / ((int64_t)C * G)) return api_fail(EQLIN_ERR_INVALID_ARG, "N = %lld overflows the index range", (long long)N);
+    return EQLIN_OK;
+}
+
+eqlin_status_t rmsnorm(const void *x, const void *residual, const void *gamma, void *sum, void *y, uint8_t *q,
+                       float *scale, float *rstd, int64_t N, int C, int G, float eps, eqlin_dtype_t dtype,
+                       eqlin_stream_t stream, bool quant, const char *what) {
+    eqlin::api_clear();
+    eqlin_status_t st = check_norm(N, C, G, dtype);
+    if (st != EQLIN_OK) return st;
+    if (!(eps >= 0.0f) || isinf(eps)) return api_fail(EQLIN_ERR_INVALID_ARG, "eps must be finite and >= 0");
+    if (N == 0) return EQLIN_OK;
+    const void *out = quant ? (const void *)q : y;
+    if (!x || !out || (quant && !scale)) return api_fail(EQLIN_ERR_INVALID_ARG, "null x or output");
+    const size_t eb = elem_bytes(dtype), n = (size_t)N * C * G;
+    if (!aligned(x, 16) || !aligned(residual, 16) || !aligned(sum, 16) || !aligned(out, 16))
+        return api_fail(EQLIN_ERR_INVALID_ARG, "x, residual, sum and the output must be 16-byte aligned");
+    if (!aligned(gamma, eb) || !aligned(rstd, 4) || !aligned(scale, 4)) return api_fail(EQLIN_ERR_INVALID_ARG, "gamma, rstd or scale misaligned");
+    const size_t ob = quant ? n : n * eb;
+    const void *ins[] = {x, residual, gamma};
+    const size_t in_bytes[] = {n * eb, n * eb, (size_t)C * eb};
+    void *outs[] = {sum, const_cast<void *>(out), rstd, scale};
+    const size_t out_bytes[] = {n * eb, ob, (size_t)N * 4, (size_t)N * 4};
+    for (int a = 0; a < 4; ++a) {
+        for (int b = 0; b < 3; ++b)
+            if (overlap(outs[a], out_bytes[a], ins[b], in_bytes[b])) return api_fail(EQLIN_ERR_INVALID_ARG, "an output overlaps an input");
+        for (int b = 0; b < a; ++b)
+            if (overlap(outs[a], out_bytes[a], outs[b], out_bytes[b])) return api_fail(EQLIN_ERR_INVALID_ARG, "outputs overlap");
+    }
+    eqlin::NormParams p = {x, residual, gamma, sum, y, q, scale, rstd, N, C, ilog2(G), eps};
+    (void)hipGetLastError();
+    return done(eqlin::launch_rmsnorm(p, dtype, (hipStream_t)stream), what);
+}
+
+// arguments shared by the attention's entry points -> the kernels' parameters
+eqlin_status_t check_attention(const eqlin_attention_args *a, eqlin::AttnParams *p) {
+    if (!a) return api_fail(EQLIN_ERR_INVALID_ARG, "null arguments");
+    if (!valid_dtype(a->dtype)) return api_fail(EQLIN_ERR_INVALID_ARG, "bad dtype %d", (int)a->dtype);
+    if (a->batch < 0 || a->total_q < 0 || a->total_k < 0)
+        return api_fail(EQLIN_ERR_INVALID_ARG, "batch = %d, total_q = %lld, total_k = %lld", a->batch, (long long)a->total_q, (long long)a->total_k);
+    if (a->heads_q < 1 || a->heads_kv < 1 || a->heads_q % a->heads_kv != 0)
+        return api_fail(EQLIN_ERR_INVALID_ARG, "heads_q = %d must be a multiple of heads_kv = %d", a->heads_q, a->heads_kv);
+    const int per = a->dtype == EQLIN_F32 ? 4 : 8;
+    if (a->dim < 1) return api_fail(EQLIN_ERR_INVALID_ARG, "dim = %d", a->dim);
+    if (a->dim > 128 || a->dim % per != 0)
+        return api_fail(EQLIN_ERR_UNSUPPORTED, "dim = %d: a multiple of %d up to 128", a->dim, per);
+    if (!(a->scale > 0.0f) || isinf(a->scale)) return api_fail(EQLIN_ERR_INVALID_ARG, "scale must be finite and > 0");
+    const int64_t most = INT64_C(0x7fffffff) - 4096;
+    if (a->total_q > most || a->total_k > most) return api_fail(EQLIN_ERR_UNSUPPORTED, "total_q or total_k beyond 2^31");
+    if (a->total_q > (1 << 30) / a->heads_q || a->batch > (1 << 22))  // the launch's index range
+        return api_fail(EQLIN_ERR_UNSUPPORTED, "total_q * heads_q beyond 2^30 or batch beyond 2^22");
+    if (a->heads_kv > 65535) return api_fail(EQLIN_ERR_UNSUPPORTED, "heads_kv = %d beyond 65535", a->heads_kv);
+    *p = eqlin::AttnParams{};
+    p->q = a->q, p->k = a->k, p->v = a->v, p->o = a->o, p->lse = a->lse;
+    p->qt = a->q_token_stride, p->qh = a->q_head_stride, p->kt = a->k_token_stride, p->kh = a->k_head_stride;
+    p->vt = a->v_token_stride, p->vh = a->v_head_stride, p->ot = a->o_token_stride, p->oh = a->o_head_stride;
+    p->cu_q = a->cu_q, p->cu_k = a->cu_k, p->len_k = a->len_k;
+    p->total_q = a->total_q, p->total_k = a->total_k;
+    p->B = a->batch, p->Hq = a->heads_q, p->Hkv = a->heads_kv, p->grp = a->heads_q / a->heads_kv, p->D = a->dim;
+    p->scale = a->scale, p->causal = a->causal != 0;
+    p->nsplit = 1;
+    return EQLIN_OK;
+}
+
+// a [tokens][heads][dim] tensor's pointer and strides
+eqlin_status_t check_tensor(const void *t, int64_t ts, int64_t hs, int64_t tokens, eqlin_dtype_t dtype, const char *name) {
+    if (tokens == 0) return EQLIN_OK;
+    if (!t) return api_fail(EQLIN_ERR_INVALID_ARG, "null %s", name);
+    const int per = dtype == EQLIN_F32 ? 4 : 8;
+    if (!aligned(t, 16) || ts % per != 0 || hs % per != 0)
+        return api_fail(EQLIN_ERR_INVALID_ARG, "%s must be 16-byte aligned, its strides multiples of %d elements", name, per);
+    if (ts < 0 || hs < 0 || ts > (INT64_C(1) << 40) / 16 || hs > (INT64_C(1) << 40) / 16)
+        return api_fail(EQLIN_ERR_INVALID_ARG, "%s: strides out of range", name);
+    return EQLIN_OK;
+}
+
+size_t extent(int64_t ts, int64_t hs, int64_t tokens, int heads, int dim, eqlin_dtype_t d) {
+    return tokens == 0 ? 0 : (size_t)((tokens - 1) * ts + (heads - 1) * hs + dim) * elem_bytes(d);
+}
+
+}  // namespace
+
+extern "C" {
+
+eqlin_status_t eqlin_rmsnorm(const void *x, const void *residual, const void *gamma, void *sum, void *y, float *rstd,
+                             int64_t N, int C, int G, float eps, eqlin_dtype_t dtype, eqlin_stream_t stream) {
+    return rmsnorm(x, residual, gamma, sum, y, nullptr, nullptr, rstd, N, C, G, eps, dtype, stream, false, "eqlin_rmsnorm launch");
+}
+
+eqlin_status_t eqlin_rmsnorm_quant(const void *x, const void *residual, const void *gamma, void *sum, uint8_t *q,
+                                   float *scale, float *rstd, int64_t N, int C, int G, float eps, eqlin_dtype_t dtype,
+                                   eqlin_stream_t stream) {
+    return rmsnorm(x, residual, gamma, sum, nullptr, q, scale, rstd, N, C, G, eps, dtype, stream, true,
+                   "eqlin_rmsnorm_quant launch");
+}
+
+size_t eqlin_rmsnorm_backward_workspace(int64_t N, int C, int G) {
+    return N <= 0 || C < 1 ? 0 : eqlin::rmsnorm_backward_workspace_bytes(N, C, G);
+}
+
+eqlin_status_t eqlin_rmsnorm_backward(const void *sum, const void *gamma, const float *rstd, const void *dy,
+                                      const void *dsum, void *dx, float *dgamma, int64_t N, int C, int G,
+                                      eqlin_dtype_t dtype, void *workspace, size_t workspace_bytes,
+                                      eqlin_stream_t stream) {
+    eqlin::api_clear();
+    eqlin_status_t st = check_norm(N, C, G, dtype);
+    if (st != EQLIN_OK) return st;
+    if (!aligned(dgamma, 4)) return api_fail(EQLIN_ERR_INVALID_ARG, "dgamma misaligned");
+    if (N == 0 && !dgamma) return EQLIN_OK;
+    if (N > 0) {
+        if (!sum || !rstd || !dy || !dx) return api_fail(EQLIN_ERR_INVALID_ARG, "null sum, rstd, dy or dx");
+        const size_t eb = elem_bytes(dtype), n = (size_t)N * C * G;
+        if (!aligned(sum, 16) || !aligned(dy, 16) || !aligned(dsum, 16) || !aligned(dx, 16))
+            return api_fail(EQLIN_ERR_INVALID_ARG, "sum, dy, dsum and dx must be 16-byte aligned");
+        if (!aligned(gamma, eb) || !aligned(rstd, 4)) return api_fail(EQLIN_ERR_INVALID_ARG, "gamma or rstd misaligned");
+        const size_t need = dgamma ? eqlin::rmsnorm_backward_workspace_bytes(N, C, G) : 0;
+        st = check_workspace(workspace, workspace_bytes, need);
+        if (st != EQLIN_OK) return st;
+        const void *ins[] = {sum, dy, dsum, gamma, rstd};
+        const size_t in_bytes[] = {n * eb, n * eb, n * eb, (size_t)C * eb, (size_t)N * 4};
+        for (int b = 0; b < 5; ++b)
+            if (overlap(dx, n * eb, ins[b], in_bytes[b]) || overlap(dgamma, (size_t)C * 4, ins[b], in_bytes[b]))
+                return api_fail(EQLIN_ERR_INVALID_ARG, "an output overlaps an input");
+        if (overlap(dx, n * eb, dgamma, (size_t)C * 4)) return api_fail(EQLIN_ERR_INVALID_ARG, "outputs overlap");
+    }
+    eqlin::NormGradParams p = {sum, gamma, dy, dsum, rstd, dx, dgamma, (float *)workspace, N, C, ilog2(G)};
+    (void)hipGetLastError();
+    return done(eqlin::launch_rmsnorm_backward(p, dtype, (hipStream_t)stream), "eqlin_rmsnorm_backward launch");
+}
+
+eqlin_status_t eqlin_rotary(const void *x, int64_t x_token_stride, int64_t x_head_stride, void *y,
+                            int64_t y_token_stride, int64_t y_head_stride, const int32_t *pos, int64_t N, int H, int dc,
+                            int G, int axes, const int *pairs, double base, unsigned flags, eqlin_dtype_t dtype,
+                            eqlin_stream_t stream) {
+    eqlin::api_clear();
+    if (!valid_dtype(dtype)) return api_fail(EQLIN_ERR_INVALID_ARG, "bad dtype %d", (int)dtype);
+    if (N < 0 || H < 1 || dc < 1) return api_fail(EQLIN_ERR_INVALID_ARG, "N = %lld, H = %d, dc = %d", (long long)N, H, dc);
+    if (!(G == 1 || G == 2 || G == 4 || G == 8)) return api_fail(EQLIN_ERR_INVALID_ARG, "G = %d not in {1, 2, 4, 8}", G);
+    if (flags & ~(EQLIN_ROTARY_INVERSE | EQLIN_ROTARY_D4)) return api_fail(EQLIN_ERR_INVALID_ARG, "unknown flags 0x%x", flags);
+    if ((flags & EQLIN_ROTARY_D4) && G != 8) return api_fail(EQLIN_ERR_INVALID_ARG, "EQLIN_ROTARY_D4 needs G = 8 (got G = %d)", G);
+    if (axes < 1 || axes > eqlin::kRotaryMaxAxes || !pairs) return api_fail(EQLIN_ERR_INVALID_ARG, "axes = %d: 1 to %d, with pairs", axes, eqlin::kRotaryMaxAxes);
+    if (!(base > 0.0) || isinf(base)) return api_fail(EQLIN_ERR_INVALID_ARG, "base must be finite and > 0");
+    eqlin::RotaryParams p = {};
+    int64_t P = 0;
+    for (int a = 0; a < axes; ++a) {
+        if (pairs[a] < 0) return api_fail(EQLIN_ERR_INVALID_ARG, "pairs[%d] = %d < 0", a, pairs[a]);
+        P += pairs[a];
+        if (2 * P > dc) return api_fail(EQLIN_ERR_INVALID_ARG, "%lld pairs need more than dc = %d channels", (long long)P, dc);
+        if (P > eqlin::kRotaryMaxPairs) return api_fail(EQLIN_ERR_UNSUPPORTED, "more than %d pairs", eqlin::kRotaryMaxPairs);
+        p.end[a] = (int)P;
+        for (int i = 0; i < pairs[a]; ++i) p.freq[P - pairs[a] + i] = pow(base, -(double)i / pairs[a]) / 6.283185307179586476925;
+    }
+    if (P < 1) return api_fail(EQLIN_ERR_INVALID_ARG, "no pairs");
+    if ((int64_t)dc * G > (1 << 20) || H > (1 << 20)) return api_fail(EQLIN_ERR_UNSUPPORTED, "dc * G or H beyond 2^20");
+    if (N > (INT64_C(1) << 40) / ((int64_t)dc * G)) return api_fail(EQLIN_ERR_UNSUPPORTED, "N = %lld overflows the index range", (long long)N);
+    if (N == 0) return EQLIN_OK;
+    if (!x || !y || !pos) return api_fail(EQLIN_ERR_INVALID_ARG, "null x, y or pos");
+    const size_t eb = elem_bytes(dtype);
+    if (!aligned(x, eb) || !aligned(y, eb) || !aligned(pos, 4)) return api_fail(EQLIN_ERR_INVALID_ARG, "x, y or pos misaligned");
+    const int64_t D = (int64_t)dc * G, smost = INT64_C(1) << 26;
+    if (x_token_stride < 0 || x_head_stride < 0 || y_token_stride < 0 || y_head_stride < 0 || x_token_stride > smost ||
+        x_head_stride > smost || y_token_stride > smost || y_head_stride > smost)
+        return api_fail(EQLIN_ERR_INVALID_ARG, "strides out of range");
+    if ((H > 1 && y_head_stride < D) || (N > 1 && y_token_stride < D)) return api_fail(EQLIN_ERR_INVALID_ARG, "y's strides fold it onto itself");
+    const size_t xb = extent(x_token_stride, x_head_stride, N, H, (int)D, dtype), yb = extent(y_token_stride, y_head_stride, N, H, (int)D, dtype);
+    if (x == y) {
+        if (x_token_stride != y_token_stride || x_head_stride != y_head_stride)
+            return api_fail(EQLIN_ERR_INVALID_ARG, "in place, x and y need the same strides");
+    } else if (overlap(y, yb, x, xb)) {
+        return api_fail(EQLIN_ERR_INVALID_ARG, "x and y overlap");
+    }
+    if (overlap(y, yb, pos, (size_t)N * axes * 4)) return api_fail(EQLIN_ERR_INVALID_ARG, "y overlaps pos");
+    p.x = x, p.y = y, p.pos = pos;
+    p.N = N, p.xt = x_token_stride, p.xh = x_head_stride, p.yt = y_token_stride, p.yh = y_head_stride;
+    p.H = H, p.dc = dc, p.lg = ilog2(G), p.axes = axes, p.P = (int)P;
+    p.d4 = (flags & EQLIN_ROTARY_D4) != 0, p.inverse = (flags & EQLIN_ROTARY_INVERSE) != 0;
+    (void)hipGetLastError();
+    return done(eqlin::launch_rotary(p, dtype, (hipStream_t)stream), "eqlin_rotary launch");
+}
+
+size_t eqlin_attention_workspace(const eqlin_attention_args *a) {
+    eqlin::AttnParams p;
+    if (check_attention(a, &p) != EQLIN_OK) return 0;
+    return eqlin::attention_workspace_bytes(p, a->dtype);
+}
+
+eqlin_status_t eqlin_attention(const eqlin_attention_args *a, void *workspace, size_t workspace_bytes,
+                               eqlin_stream_t stream) {
+    eqlin::api_clear();
+    eqlin::AttnParams p;
+    eqlin_status_t st = check_attention(a, &p);
+    if (st != EQLIN_OK) return st;
+    if (a->total_q == 0 || a->batch == 0) return EQLIN_OK;
+    if ((st = check_tensor(a->q, p.qt, p.qh, a->total_q, a->dtype, "q")) != EQLIN_OK) return st;
+    if ((st = check_tensor(a->k, p.kt, p.kh, a->total_k, a->dtype, "k")) != EQLIN_OK) return st;
+    if ((st = check_tensor(a->v, p.vt, p.vh, a->total_k, a->dtype, "v")) != EQLIN_OK) return st;
+    if ((st = check_tensor(a->o, p.ot, p.oh, a->total_q, a->dtype, "o")) != EQLIN_OK) return st;
+    if (!a->cu_q || !a->cu_k) return api_fail(EQLIN_ERR_INVALID_ARG, "null cu_q or cu_k");
+    if (!aligned(a->cu_q, 4) || !aligned(a->cu_k, 4) || !aligned(a->len_k, 4) || !aligned(a->lse, 4))
+        return api_fail(EQLIN_ERR_INVALID_ARG, "cu_q, cu_k, len_k or lse misaligned");
+    if ((st = check_workspace(workspace, workspace_bytes, eqlin::attention_workspace_bytes(p, a->dtype))) != EQLIN_OK) return st;
+    const size_t ob = extent(p.ot, p.oh, a->total_q, p.Hq, p.D, a->dtype), lb = (size_t)a->total_q * p.Hq * 4;
+    const void *ins[] = {a->q, a->k, a->v};
+    const size_t in_bytes[] = {extent(p.qt, p.qh, a->total_q, p.Hq, p.D, a->dtype), extent(p.kt, p.kh, a->total_k, p.Hkv, p.D, a->dtype),
+                               extent(p.vt, p.vh, a->total_k, p.Hkv, p.D, a->dtype)};
+    for (int i = 0; i < 3; ++i)
+        if (overlap(a->o, ob, ins[i], in_bytes[i]) || overlap(a->lse, lb, ins[i], in_bytes[i]))
+            return api_fail(EQLIN_ERR_INVALID_ARG, "an output overlaps an input");
+    if (overlap(a->lse, lb, a->o, ob)) return api_fail(EQLIN_ERR_INVALID_ARG, "o and lse overlap");
+    p.ws = (float *)workspace;
+    (void)hipGetLastError();
+    return done(eqlin::launch_attention(p, a->dtype, (hipStream_t)stream), "eqlin_attention launch");
+}
+
+size_t eqlin_attention_backward_workspace(const eqlin_attention_args *a) {
+    eqlin::AttnParams p;
+    if (check_attention(a, &p) != EQLIN_OK) return 0;
+    return eqlin::attention_backward_workspace_bytes(p);
+}
+
+eqlin_status_t eqlin_attention_backward(const eqlin_attention_args *a, const eqlin_attention_grads *g, void *workspace,
+                                        size_t workspace_bytes, eqlin_stream_t stream) {
+    eqlin::api_clear();
+    eqlin::AttnParams p;
+    eqlin_status_t st = check_attention(a, &p);
+    if (st != EQLIN_OK) return st;
+    if (!g) return api_fail(EQLIN_ERR_INVALID_ARG, "null gradients");
+    if (a->batch == 0 || (a->total_q == 0 && a->total_k == 0)) return EQLIN_OK;
+    struct {
+        const void *t;
+        int64_t ts, hs, tokens;
+        int heads;
+        const char *name;
+        bool out;
+    } t[] = {{a->q, p.qt, p.qh, a->total_q, p.Hq, "q", false},
+             {a->k, p.kt, p.kh, a->total_k, p.Hkv, "k", false},
+             {a->v, p.vt, p.vh, a->total_k, p.Hkv, "v", false},
+             {a->o, p.ot, p.oh, a->total_q, p.Hq, "o", false},
+             {g->d_o, g->do_token_stride, g->do_head_stride, a->total_q, p.Hq, "d_o", false},
+             {g->dq, g->dq_token_stride, g->dq_head_stride, a->total_q, p.Hq, "dq", true},
+             {g->dk, g->dk_token_stride, g->dk_head_stride, a->total_k, p.Hkv, "dk", true},
+             {g->dv, g->dv_token_stride, g->dv_head_stride, a->total_k, p.Hkv, "dv", true}};
+    for (const auto &x : t)
+        if ((st = check_tensor(x.t, x.ts, x.hs, x.tokens, a->dtype, x.name)) != EQLIN_OK) return st;
+    if (!a->cu_q || !a->cu_k || (a->total_q > 0 && !a->lse)) return api_fail(EQLIN_ERR_INVALID_ARG, "null cu_q, cu_k or lse");
+    if (!aligned(a->cu_q, 4) || !aligned(a->cu_k, 4) || !aligned(a->len_k, 4) || !aligned(a->lse, 4))
+        return api_fail(EQLIN_ERR_INVALID_ARG, "cu_q, cu_k, len_k or lse misaligned");
+    if ((st = check_workspace(workspace, workspace_bytes, eqlin::attention_backward_workspace_bytes(p))) != EQLIN_OK) return st;
+    // dq, dk and dv may be interleaved parts of one tensor (the gradient of a qkv layer's output), so only an
+    // output over an input is refused
+    for (const auto &x : t)
+        for (const auto &y : t)
+            if (x.out && !y.out &&
+                overlap(x.t, extent(x.ts, x.hs, x.tokens, x.heads, p.D, a->dtype), y.t, extent(y.ts, y.hs, y.tokens, y.heads, p.D, a->dtype)))
+                return api_fail(EQLIN_ERR_INVALID_ARG, "%s overlaps %s", x.name, y.name);
+    p.dout = g->d_o, p.dot = g->do_token_stride, p.doh = g->do_head_stride;
+    p.dq = g->dq, p.dqt = g->dq_token_stride, p.dqh = g->dq_head_stride;
+    p.dk = g->dk, p.dkt = g->dk_token_stride, p.dkh = g->dk_head_stride;
+    p.dv = g->dv, p.dvt = g->dv_token_stride, p.dvh = g->dv_head_stride;
+    p.ws = (float *)workspace;
+    (void)hipGetLastError();
+    return done(eqlin::launch_attention_backward(p, a->dtype, (hipStream_t)stream), "eqlin_attention_backward launch");
+}
+
+}  // extern "C"

@@ -277,6 +277,148 @@ eqlin_status_t eqlin_conv_forward(eqlin_handle_t h, const void *x, const void *b
 eqlin_status_t eqlin_conv_forward_expanded(eqlin_handle_t h, const void *x, const void *bias, void *y, int64_t B,
                                            int H, int W, eqlin_stream_t stream);
 
+/*
+ * ---- The operators around the layer in a transformer stage ----
+ *
+ * A stage holds its tokens as x[N][C][G] and runs: norm, EQ-Linear (q, k, v), rotary positions, attention,
+ * EQ-Linear, norm with the residual's addition, MLP block. The three operators below are the ones between
+ * the layers, forward and backward. They need no handle: everything is an argument, and a call works on the
+ * current device and on `stream` only. The rules of the head of this file hold (arguments checked on the
+ * host before anything is enqueued, no allocation, no synchronisation, no exceptions); contents of device
+ * arrays (positions, sequence bounds) cannot be checked there, and no kernel reads or writes outside the
+ * given tensors whatever they hold. All results are the same bits on every call (no atomics).
+ */
+
+/*
+ * eqlin_rmsnorm -- root-mean-square norm of each token over its C x G values, with the residual's addition:
+ *
+ *     s = x + residual;   rstd = (mean over (c, g) of s^2 + eps)^(-1/2);   y[n, c, g] = s[n, c, g] rstd[n] gamma[c]
+ *
+ * The mean runs over the group axis too and gamma has one value a channel, so a shift of the group axis
+ * passes through. fp32 throughout; y is taken from the unrounded sum; s and y are each rounded once.
+ *   x, residual  device [N][C][G] of dtype (EQLIN_F32, EQLIN_BF16 or EQLIN_F16); residual may be NULL (s = x).
+ *   gamma        device [C] of dtype, or NULL (ones).
+ *   sum          device [N][C][G], receives s, or NULL;  y device [N][C][G];  rstd device float [N] or NULL.
+ *   N >= 0 (0 enqueues nothing); C >= 1; G in {1, 2, 4, 8}; C * G <= 2^20 (else UNSUPPORTED); eps >= 0, finite.
+ * x, residual, sum and y must be 16-byte aligned; sum and y overlap neither the inputs nor each other.
+ * Rows that are no whole number of 16-byte vectors, or longer than 16384 (fp32: 8192) values, run a slower
+ * kernel.
+ */
+eqlin_status_t eqlin_rmsnorm(const void *x, const void *residual, const void *gamma, void *sum, void *y, float *rstd,
+                             int64_t N, int C, int G, float eps, eqlin_dtype_t dtype, eqlin_stream_t stream);
+
+/*
+ * eqlin_rmsnorm_quant -- the same with an 8-bit output for a product in e4m3 (OCP: 4 exponent and 3 mantissa
+ * bits, largest value 448): q = y / scale rounded to nearest even, with one scale a token, scale = max |y| / 448
+ * (1 for a row of zeros; at least the smallest normal fp32 number), so y = q scale.
+ *   q  device [N][C][G] bytes, 16-byte aligned;  scale  device float [N].  Otherwise as eqlin_rmsnorm.
+ */
+eqlin_status_t eqlin_rmsnorm_quant(const void *x, const void *residual, const void *gamma, void *sum, uint8_t *q,
+                                   float *scale, float *rstd, int64_t N, int C, int G, float eps, eqlin_dtype_t dtype,
+                                   eqlin_stream_t stream);
+
+/*
+ * eqlin_rmsnorm_backward -- with xh = s rstd and w = dy gamma:
+ *
+ *     dx = dsum + rstd (w - xh mean(w xh));     dgamma[c] = sum over n, g of dy xh
+ *
+ *   sum, rstd  the forward's s and rstd;  dy device [N][C][G];  dsum device [N][C][G], the gradient that
+ *              reaches s from the residual stream, or NULL.
+ *   dx         device [N][C][G] of dtype: the gradient of x and of the residual;  dgamma device float [C] or NULL
+ *              (overwritten; zeros for N == 0).
+ *   workspace  eqlin_rmsnorm_backward_workspace(N, C, G) bytes, 256-byte aligned (may be NULL without dgamma).
+ */
+size_t eqlin_rmsnorm_backward_workspace(int64_t N, int C, int G);
+eqlin_status_t eqlin_rmsnorm_backward(const void *sum, const void *gamma, const float *rstd, const void *dy,
+                                      const void *dsum, void *dx, float *dgamma, int64_t N, int C, int G,
+                                      eqlin_dtype_t dtype, void *workspace, size_t workspace_bytes,
+                                      eqlin_stream_t stream);
+
+/*
+ * eqlin_rotary -- rotary positions over 1 to 4 axes (the last two: row, column) on heads of dc channels x G:
+ *
+ *     (a, b) = (x[n, h, j, g], x[n, h, j + P, g]) -> (a cos t - b sin t, a sin t + b cos t),  j < P
+ *     t = base^(-i / pairs[axis]) * (position of token n on pair j's axis, as group element g sees it)
+ *
+ * Pairs are dealt to the axes in order: the first pairs[0] to axis 0, and so on; i counts within the axis and
+ * P is their sum; channels from 2 P on are copied. With two axes or more and G > 1, group element g sees the
+ * (row, column) turned by its inverse: R^-g (row, column) for the cyclic group (R(row, col) = (-col, row) at a
+ * quarter turn, eighth turns at G = 8), S^b R^-a for element a + 4 b of D4, S(row, col) = (row, -col). Turning
+ * the image and shifting the group axis (by left translation) then commutes with the operator, and so with
+ * the scores of two rotated heads; further axes (time) are the same for every g. G = 1 is the plain rotation.
+ *   x, y   device [N][H][dc][G] of dtype with token and head strides in elements (dc * G contiguous); y may be x
+ *          (with x's strides), else they must not overlap. Unaligned pointers or strides run a slower kernel.
+ *   pos    device int32 [N][axes].
+ *   pairs  HOST int [axes], each >= 0, read during the call; 1 <= P <= 256 (else UNSUPPORTED), 2 P <= dc.
+ *   base   > 0, finite.   flags: EQLIN_ROTARY_D4 (G must be 8), EQLIN_ROTARY_INVERSE (turns by -t: the
+ *          backward, dx from dy, and the way back).
+ * Angles are exact to fp32 at any position (reduced to a turn in fp64); one rounding of y.
+ */
+#define EQLIN_ROTARY_INVERSE 1u
+#define EQLIN_ROTARY_D4 4u
+eqlin_status_t eqlin_rotary(const void *x, int64_t x_token_stride, int64_t x_head_stride, void *y,
+                            int64_t y_token_stride, int64_t y_head_stride, const int32_t *pos, int64_t N, int H, int dc,
+                            int G, int axes, const int *pairs, double base, unsigned flags, eqlin_dtype_t dtype,
+                            eqlin_stream_t stream);
+
+/*
+ * eqlin_attention -- attention over packed sequences with grouped heads:
+ *
+ *     o[t, h] = sum over j of softmax_j(scale q[t, h] . k[j, h / group]) v[j, h / group]
+ *     lse[t, h] = log sum over j of exp(scale q . k)
+ *
+ * for token t of sequence i over the keys j of sequence i. heads_q = group * heads_kv. A head is `dim`
+ * contiguous elements: dc channels x G of the layer's layout, on which q . k is unchanged and o follows a shift
+ * of the group axis. causal: token t (of lq) sees key j (of lk) when j <= t + lk - lq, so the last token sees
+ * all keys (one new token over a cache, the next piece of a prompt). A token that sees no key gets o = 0 and
+ * lse = -infinity. Keys that a token does not see have no part in its result, whatever they hold.
+ *   q, k, v, o   tensor[token][head][dim] of dtype with token and head strides in ELEMENTS; pointers 16-byte
+ *                aligned, strides a multiple of 16 bytes (else INVALID_ARG); dim a multiple of 8 (fp32: of 4)
+ *                up to 128 (else UNSUPPORTED). o overlaps no input.
+ *   cu_q, cu_k   device int32 [batch + 1]: sequence i has the tokens from cu[i] to cu[i + 1]. cu[0] = 0 and
+ *                cu[batch] = total; rows outside every sequence are not written.
+ *   len_k        device int32 [batch] or NULL: how many keys of sequence i's stretch of cu_k count (a cache
+ *                with room to grow).
+ *   lse          device float [total_q][heads_q] or NULL (the backward needs it).
+ *   scale        > 0, finite.   batch in 0..2^22; total_k < 2^31 - 4096, total_q * heads_q <= 2^30.
+ * Products and sums in fp32; the half types round the unnormalised probabilities (at most 2^8) to the type
+ * for the second product.
+ *   workspace    eqlin_attention_workspace(a) bytes, 256-byte aligned (NULL when that is 0): partial results
+ *                where few query rows make it split the keys. Calls sharing it must not overlap.
+ */
+typedef struct eqlin_attention_args {
+    const void *q, *k, *v;
+    void *o;
+    float *lse;
+    int64_t q_token_stride, q_head_stride, k_token_stride, k_head_stride;
+    int64_t v_token_stride, v_head_stride, o_token_stride, o_head_stride;
+    const int32_t *cu_q, *cu_k, *len_k;
+    int64_t total_q, total_k;
+    int batch, heads_q, heads_kv, dim;
+    float scale;
+    int causal;
+    eqlin_dtype_t dtype;
+} eqlin_attention_args;
+size_t eqlin_attention_workspace(const eqlin_attention_args *a);
+eqlin_status_t eqlin_attention(const eqlin_attention_args *a, void *workspace, size_t workspace_bytes,
+                               eqlin_stream_t stream);
+
+/*
+ * eqlin_attention_backward -- dq, dk, dv from d_o (the gradient of o; lse's is zero). a: the forward's
+ * arguments, with its o and lse. d_o, dq, dk, dv: as q, o, k, v, with strides; outputs are overwritten (keys
+ * beyond len_k get zeros). Probabilities and score gradients are rounded to the half type for their products;
+ * everything else is fp32. workspace: eqlin_attention_backward_workspace(a) bytes, 256-byte aligned.
+ */
+typedef struct eqlin_attention_grads {
+    const void *d_o;
+    void *dq, *dk, *dv;
+    int64_t do_token_stride, do_head_stride, dq_token_stride, dq_head_stride;
+    int64_t dk_token_stride, dk_head_stride, dv_token_stride, dv_head_stride;
+} eqlin_attention_grads;
+size_t eqlin_attention_backward_workspace(const eqlin_attention_args *a);
+eqlin_status_t eqlin_attention_backward(const eqlin_attention_args *a, const eqlin_attention_grads *g, void *workspace,
+                                        size_t workspace_bytes, eqlin_stream_t stream);
+
 /* Frees the handle's device memory (hipFree, which synchronises the device). NULL is a no-op. */
 eqlin_status_t eqlin_destroy(eqlin_handle_t h);
 
