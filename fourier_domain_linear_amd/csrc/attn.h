@@ -49,6 +49,13 @@ __device__ __forceinline__ f32x16 mma_frag(const uint4 &a, const uint4 &b, f32x1
 
 // W (a 32x32 product's D layout, 16 values a lane) -> B-operand fragments of the next product: NF = 2
 // (half types, rounded to nearest even) or 4 (fp32, exact).
+__device__ __forceinline__ f32x16 zero16() {
+    f32x16 z;
+#pragma unroll
+    for (int v = 0; v < 16; ++v) z[v] = 0.0f;
+    return z;
+}
+
 template <class E>
 struct WFrags {
     static constexpr int NF = __is_same(E, F32) ? 4 : 2;
@@ -86,37 +93,52 @@ struct Tile {
         else if constexpr (kRow == 128) return (((row >> 1) & 1) << 2) | ((row >> 2) & 3);
         else return (row >> 2) & 3;
     }
-    __device__ static __forceinline__ int at(int row, int chunk) { return row * kRow + ((chunk ^ swz(row)) << 4); }
-
-    // A (or B) operand of a product reducing over d: row `row` of the tile, step s
-    __device__ static __forceinline__ uint4 row_frag(const char *tile, int row, int s, int h) {
-        return *(const uint4 *)(tile + at(row, 2 * s + h));
+    // Addresses. A tile begins at a multiple of 512 bytes and the swizzle takes the row modulo 16, so every
+    // fragment's address is (tile + a lane's constant) XOR a compile-time constant, plus an immediate.
+    struct Lane {
+        uint32_t row, col0, col1;
+    };
+    __device__ static __forceinline__ Lane lane_of(int lane) {
+        const int h = lane >> 5, l32 = lane & 31, l16 = lane & 15;
+        Lane L;
+        L.row = l32 * kRow + ((h ^ swz(l32)) << 4);
+        if constexpr (__is_same(E, F32)) {
+            L.col0 = 4 * h * kRow + (((l32 >> 2) ^ h) << 4) + (l32 & 3) * 4;
+            L.col1 = 0;
+        } else {
+            const int r = 4 * h + (l16 >> 2), x = 2 * ((lane >> 4) & 1) + ((l16 >> 1) & 1);
+            L.col0 = r * kRow + ((x ^ swz(r)) << 4) + (l16 & 1) * 8;
+            L.col1 = (r + 8) * kRow + ((x ^ swz(r + 8)) << 4) + (l16 & 1) * 8;
+        }
+        return L;
+    }
+    template <class V>
+    __device__ static __forceinline__ V lds_at(uint32_t a) {
+        return *(const __attribute__((address_space(3))) V *)(uintptr_t)a;
+    }
+    // A (or B) operand of a product reducing over d: row 32 blk + lane % 32 of the tile, step s
+    __device__ static __forceinline__ uint4 row_frag(uint32_t tile, const Lane &L, int blk, int s) {
+        typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+        const u32x4 v = lds_at<u32x4>(((tile + L.row) ^ (s << 5)) + blk * 32 * kRow);
+        return __builtin_bit_cast(uint4, v);
     }
     // A operand of a product reducing over the tile's rows: rows (of the product) d = 32 db + lane % 32,
-    // reduction slots = tile rows row0 + the D-layout rows of W's fragment f (32 rows from row0)
-    __device__ static __forceinline__ uint4 col_frag(const char *tile, int row0, int f, int db, int lane) {
-        const int h = lane >> 5;
+    // reduction slots = the tile rows, from row 32 blk on, that W's fragment f holds
+    __device__ static __forceinline__ uint4 col_frag(uint32_t tile, const Lane &L, int blk, int f, int db) {
         if constexpr (__is_same(E, F32)) {
-            uint4 r;
             uint32_t v[4];
-            const int d = 32 * db + (lane & 31);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const int row = row0 + 8 * f + 4 * h + j;
-                v[j] = *(const uint32_t *)(tile + at(row, d >> 2) + (d & 3) * 4);
+                const int sw = (kRow >= 256 ? j << 2 : (j >> 1) << 2) | (2 * (f & 1));
+                v[j] = lds_at<uint32_t>(((tile + L.col0) ^ ((8 * db ^ sw) << 4)) + (32 * blk + 8 * f + j) * kRow);
             }
-            r.x = v[0], r.y = v[1], r.z = v[2], r.w = v[3];
-            return r;
+            return make_uint4(v[0], v[1], v[2], v[3]);
         } else {
             typedef short s16x4 __attribute__((ext_vector_type(4)));
             typedef __attribute__((address_space(3))) s16x4 *lds_s16x4;
-            const int l16 = lane & 15;
-            const int row = row0 + 16 * f + 4 * h + (l16 >> 2);
-            const int chunk = 4 * db + 2 * ((lane >> 4) & 1) + ((l16 >> 1) & 1);
-            const char *p0 = tile + at(row, chunk) + (l16 & 1) * 8;
-            const char *p1 = tile + at(row + 8, chunk) + (l16 & 1) * 8;
-            const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)p0);
-            const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)p1);
+            const uint32_t at = (32 * blk + 16 * f) * kRow;
+            const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(uintptr_t)(((tile + L.col0) ^ (db << 6)) + at));
+            const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(uintptr_t)(((tile + L.col1) ^ (db << 6)) + at));
             const uint2 ua = __builtin_bit_cast(uint2, a), ub = __builtin_bit_cast(uint2, b);
             return make_uint4(ua.x, ua.y, ub.x, ub.y);
         }
@@ -143,6 +165,9 @@ __device__ __forceinline__ float half_sum(float x) {
     return a + b;
 }
 __device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
+__device__ __forceinline__ int64_t uniform(int64_t x) {
+    return (int64_t)(((uint64_t)(uint32_t)uniform((int)(x >> 32)) << 32) | (uint32_t)uniform((int)x));
+}
 
 // D-layout row of value v for lane half h
 __device__ __forceinline__ constexpr int d_row(int v, int h) { return (v & 3) + 8 * (v >> 2) + 4 * h; }
@@ -165,6 +190,8 @@ __device__ __forceinline__ Seq seq_at(const AttnParams &p, int i) {
     s.k0 = clamp64(p.cu_k[i], 0, p.total_k);
     s.lk_slot = (int)(clamp64(p.cu_k[i + 1], s.k0, p.total_k) - s.k0);
     s.lk = p.len_k ? (int)clamp64(p.len_k[i], 0, s.lk_slot) : s.lk_slot;
+    s.q0 = uniform(s.q0), s.k0 = uniform(s.k0);
+    s.lq = uniform(s.lq), s.lk = uniform(s.lk), s.lk_slot = uniform(s.lk_slot);
     return s;
 }
 

@@ -43,26 +43,26 @@ __global__ void __launch_bounds__(256) k_attn_delta(const AttnParams p) {
 
 // ---- dQ: as the forward, 32 rows a wave (columns), key tiles through LDS ----
 
-template <class E, int DP, int NKB, bool MASK>
-__device__ __forceinline__ void dq_block(f32x16 *dq, const uint4 *qf, const uint4 *gf, const char *kt, const char *vt, float c,
-                                         float lse2, float delta, int lim, int lane) {
+template <class E, int DP, int NKB>
+__device__ __forceinline__ void dq_block(f32x16 *dq, const uint4 *qf, const uint4 *gf, const typename Tile<E, DP>::Lane &L, uint32_t kt,
+                                         uint32_t vt, float c, float lse2, float delta, bool masked, int lim, int h) {
     typedef Tile<E, DP> TL;
-    const int h = lane >> 5, l32 = lane & 31;
 #pragma unroll
     for (int kb = 0; kb < NKB; ++kb) {
-        f32x16 s, dp;
-#pragma unroll
-        for (int v = 0; v < 16; ++v) s[v] = 0.0f, dp[v] = 0.0f;
+        f32x16 s = zero16(), dp = zero16();
 #pragma unroll
         for (int t = 0; t < TL::kSteps; ++t) {
-            s = mma_frag<E>(TL::row_frag(kt, 32 * kb + l32, t, h), qf[t], s);
-            dp = mma_frag<E>(TL::row_frag(vt, 32 * kb + l32, t, h), gf[t], dp);
+            s = mma_frag<E>(TL::row_frag(kt, L, kb, t), qf[t], s);
+            dp = mma_frag<E>(TL::row_frag(vt, L, kb, t), gf[t], dp);
         }
 #pragma unroll
         for (int v = 0; v < 16; ++v) {
             const float pr = __builtin_amdgcn_exp2f(fmaf(s[v], c, -lse2));
             s[v] = pr * (dp[v] - delta);
-            if constexpr (MASK) s[v] = 32 * kb + d_row(v, h) <= lim ? s[v] : 0.0f;
+        }
+        if (masked) {
+#pragma unroll
+            for (int v = 0; v < 16; ++v) s[v] = 32 * kb + d_row(v, 0) <= lim - 4 * h ? s[v] : 0.0f;
         }
         WFrags<E> w;
         w.set(s);
@@ -70,7 +70,7 @@ __device__ __forceinline__ void dq_block(f32x16 *dq, const uint4 *qf, const uint
         for (int f = 0; f < WFrags<E>::NF; ++f)
 #pragma unroll
             for (int db = 0; db < DP / 32; ++db)
-                dq[db] = mma_frag<E>(TL::col_frag(kt, 32 * kb, f, db, lane), w.f[f], dq[db]);
+                dq[db] = mma_frag<E>(TL::col_frag(kt, L, kb, f, db), w.f[f], dq[db]);
     }
 }
 
@@ -126,31 +126,32 @@ __global__ void __launch_bounds__(256, __is_same(E, F32) ? 1 : 2) k_attn_dq(cons
     const float c = p.scale * kLog2e;
     const T *kg = (const T *)p.k + sq.k0 * p.kt + hk * p.kh;
     const T *vg = (const T *)p.v + sq.k0 * p.vt + hk * p.vh;
-    Stage<E, DP, C::kStage, 256> sk, sv;
+    TileDma<E, DP, C::BN> tk, tv;
+    const uint32_t lds0 = lds_offset(lds);
+    const typename TL::Lane L = TL::lane_of(lane);
+    auto fetch = [&](int k0, int buf) {
+        const int valid = sq.lk - k0;
+        if (valid < C::BN) {
+            tk.offsets(p.kt, valid, wave, lane);
+            tv.offsets(p.vt, valid, wave, lane);
+        }
+        tk.issue(lds0 + buf * 2 * C::kTileBytes, kg + (int64_t)k0 * p.kt, p.D, wave, lane);
+        tv.issue(lds0 + buf * 2 * C::kTileBytes + C::kTileBytes, vg + (int64_t)k0 * p.vt, p.D, wave, lane);
+    };
+    zero_pad(lds, C::kLds, p.D, DP, tid);
     if (k_end > 0) {
-        sk.load(kg, p.kt, sq.lk, p.D, tid);
-        sv.load(vg, p.vt, sq.lk, p.D, tid);
-        sk.store(lds, tid);
-        sv.store(lds + C::kTileBytes, tid);
+        tk.offsets(p.kt, C::BN, wave, lane);
+        tv.offsets(p.vt, C::BN, wave, lane);
+        fetch(0, 0);
     }
     int buf = 0;
     for (int k0 = 0; k0 < k_end; k0 += C::BN) {
-        __syncthreads();
-        const bool more = k0 + C::BN < k_end;
-        if (more) {
-            sk.load(kg + (int64_t)(k0 + C::BN) * p.kt, p.kt, sq.lk - k0 - C::BN, p.D, tid);
-            sv.load(vg + (int64_t)(k0 + C::BN) * p.vt, p.vt, sq.lk - k0 - C::BN, p.D, tid);
-        }
-        const char *kt = lds + buf * 2 * C::kTileBytes, *vt = kt + C::kTileBytes;
-        if (k0 <= wave_max) {
-            if (k0 + C::BN - 1 <= wave_min) dq_block<E, DP, C::NKB, false>(dq, qf, gf, kt, vt, c, lse2, delta, 0, lane);
-            else dq_block<E, DP, C::NKB, true>(dq, qf, gf, kt, vt, c, lse2, delta, last - k0, lane);
-        }
-        if (more) {
-            char *nt = lds + (buf ^ 1) * 2 * C::kTileBytes;
-            sk.store(nt, tid);
-            sv.store(nt + C::kTileBytes, tid);
-        }
+        dma_wait();
+        __syncthreads();  // this tile is in LDS; the other buffer's readers are done
+        if (k0 + C::BN < k_end) fetch(k0 + C::BN, buf ^ 1);
+        const uint32_t kt = lds0 + buf * 2 * C::kTileBytes, vt = kt + C::kTileBytes;
+        if (k0 <= wave_max)
+            dq_block<E, DP, C::NKB>(dq, qf, gf, L, kt, vt, c, lse2, delta, k0 + C::BN - 1 > wave_min, last - k0, h);
         buf ^= 1;
     }
     if (live) store_column<E, DP>(dq, p.scale, (T *)p.dq + (sq.q0 + tok) * p.dqt + hq * p.dqh, p.D, h);
@@ -158,64 +159,42 @@ __global__ void __launch_bounds__(256, __is_same(E, F32) ? 1 : 2) k_attn_dq(cons
 
 // ---- dK, dV: 32 keys a wave (columns), tiles of packed rows (q and dO) through LDS ----
 
-// A tile of packed rows of q or dO.
-template <class E, int DP, int N>
-struct RowStage {
+template <class E, int DP, int NRB>
+__device__ __forceinline__ void dkv_block(f32x16 *dk, f32x16 *dv, const uint4 *kf, const uint4 *vf,
+                                          const typename Tile<E, DP>::Lane &L, uint32_t qt, uint32_t gt, uint32_t stats, float c,
+                                          bool masked, int key, int h) {
     typedef Tile<E, DP> TL;
-    typedef typename ElemOf<E>::type T;
-    uint4 r[N];
-    __device__ __forceinline__ void load(const T *base, int64_t ts, int64_t hs, int64_t row0, int64_t row_end, int grp, int D,
-                                         int tid) {
-#pragma unroll
-        for (int j = 0; j < N; ++j) {
-            const int id = tid + j * 256, c = id % TL::kChunks, col = c * (16 / (int)sizeof(T));
-            const int64_t row = row0 + id / TL::kChunks;
-            const int tok = (int)((uint32_t)row / (uint32_t)grp), hh = (int)((uint32_t)row - (uint32_t)tok * (uint32_t)grp);
-            r[j] = row < row_end && col < D ? *(const uint4 *)(base + tok * ts + hh * hs + col) : make_uint4(0, 0, 0, 0);
-        }
-    }
-    __device__ __forceinline__ void store(char *tile, int tid) const {
-#pragma unroll
-        for (int j = 0; j < N; ++j) {
-            const int id = tid + j * 256;
-            *(uint4 *)(tile + TL::at(id / TL::kChunks, id % TL::kChunks)) = r[j];
-        }
-    }
-};
-
-template <class E, int DP, int NRB, bool MASK>
-__device__ __forceinline__ void dkv_block(f32x16 *dk, f32x16 *dv, const uint4 *kf, const uint4 *vf, const char *qt,
-                                          const char *gt, const float *lse2, const float *delta, const int *last, float c,
-                                          int key, int lane) {
-    typedef Tile<E, DP> TL;
-    const int h = lane >> 5, l32 = lane & 31;
+    constexpr int BR = 32 * NRB;
 #pragma unroll
     for (int rb = 0; rb < NRB; ++rb) {
-        f32x16 s, dp;
-#pragma unroll
-        for (int v = 0; v < 16; ++v) s[v] = 0.0f, dp[v] = 0.0f;
+        f32x16 s = zero16(), dp = zero16();
 #pragma unroll
         for (int t = 0; t < TL::kSteps; ++t) {
-            s = mma_frag<E>(TL::row_frag(qt, 32 * rb + l32, t, h), kf[t], s);
-            dp = mma_frag<E>(TL::row_frag(gt, 32 * rb + l32, t, h), vf[t], dp);
+            s = mma_frag<E>(TL::row_frag(qt, L, rb, t), kf[t], s);
+            dp = mma_frag<E>(TL::row_frag(gt, L, rb, t), vf[t], dp);
         }
+        const uint32_t at = stats + 16 * h + 32 * rb * 4;
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
-            const int row = 32 * rb + 8 * g + 4 * h;
-            const float4 ls = *(const float4 *)(lse2 + row), de = *(const float4 *)(delta + row);
-            const float l4[4] = {ls.x, ls.y, ls.z, ls.w}, d4[4] = {de.x, de.y, de.z, de.w};
+            const f32x4 ls = TL::template lds_at<f32x4>(at + 32 * g), de = TL::template lds_at<f32x4>(at + 32 * g + BR * 4);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const int v = 4 * g + j;
-                float pr = __builtin_amdgcn_exp2f(fmaf(s[v], c, -l4[j]));
-                float ds = pr * (dp[v] - d4[j]);
-                if constexpr (MASK) {
-                    const bool see = key <= last[row + j];
-                    pr = see ? pr : 0.0f;
-                    ds = see ? ds : 0.0f;
+                s[v] = __builtin_amdgcn_exp2f(fmaf(s[v], c, -ls[j]));
+                dp[v] = s[v] * (dp[v] - de[j]);
+            }
+        }
+        if (masked) {
+            typedef int i32x4 __attribute__((ext_vector_type(4)));
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                const i32x4 la = TL::template lds_at<i32x4>(at + 32 * g + 2 * BR * 4);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int v = 4 * g + j;
+                    s[v] = key <= la[j] ? s[v] : 0.0f;
+                    dp[v] = key <= la[j] ? dp[v] : 0.0f;
                 }
-                s[v] = pr;
-                dp[v] = ds;
             }
         }
         WFrags<E> w;
@@ -224,13 +203,13 @@ __device__ __forceinline__ void dkv_block(f32x16 *dk, f32x16 *dv, const uint4 *k
         for (int f = 0; f < WFrags<E>::NF; ++f)
 #pragma unroll
             for (int db = 0; db < DP / 32; ++db)
-                dv[db] = mma_frag<E>(TL::col_frag(gt, 32 * rb, f, db, lane), w.f[f], dv[db]);
+                dv[db] = mma_frag<E>(TL::col_frag(gt, L, rb, f, db), w.f[f], dv[db]);
         w.set(dp);
 #pragma unroll
         for (int f = 0; f < WFrags<E>::NF; ++f)
 #pragma unroll
             for (int db = 0; db < DP / 32; ++db)
-                dk[db] = mma_frag<E>(TL::col_frag(qt, 32 * rb, f, db, lane), w.f[f], dk[db]);
+                dk[db] = mma_frag<E>(TL::col_frag(qt, L, rb, f, db), w.f[f], dk[db]);
     }
 }
 
@@ -241,9 +220,9 @@ struct DkvCfg {
     static constexpr int NRB = __is_same(E, F32) ? 1 : 2;
     static constexpr int BR = 32 * NRB;  // packed rows of a tile
     static constexpr int kTileBytes = BR * TL::kRow;
-    static constexpr int kStage = kTileBytes / 16 / 256;
-    static constexpr int kBuf = 2 * kTileBytes + 3 * BR * 4;  // q, dO, lse, delta, last key
-    static constexpr int kLds = 2 * kBuf;
+    static constexpr int kStats = 3 * BR * 4;                    // lse, delta, last key of each row
+    static constexpr int kLds = 4 * kTileBytes + 2 * kStats;     // q and dO, two buffers; then the rows' values
+    static_assert(4 * kTileBytes <= 65536, "tiles in the first 64 KB");
 };
 
 template <class E, int DP>
@@ -286,50 +265,58 @@ __global__ void __launch_bounds__(256, __is_same(E, F32) || DP > 64 ? 1 : 2) k_a
     const T *qg = (const T *)p.q + sq.q0 * p.qt + (int64_t)hk * p.grp * p.qh;
     const T *gg = (const T *)p.dout + sq.q0 * p.dot + (int64_t)hk * p.grp * p.doh;
     const float *lse = p.lse + sq.q0 * p.Hq + hk * p.grp, *del = p.ws + sq.q0 * p.Hq + hk * p.grp;
-    RowStage<E, DP, C::kStage> sqs, sgs;
+    TileDma<E, DP, C::BR> tq, tg;
+    const uint32_t lds0 = lds_offset(lds);
+    const typename TL::Lane L = TL::lane_of(lane);
     float st_lse = INFINITY, st_del = 0.0f;
     int st_last = -1;
-    auto load = [&](int64_t r0) {
-        sqs.load(qg, p.qt, p.qh, r0, row_end, p.grp, p.D, tid);
-        sgs.load(gg, p.dot, p.doh, r0, row_end, p.grp, p.D, tid);
+    // Row offsets within a tile repeat from tile to tile where the group divides the tile.
+    const bool repeats = C::BR % p.grp == 0;
+    auto load = [&](int64_t r0, int buf) {
+        const int tok0 = (int)((uint32_t)r0 / (uint32_t)p.grp), rem = (int)((uint32_t)r0 - (uint32_t)tok0 * (uint32_t)p.grp);
+        const int64_t valid = row_end - r0;
+        if (!repeats || valid < C::BR) {
+            tq.offsets_packed(p.qt, p.qh, rem, p.grp, (int)min(valid, (int64_t)C::BR), wave, lane);
+            tg.offsets_packed(p.dot, p.doh, rem, p.grp, (int)min(valid, (int64_t)C::BR), wave, lane);
+        }
+        tq.issue(lds0 + 2 * buf * C::kTileBytes, qg + tok0 * p.qt, p.D, wave, lane);
+        tg.issue(lds0 + (2 * buf + 1) * C::kTileBytes, gg + tok0 * p.dot, p.D, wave, lane);
         if (tid < C::BR) {
-            const int64_t row = r0 + tid;
-            const int tok = (int)((uint32_t)row / (uint32_t)p.grp), hh = (int)((uint32_t)row - (uint32_t)tok * (uint32_t)p.grp);
-            const bool in = row < row_end;
+            const uint32_t r = (uint32_t)(rem + tid);
+            const int tok = tok0 + (int)(r / (uint32_t)p.grp), hh = (int)(r % (uint32_t)p.grp);
+            const bool in = tid < valid;
             st_lse = in ? lse[(int64_t)tok * p.Hq + hh] * kLog2e : INFINITY;
             st_del = in ? del[(int64_t)tok * p.Hq + hh] : 0.0f;
             st_last = in ? (p.causal ? min(tok + off, sq.lk - 1) : sq.lk - 1) : -1;
         }
     };
-    auto store = [&](char *b) {
-        sqs.store(b, tid);
-        sgs.store(b + C::kTileBytes, tid);
+    auto store = [&](int buf) {
         if (tid < C::BR) {
-            float *f = (float *)(b + 2 * C::kTileBytes);
+            float *f = (float *)(lds + 4 * C::kTileBytes + buf * C::kStats);
             f[tid] = st_lse;
             f[C::BR + tid] = st_del;
             ((int *)f)[2 * C::BR + tid] = st_last;
         }
     };
+    zero_pad(lds, C::kLds, p.D, DP, tid);
     if (row_beg < row_end) {
-        load(row_beg);
-        store(lds);
+        tq.offsets_packed(p.qt, p.qh, 0, p.grp, C::BR, wave, lane);
+        tg.offsets_packed(p.dot, p.doh, 0, p.grp, C::BR, wave, lane);
+        load(row_beg, 0);
+        store(0);
     }
     int buf = 0;
     const int wave_last = (int)key_wg + wave * 32 + 31;  // the wave's last key
     for (int64_t r0 = row_beg; r0 < row_end; r0 += C::BR) {
+        dma_wait();
         __syncthreads();
         const bool more = r0 + C::BR < row_end;
-        if (more) load(r0 + C::BR);
-        const char *b = lds + buf * C::kBuf;
-        const float *f = (const float *)(b + 2 * C::kTileBytes);
+        if (more) load(r0 + C::BR, buf ^ 1);
+        const uint32_t qt = lds0 + 2 * buf * C::kTileBytes, gt = qt + C::kTileBytes, stats = lds0 + 4 * C::kTileBytes + buf * C::kStats;
         // rows see a prefix of the keys, longer for later rows: the tile's first row decides
-        const bool whole = uniform(((const int *)f)[2 * C::BR]) >= wave_last && r0 + C::BR <= row_end;
-        if (whole)
-            dkv_block<E, DP, C::NRB, false>(dk, dv, kf, vf, b, b + C::kTileBytes, f, f + C::BR, (const int *)f + 2 * C::BR, c, key, lane);
-        else
-            dkv_block<E, DP, C::NRB, true>(dk, dv, kf, vf, b, b + C::kTileBytes, f, f + C::BR, (const int *)f + 2 * C::BR, c, key, lane);
-        if (more) store(lds + (buf ^ 1) * C::kBuf);
+        const bool whole = uniform(TL::template lds_at<int>(stats + 2 * C::BR * 4)) >= wave_last && r0 + C::BR <= row_end;
+        dkv_block<E, DP, C::NRB>(dk, dv, kf, vf, L, qt, gt, stats, c, !whole, key, h);
+        if (more) store(buf ^ 1);
         buf ^= 1;
     }
     if (key < sq.lk_slot) {  // keys beyond the sequence's length in its slot get zeros

@@ -16,29 +16,31 @@ struct FwdState {
     float m, l;  // m: running maximum in log2 units (scaled); l: this lane's half of the sum
 };
 
-// One 32 x 32 NKB block of keys against a wave's 32 columns. lim: last key (within the tile) the column may
-// see; MASK: some key of the tile is beyond some column's lim.
-template <class E, int DP, int NKB, bool MASK>
-__device__ __forceinline__ void fwd_block(FwdState<E, DP> &st, const uint4 *qf, const char *kt, const char *vt, float c,
-                                          int lim, int lane) {
+// One tile of 32 NKB keys against a wave's 32 columns. lim: last key (within the tile) the column may see;
+// masked: some key of the tile is beyond some column's lim. (The test wraps the masking alone: accumulators that
+// two branches write cost a second set of registers.)
+template <class E, int DP, int NKB>
+__device__ __forceinline__ void fwd_block(FwdState<E, DP> &st, const uint4 *qf, const typename Tile<E, DP>::Lane &L, uint32_t kt,
+                                          uint32_t vt, float c, bool masked, int lim, int h) {
     typedef Tile<E, DP> TL;
-    const int h = lane >> 5, l32 = lane & 31;
     f32x16 s[NKB];
 #pragma unroll
     for (int kb = 0; kb < NKB; ++kb) {
+        s[kb] = zero16();
 #pragma unroll
-        for (int v = 0; v < 16; ++v) s[kb][v] = 0.0f;
+        for (int t = 0; t < TL::kSteps; ++t) s[kb] = mma_frag<E>(TL::row_frag(kt, L, kb, t), qf[t], s[kb]);
+    }
+    if (masked) {
 #pragma unroll
-        for (int t = 0; t < TL::kSteps; ++t) s[kb] = mma_frag<E>(TL::row_frag(kt, 32 * kb + l32, t, h), qf[t], s[kb]);
+        for (int kb = 0; kb < NKB; ++kb)
+#pragma unroll
+            for (int v = 0; v < 16; ++v) s[kb][v] = 32 * kb + d_row(v, 0) <= lim - 4 * h ? s[kb][v] : -INFINITY;
     }
     float mx = -INFINITY;
 #pragma unroll
     for (int kb = 0; kb < NKB; ++kb)
 #pragma unroll
-        for (int v = 0; v < 16; ++v) {
-            if constexpr (MASK) s[kb][v] = 32 * kb + d_row(v, h) <= lim ? s[kb][v] : -INFINITY;
-            mx = fmaxf(mx, s[kb][v]);
-        }
+        for (int v = 0; v < 16; ++v) mx = fmaxf(mx, s[kb][v]);
     mx = half_max(mx) * c;
     // The maximum is only raised when it grew by more than 8 (in log2 units): a stale one keeps every
     // p <= 2^8, exact in the sums' fp32 and in range of fp16, and saves the pass over the accumulators.
@@ -67,7 +69,7 @@ __device__ __forceinline__ void fwd_block(FwdState<E, DP> &st, const uint4 *qf, 
         for (int f = 0; f < WFrags<E>::NF; ++f)
 #pragma unroll
             for (int db = 0; db < DP / 32; ++db)
-                st.o[db] = mma_frag<E>(TL::col_frag(vt, 32 * kb, f, db, lane), w.f[f], st.o[db]);
+                st.o[db] = mma_frag<E>(TL::col_frag(vt, L, kb, f, db), w.f[f], st.o[db]);
     }
     st.l += sum;
 }
@@ -133,31 +135,32 @@ __global__ void __launch_bounds__(256, __is_same(E, F32) ? 1 : 2) k_attn_fwd(con
 
     const T *kg = (const T *)p.k + sq.k0 * p.kt + hk * p.kh;
     const T *vg = (const T *)p.v + sq.k0 * p.vt + hk * p.vh;
-    Stage<E, DP, C::kStage, 256> sk, sv;
+    TileDma<E, DP, C::BN> dk, dv;
+    const uint32_t lds0 = lds_offset(lds);
+    const typename TL::Lane L = TL::lane_of(lane);
+    auto fetch = [&](int k0, int buf) {
+        const int valid = sq.lk - k0;
+        if (valid < C::BN) {
+            dk.offsets(p.kt, valid, wave, lane);
+            dv.offsets(p.vt, valid, wave, lane);
+        }
+        dk.issue(lds0 + buf * 2 * C::kTileBytes, kg + (int64_t)k0 * p.kt, p.D, wave, lane);
+        dv.issue(lds0 + buf * 2 * C::kTileBytes + C::kTileBytes, vg + (int64_t)k0 * p.vt, p.D, wave, lane);
+    };
+    zero_pad(lds, C::kLds, p.D, DP, tid);
     if (k_beg < k_end) {
-        sk.load(kg + (int64_t)k_beg * p.kt, p.kt, sq.lk - k_beg, p.D, tid);
-        sv.load(vg + (int64_t)k_beg * p.vt, p.vt, sq.lk - k_beg, p.D, tid);
-        sk.store(lds, tid);
-        sv.store(lds + C::kTileBytes, tid);
+        dk.offsets(p.kt, C::BN, wave, lane);
+        dv.offsets(p.vt, C::BN, wave, lane);
+        fetch(k_beg, 0);
     }
     int buf = 0;
     for (int k0 = k_beg; k0 < k_end; k0 += C::BN) {
+        dma_wait();
         __syncthreads();  // this tile is in LDS; the other buffer's readers are done
-        const bool more = k0 + C::BN < k_end;
-        if (more) {
-            sk.load(kg + (int64_t)(k0 + C::BN) * p.kt, p.kt, sq.lk - k0 - C::BN, p.D, tid);
-            sv.load(vg + (int64_t)(k0 + C::BN) * p.vt, p.vt, sq.lk - k0 - C::BN, p.D, tid);
-        }
-        const char *kt = lds + buf * 2 * C::kTileBytes, *vt = kt + C::kTileBytes;
-        if (k0 <= wave_max) {
-            if (k0 + C::BN - 1 <= wave_min) fwd_block<E, DP, C::NKB, false>(st, qf, kt, vt, c, 0, lane);
-            else fwd_block<E, DP, C::NKB, true>(st, qf, kt, vt, c, last - k0, lane);
-        }
-        if (more) {
-            char *nt = lds + (buf ^ 1) * 2 * C::kTileBytes;
-            sk.store(nt, tid);
-            sv.store(nt + C::kTileBytes, tid);
-        }
+        if (k0 + C::BN < k_end) fetch(k0 + C::BN, buf ^ 1);
+        const uint32_t kt = lds0 + buf * 2 * C::kTileBytes, vt = kt + C::kTileBytes;
+        if (k0 <= wave_max)
+            fwd_block<E, DP, C::NKB>(st, qf, L, kt, vt, c, k0 + C::BN - 1 > wave_min, last - k0, h);
         buf ^= 1;
     }
 

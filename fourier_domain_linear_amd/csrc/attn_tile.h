@@ -1,7 +1,11 @@
-// attn_tile.h -- tiles of keys and values through LDS, shared by the forward and the dQ kernel.
+// attn_tile.h -- tiles of keys, values or packed query rows from global memory into LDS, and the stores of
+// results, shared by the attention kernels.
 #pragma once
 
 #include "attn.h"
+
+// m0 is written and used inside one asm statement
+#pragma clang diagnostic ignored "-Winline-asm"
 
 namespace eqlin {
 
@@ -15,33 +19,71 @@ struct TileCfg {
     static constexpr int BN = 32 * NKB;
     static constexpr int kTileBytes = BN * TL::kRow;
     static constexpr int kLds = 4 * kTileBytes;                // k and v, two buffers
-    static constexpr int kStage = kTileBytes / 16 / (64 * kWaves);  // 16-byte chunks a thread stages per tile
-    static_assert(kTileBytes % (16 * 64 * kWaves) == 0, "whole chunks");
+    static_assert(kLds <= 65536, "tiles in the first 64 KB");
 };
 
-// One tile of `rows` x D elements (row stride in elements) from global memory, in 16-byte chunks; rows from
-// `valid` on and columns from D on read as zero.
-template <class E, int DP, int N, int THREADS>
-struct Stage {
+// LDS offset (bytes) of a pointer into the workgroup's LDS.
+__device__ __forceinline__ uint32_t lds_offset(const char *p) {
+    return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const char *)p;
+}
+
+// 1 KB from global memory straight into LDS: lane l's 16 bytes at base + off go to lds + 16 l. The compiler does
+// not see these loads (it would wait for them before every later LDS read): dma_wait() before the barrier that
+// publishes them. m0 carries 16 bits of the LDS address here, so tiles lie in the first 64 KB; the wait states
+// are those of a scalar base that a vector instruction has just written, which the compiler cannot count inside asm.
+__device__ __forceinline__ void dma_1k(uint32_t lds, const void *base, uint32_t off) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(base) : "memory", "m0");
+}
+__device__ __forceinline__ void dma_wait() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+
+// A tile of ROWS rows, moved by the workgroup's WAVES waves. Chunks are permuted on the way (a lane fetches the
+// chunk that the swizzle puts at its place). Rows past the last valid one repeat it; columns from D on are
+// not written (zero_pad clears them once).
+template <class E, int DP, int ROWS, int WAVES = 4>
+struct TileDma {
     typedef Tile<E, DP> TL;
     typedef typename ElemOf<E>::type T;
-    uint4 r[N];
-    __device__ __forceinline__ void load(const T *base, int64_t stride, int valid, int D, int tid) {
+    static constexpr int N = ROWS * TL::kRow / (1024 * WAVES);
+    static_assert(ROWS * TL::kRow % (1024 * WAVES) == 0, "whole kilobytes");
+    uint32_t off[N];
+    __device__ static __forceinline__ int place(int wave, int lane, int j) { return (j * WAVES + wave) * 1024 + lane * 16; }
+    __device__ static __forceinline__ int row_of(int wave, int lane, int j) { return place(wave, lane, j) / TL::kRow; }
+    __device__ static __forceinline__ int col_of(int wave, int lane, int j) {  // first element of the chunk
+        const int at = place(wave, lane, j);
+        return (((at % TL::kRow) >> 4) ^ TL::swz(at / TL::kRow)) * (16 / (int)sizeof(T));
+    }
+    // rows of one stride, `valid` of them (> 0)
+    __device__ __forceinline__ void offsets(int64_t stride, int valid, int wave, int lane) {
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+            off[j] = ((uint32_t)min(row_of(wave, lane, j), valid - 1) * (uint32_t)stride + (uint32_t)col_of(wave, lane, j)) * (uint32_t)sizeof(T);
+    }
+    // packed rows: row `rem` + r of the tokens from the base on, head (rem + r) % grp
+    __device__ __forceinline__ void offsets_packed(int64_t ts, int64_t hs, int rem, int grp, int valid, int wave, int lane) {
 #pragma unroll
         for (int j = 0; j < N; ++j) {
-            const int id = tid + j * THREADS, row = id / TL::kChunks, c = id % TL::kChunks;
-            const int col = c * (16 / (int)sizeof(T));
-            r[j] = row < valid && col < D ? *(const uint4 *)(base + row * stride + col) : make_uint4(0, 0, 0, 0);
+            const uint32_t r = (uint32_t)(rem + min(row_of(wave, lane, j), valid - 1)), t = r / (uint32_t)grp, h = r - t * (uint32_t)grp;
+            off[j] = (t * (uint32_t)ts + h * (uint32_t)hs + (uint32_t)col_of(wave, lane, j)) * (uint32_t)sizeof(T);
         }
     }
-    __device__ __forceinline__ void store(char *tile, int tid) const {
+    __device__ __forceinline__ void issue(uint32_t lds, const T *base, int D, int wave, int lane) const {
+        if (D == DP) {
 #pragma unroll
-        for (int j = 0; j < N; ++j) {
-            const int id = tid + j * THREADS, row = id / TL::kChunks, c = id % TL::kChunks;
-            *(uint4 *)(tile + TL::at(row, c)) = r[j];
+            for (int j = 0; j < N; ++j) dma_1k(lds + (j * WAVES + wave) * 1024, base, off[j]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < N; ++j)
+                if (col_of(wave, lane, j) < D) dma_1k(lds + (j * WAVES + wave) * 1024, base, off[j]);
         }
     }
 };
+
+// Clears LDS where heads are padded to DP: the columns from D on stay zero.
+__device__ __forceinline__ void zero_pad(char *lds, int bytes, int D, int DP, int tid) {
+    if (D == DP) return;
+    for (int i = tid * 16; i < bytes; i += 256 * 16) *(uint4 *)(lds + i) = make_uint4(0, 0, 0, 0);
+    __syncthreads();
+}
 
 // Stores a column's 32 db + d_row(v, h) values (o^T in D layout), scaled, to dst[0..D).
 template <class E, int DP>

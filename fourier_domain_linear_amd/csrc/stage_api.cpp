@@ -105,14 +105,17 @@ eqlin_status_t check_attention(const eqlin_attention_args *a, eqlin::AttnParams 
 }
 
 // a [tokens][heads][dim] tensor's pointer and strides
-eqlin_status_t check_tensor(const void *t, int64_t ts, int64_t hs, int64_t tokens, eqlin_dtype_t dtype, const char *name) {
+eqlin_status_t check_tensor(const void *t, int64_t ts, int64_t hs, int64_t tokens, int heads, eqlin_dtype_t dtype,
+                            const char *name) {
     if (tokens == 0) return EQLIN_OK;
     if (!t) return api_fail(EQLIN_ERR_INVALID_ARG, "null %s", name);
     const int per = dtype == EQLIN_F32 ? 4 : 8;
     if (!aligned(t, 16) || ts % per != 0 || hs % per != 0)
         return api_fail(EQLIN_ERR_INVALID_ARG, "%s must be 16-byte aligned, its strides multiples of %d elements", name, per);
-    if (ts < 0 || hs < 0 || ts > (INT64_C(1) << 40) / 16 || hs > (INT64_C(1) << 40) / 16)
-        return api_fail(EQLIN_ERR_INVALID_ARG, "%s: strides out of range", name);
+    // a tile of up to 64 rows is addressed with 32-bit byte offsets from its first
+    if (ts < 0 || hs < 0) return api_fail(EQLIN_ERR_INVALID_ARG, "%s: negative strides", name);
+    if (ts > (INT64_C(1) << 23) || hs * heads > (INT64_C(1) << 28))
+        return api_fail(EQLIN_ERR_UNSUPPORTED, "%s: token stride beyond 2^23 or heads beyond 2^28 elements", name);
     return EQLIN_OK;
 }
 
@@ -233,10 +236,10 @@ eqlin_status_t eqlin_attention(const eqlin_attention_args *a, void *workspace, s
     eqlin_status_t st = check_attention(a, &p);
     if (st != EQLIN_OK) return st;
     if (a->total_q == 0 || a->batch == 0) return EQLIN_OK;
-    if ((st = check_tensor(a->q, p.qt, p.qh, a->total_q, a->dtype, "q")) != EQLIN_OK) return st;
-    if ((st = check_tensor(a->k, p.kt, p.kh, a->total_k, a->dtype, "k")) != EQLIN_OK) return st;
-    if ((st = check_tensor(a->v, p.vt, p.vh, a->total_k, a->dtype, "v")) != EQLIN_OK) return st;
-    if ((st = check_tensor(a->o, p.ot, p.oh, a->total_q, a->dtype, "o")) != EQLIN_OK) return st;
+    if ((st = check_tensor(a->q, p.qt, p.qh, a->total_q, p.Hq, a->dtype, "q")) != EQLIN_OK) return st;
+    if ((st = check_tensor(a->k, p.kt, p.kh, a->total_k, p.Hkv, a->dtype, "k")) != EQLIN_OK) return st;
+    if ((st = check_tensor(a->v, p.vt, p.vh, a->total_k, p.Hkv, a->dtype, "v")) != EQLIN_OK) return st;
+    if ((st = check_tensor(a->o, p.ot, p.oh, a->total_q, p.Hq, a->dtype, "o")) != EQLIN_OK) return st;
     if (!a->cu_q || !a->cu_k) return api_fail(EQLIN_ERR_INVALID_ARG, "null cu_q or cu_k");
     if (!aligned(a->cu_q, 4) || !aligned(a->cu_k, 4) || !aligned(a->len_k, 4) || !aligned(a->lse, 4))
         return api_fail(EQLIN_ERR_INVALID_ARG, "cu_q, cu_k, len_k or lse misaligned");
@@ -283,7 +286,7 @@ eqlin_status_t eqlin_attention_backward(const eqlin_attention_args *a, const eql
              {g->dk, g->dk_token_stride, g->dk_head_stride, a->total_k, p.Hkv, "dk", true},
              {g->dv, g->dv_token_stride, g->dv_head_stride, a->total_k, p.Hkv, "dv", true}};
     for (const auto &x : t)
-        if ((st = check_tensor(x.t, x.ts, x.hs, x.tokens, a->dtype, x.name)) != EQLIN_OK) return st;
+        if ((st = check_tensor(x.t, x.ts, x.hs, x.tokens, x.heads, a->dtype, x.name)) != EQLIN_OK) return st;
     if (!a->cu_q || !a->cu_k || (a->total_q > 0 && !a->lse)) return api_fail(EQLIN_ERR_INVALID_ARG, "null cu_q, cu_k or lse");
     if (!aligned(a->cu_q, 4) || !aligned(a->cu_k, 4) || !aligned(a->len_k, 4) || !aligned(a->lse, 4))
         return api_fail(EQLIN_ERR_INVALID_ARG, "cu_q, cu_k, len_k or lse misaligned");
