@@ -217,4 +217,23 @@ __device__ __forceinline__ int seq_of_slot(const int *cu, int B, int64_t total, 
     return uniform(lo);
 }
 
+// ---- which tile a workgroup takes ----
+//
+// Workgroups go round-robin over the 8 XCDs, each with an L2 of its own, and the tiles of one sequence and head
+// read the same keys. Units are ordered (run of slots, head, slot of the run) and a run goes to one XCD: short
+// sequences have their tiles in one run, one after the other; long ones (run = 1) go slot by slot over all heads, so
+// that every head's longest causal tiles come first and, with a multiple of 8 heads, a head stays on its XCD.
+constexpr int kXcds = 8;
+__host__ __device__ __forceinline__ int64_t xcd_grid(int64_t slots, int heads, int run) {
+    const int64_t units = (slots + run - 1) / run * run * heads, round = (int64_t)kXcds * run;
+    return (units + round - 1) / round * round;
+}
+// (slot, head) of a workgroup; a slot past the last means none
+__device__ __forceinline__ int64_t xcd_slot(uint32_t wg, int heads, int run, int &head) {
+    const uint32_t x = wg & (kXcds - 1), pos = wg / kXcds, r = pos / (uint32_t)run, k = pos - r * (uint32_t)run;
+    const uint32_t t = r * kXcds + x, g = t / (uint32_t)heads;
+    head = (int)(t - g * (uint32_t)heads);
+    return (int64_t)g * run + k;
+}
+
 }  // namespace eqlin

@@ -81,8 +81,9 @@ __global__ void __launch_bounds__(256, __is_same(E, F32) ? 1 : 2) k_attn_dq(cons
     typedef typename ElemOf<E>::type T;
     extern __shared__ __align__(16) char lds[];
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), h = lane >> 5;
-    const int hk = blockIdx.y;
-    const int64_t slot = blockIdx.x;
+    int hk;
+    const int64_t slot = p.slots - 1 - xcd_slot(blockIdx.x, p.Hkv, p.run, hk);  // causal: a sequence's longest rows first
+    if (slot < 0) return;
     const int i = seq_of_slot(p.cu_q, p.B, p.total_q, p.grp, C::BM, slot);
     const Seq sq = seq_at(p, i);
     const int64_t row_end = (int64_t)sq.lq * p.grp;
@@ -222,7 +223,6 @@ struct DkvCfg {
     static constexpr int kTileBytes = BR * TL::kRow;
     static constexpr int kStats = 3 * BR * 4;                    // lse, delta, last key of each row
     static constexpr int kLds = 4 * kTileBytes + 2 * kStats;     // q and dO, two buffers; then the rows' values
-    static_assert(4 * kTileBytes <= 65536, "tiles in the first 64 KB");
 };
 
 template <class E, int DP>
@@ -232,8 +232,9 @@ __global__ void __launch_bounds__(256, __is_same(E, F32) || DP > 64 ? 1 : 2) k_a
     typedef typename ElemOf<E>::type T;
     extern __shared__ __align__(16) char lds[];
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), h = lane >> 5;
-    const int hk = blockIdx.y;
-    const int64_t slot = blockIdx.x;
+    int hk;
+    const int64_t slot = xcd_slot(blockIdx.x, p.Hkv, p.run, hk);  // causal: a sequence's first keys have most rows
+    if (slot >= p.slots) return;
     const int i = seq_of_slot(p.cu_k, p.B, p.total_k, 1, C::BK, slot);
     const Seq sq = seq_at(p, i);
     const int64_t key_wg = (slot - slot_start(p.cu_k, i, p.total_k, 1, C::BK)) * C::BK;
@@ -332,7 +333,8 @@ hipError_t set_lds(K kernel, int bytes) {
 }
 
 template <class E, int DP>
-hipError_t run_bwd(const AttnParams &p, hipStream_t s) {
+hipError_t run_bwd(const AttnParams &p0, hipStream_t s) {
+    AttnParams p = p0;
     typedef TileCfg<E, DP> CQ;
     typedef DkvCfg<E, DP> CK;
     hipError_t e = set_lds(k_attn_dq<E, DP>, CQ::kLds);
@@ -340,10 +342,15 @@ hipError_t run_bwd(const AttnParams &p, hipStream_t s) {
     if (e != hipSuccess) return e;
     if (p.total_q > 0) {
         hipLaunchKernelGGL((k_attn_delta<E>), dim3((unsigned)std::min<int64_t>((p.total_q * p.Hq + 15) / 16, 1 << 20)), dim3(256), 0, s, p);
-        hipLaunchKernelGGL((k_attn_dq<E, DP>), dim3((unsigned)(p.total_q * p.grp / CQ::BM + p.B), p.Hkv), dim3(256), CQ::kLds, s, p);
+        p.slots = p.total_q * p.grp / CQ::BM + p.B;
+        p.run = run_of(p.slots, p.B);
+        hipLaunchKernelGGL((k_attn_dq<E, DP>), dim3((unsigned)xcd_grid(p.slots, p.Hkv, p.run)), dim3(256), CQ::kLds, s, p);
     }
-    if (p.total_k > 0)
-        hipLaunchKernelGGL((k_attn_dkv<E, DP>), dim3((unsigned)(p.total_k / CK::BK + p.B), p.Hkv), dim3(256), CK::kLds, s, p);
+    if (p.total_k > 0) {
+        p.slots = p.total_k / CK::BK + p.B;
+        p.run = run_of(p.slots, p.B);
+        hipLaunchKernelGGL((k_attn_dkv<E, DP>), dim3((unsigned)xcd_grid(p.slots, p.Hkv, p.run)), dim3(256), CK::kLds, s, p);
+    }
     return hipGetLastError();
 }
 

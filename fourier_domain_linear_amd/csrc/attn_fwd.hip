@@ -81,8 +81,9 @@ __global__ void __launch_bounds__(256, __is_same(E, F32) ? 1 : 2) k_attn_fwd(con
     typedef typename ElemOf<E>::type T;
     extern __shared__ __align__(16) char lds[];
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), h = lane >> 5;
-    const int hk = blockIdx.y;
-    const int64_t slot = blockIdx.x;
+    int hk;
+    const int64_t slot = p.slots - 1 - xcd_slot(blockIdx.x, p.Hkv, p.run, hk);  // causal: a sequence's longest rows first
+    if (slot < 0) return;
     const int i = seq_of_slot(p.cu_q, p.B, p.total_q, p.grp, C::BM, slot);
     const Seq sq = seq_at(p, i);
     const int64_t row_end = (int64_t)sq.lq * p.grp;
@@ -219,14 +220,16 @@ __global__ void __launch_bounds__(256) k_attn_join(const AttnParams p) {
 }
 
 template <class E, int DP>
-hipError_t run_fwd(const AttnParams &p, hipStream_t s) {
+hipError_t run_fwd(const AttnParams &p0, hipStream_t s) {
     typedef TileCfg<E, DP> C;
-    const int64_t slots = p.total_q * p.grp / C::BM + p.B;
+    AttnParams p = p0;
+    p.slots = p.total_q * p.grp / C::BM + p.B;
+    p.run = run_of(p.slots, p.B);
     if (C::kLds > 64 * 1024) {
         hipError_t e = hipFuncSetAttribute((const void *)k_attn_fwd<E, DP>, hipFuncAttributeMaxDynamicSharedMemorySize, C::kLds);
         if (e != hipSuccess) return e;
     }
-    hipLaunchKernelGGL((k_attn_fwd<E, DP>), dim3((unsigned)slots, p.Hkv, p.nsplit), dim3(256), C::kLds, s, p);
+    hipLaunchKernelGGL((k_attn_fwd<E, DP>), dim3((unsigned)xcd_grid(p.slots, p.Hkv, p.run), 1, p.nsplit), dim3(256), C::kLds, s, p);
     if (p.nsplit > 1) {
         const int64_t rows = p.total_q * p.Hq;
         hipLaunchKernelGGL((k_attn_join<E>), dim3((unsigned)std::min<int64_t>((rows + 3) / 4, 1 << 20)), dim3(256), 0, s, p);

@@ -19,8 +19,10 @@ struct TileCfg {
     static constexpr int BN = 32 * NKB;
     static constexpr int kTileBytes = BN * TL::kRow;
     static constexpr int kLds = 4 * kTileBytes;                // k and v, two buffers
-    static_assert(kLds <= 65536, "tiles in the first 64 KB");
 };
+
+// Units an XCD takes in a run: the tiles of a sequence where they are few, else one.
+inline int run_of(int64_t slots, int B) { return slots > 16 * (int64_t)B ? 1 : (int)std::max<int64_t>(1, (slots + B - 1) / B); }
 
 // LDS offset (bytes) of a pointer into the workgroup's LDS.
 __device__ __forceinline__ uint32_t lds_offset(const char *p) {
@@ -29,8 +31,8 @@ __device__ __forceinline__ uint32_t lds_offset(const char *p) {
 
 // 1 KB from global memory straight into LDS: lane l's 16 bytes at base + off go to lds + 16 l. The compiler does
 // not see these loads (it would wait for them before every later LDS read): dma_wait() before the barrier that
-// publishes them. m0 carries 16 bits of the LDS address here, so tiles lie in the first 64 KB; the wait states
-// are those of a scalar base that a vector instruction has just written, which the compiler cannot count inside asm.
+// publishes them. The wait states are those of a scalar base that a vector instruction has just written, which the
+// compiler cannot count inside asm.
 __device__ __forceinline__ void dma_1k(uint32_t lds, const void *base, uint32_t off) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(base) : "memory", "m0");
 }

@@ -202,6 +202,8 @@ struct AttnParams {
     float *ws;   // workspace
     int chunk;   // keys a workgroup of the split kernel takes (0: not split)
     int nsplit;  // key ranges the tile kernel's rows are split into
+    int64_t slots;  // tile slots of a launch (a sequence's, then the next one's), and units a run of an XCD
+    int run;
 };
 size_t attention_workspace_bytes(const AttnParams &p, eqlin_dtype_t dtype);
 hipError_t launch_attention(const AttnParams &p, eqlin_dtype_t dtype, hipStream_t s);

@@ -87,10 +87,9 @@ eqlin_status_t check_attention(const eqlin_attention_args *a, eqlin::AttnParams 
     if (a->dim > 128 || a->dim % per != 0)
         return api_fail(EQLIN_ERR_UNSUPPORTED, "dim = %d: a multiple of %d up to 128", a->dim, per);
     if (!(a->scale > 0.0f) || isinf(a->scale)) return api_fail(EQLIN_ERR_INVALID_ARG, "scale must be finite and > 0");
-    const int64_t most = INT64_C(0x7fffffff) - 4096;
-    if (a->total_q > most || a->total_k > most) return api_fail(EQLIN_ERR_UNSUPPORTED, "total_q or total_k beyond 2^31");
-    if (a->total_q > (1 << 30) / a->heads_q || a->batch > (1 << 22))  // the launch's index range
-        return api_fail(EQLIN_ERR_UNSUPPORTED, "total_q * heads_q beyond 2^30 or batch beyond 2^22");
+    // the launches' index range (at most 2^24 workgroups)
+    if (a->total_q > (1 << 29) / a->heads_q || a->total_k > (1 << 29) / a->heads_kv || a->batch > (1 << 21) / a->heads_kv)
+        return api_fail(EQLIN_ERR_UNSUPPORTED, "total_q * heads_q or total_k * heads_kv beyond 2^29, or batch * heads_kv beyond 2^21");
     if (a->heads_kv > 65535) return api_fail(EQLIN_ERR_UNSUPPORTED, "heads_kv = %d beyond 65535", a->heads_kv);
     *p = eqlin::AttnParams{};
     p->q = a->q, p->k = a->k, p->v = a->v, p->o = a->o, p->lse = a->lse;

@@ -380,7 +380,8 @@ eqlin_status_t eqlin_rotary(const void *x, int64_t x_token_stride, int64_t x_hea
  *   len_k        device int32 [batch] or NULL: how many keys of sequence i's stretch of cu_k count (a cache
  *                with room to grow).
  *   lse          device float [total_q][heads_q] or NULL (the backward needs it).
- *   scale        > 0, finite.   batch in 0..2^22; total_k < 2^31 - 4096, total_q * heads_q <= 2^30.
+ *   scale        > 0, finite.   batch * heads_kv <= 2^21; total_q * heads_q and
+ *                total_k * heads_kv <= 2^29 (else UNSUPPORTED).
  * Products and sums in fp32; the half types round the unnormalised probabilities (at most 2^8) to the type
  * for the second product.
  *   workspace    eqlin_attention_workspace(a) bytes, 256-byte aligned (NULL when that is 0): partial results
