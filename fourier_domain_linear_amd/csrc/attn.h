@@ -172,6 +172,20 @@ __device__ __forceinline__ int64_t uniform(int64_t x) {
 // D-layout row of value v for lane half h
 __device__ __forceinline__ constexpr int d_row(int v, int h) { return (v & 3) + 8 * (v >> 2) + 4 * h; }
 
+// Order of a block that multiplies LDS fragments: AHEAD reads first, then one read a product, so that no product
+// waits for its own read (left alone, the compiler reuses one register quad: read, wait, multiply).
+template <int READS, int PRODUCTS, int AHEAD>
+__device__ __forceinline__ void read_ahead() {
+    constexpr int kRead = 0x100, kMfma = 0x8, kPer = PRODUCTS / READS > 0 ? PRODUCTS / READS : 1;
+    __builtin_amdgcn_sched_group_barrier(kRead, AHEAD, 0);
+#pragma unroll
+    for (int i = 0; i < READS - AHEAD; ++i) {
+        __builtin_amdgcn_sched_group_barrier(kMfma, kPer, 0);
+        __builtin_amdgcn_sched_group_barrier(kRead, 1, 0);
+    }
+    __builtin_amdgcn_sched_group_barrier(kMfma, PRODUCTS - kPer * (READS - AHEAD), 0);
+}
+
 // ---- sequences ----
 
 struct Seq {
@@ -182,39 +196,47 @@ struct Seq {
 
 __device__ __forceinline__ int64_t clamp64(int64_t x, int64_t lo, int64_t hi) { return x < lo ? lo : x > hi ? hi : x; }
 
-// Sequence i, with every bound forced into the tensors whatever the arrays hold.
-__device__ __forceinline__ Seq seq_at(const AttnParams &p, int i) {
-    Seq s;
-    s.q0 = clamp64(p.cu_q[i], 0, p.total_q);
-    s.lq = (int)(clamp64(p.cu_q[i + 1], s.q0, p.total_q) - s.q0);
-    s.k0 = clamp64(p.cu_k[i], 0, p.total_k);
-    s.lk_slot = (int)(clamp64(p.cu_k[i + 1], s.k0, p.total_k) - s.k0);
-    s.lk = p.len_k ? (int)clamp64(p.len_k[i], 0, s.lk_slot) : s.lk_slot;
-    s.q0 = uniform(s.q0), s.k0 = uniform(s.k0);
-    s.lq = uniform(s.lq), s.lk = uniform(s.lk), s.lk_slot = uniform(s.lk_slot);
-    return s;
-}
-
 // Tiles of `size` units over sequences of cu[i + 1] - cu[i] items of `mul` units: sequence i owns the tile
 // slots from cu[i] * mul / size + i on, at least as many as it has tiles, so the launch needs no lengths on
-// the host. Finds the sequence of a slot with a 64-way search by the wave, one load a level.
-__device__ __forceinline__ int64_t slot_start(const int *cu, int i, int64_t total, int mul, int size) {
-    return clamp64(cu[i], 0, total) * mul / size + i;
-}
-__device__ __forceinline__ int seq_of_slot(const int *cu, int B, int64_t total, int mul, int size, int64_t slot) {
+// the host.
+__device__ __forceinline__ int64_t slot_start(int64_t cu, int i, int mul, int size) { return cu * mul / size + i; }
+
+// The sequence of a slot and the slot's tile in it, by a 64-way search of the wave. The last level's lanes load
+// all that is asked of a sequence at once, so up to 64 sequences cost one round trip to memory. Every bound
+// is forced into the tensors whatever the arrays hold. BY_K: slots over the keys, else over the queries.
+template <bool BY_K>
+__device__ __forceinline__ Seq seq_of_slot(const AttnParams &p, int mul, int size, int64_t slot, int64_t &tile) {
     const int lane = threadIdx.x & 63;
-    int lo = 0, n = B;
-    while (n > 1) {
+    const int *cu = BY_K ? p.cu_k : p.cu_q;
+    const int64_t total = BY_K ? p.total_k : p.total_q;
+    int lo = 0, n = p.B;
+    while (n > 64) {
         const int step = (n + 63) / 64;
         const int i = lo + lane * step;
-        const bool in = lane * step < n && slot_start(cu, i, total, mul, size) <= slot;
+        const bool in = lane * step < n && slot_start(clamp64(cu[i < p.B ? i : p.B], 0, total), i, mul, size) <= slot;
         int c = __popcll(__ballot(in));
         c = c < 1 ? 1 : c;
         const int skip = (c - 1) * step;
         lo += skip;
         n = n - skip < step ? n - skip : step;
     }
-    return uniform(lo);
+    const int i = lo + (lane < n ? lane : n - 1);
+    const int q0 = p.cu_q[i], q1 = p.cu_q[i + 1], k0 = p.cu_k[i], k1 = p.cu_k[i + 1], len = p.len_k ? p.len_k[i] : 0x7fffffff;
+    const bool in = lane < n && slot_start(clamp64(BY_K ? k0 : q0, 0, total), i, mul, size) <= slot;
+    int c = __popcll(__ballot(in));
+    c = uniform(c < 1 ? 0 : c - 1);
+    const int uq0 = __builtin_amdgcn_readlane(q0, c), uq1 = __builtin_amdgcn_readlane(q1, c);
+    const int uk0 = __builtin_amdgcn_readlane(k0, c), uk1 = __builtin_amdgcn_readlane(k1, c);
+    const int ulen = __builtin_amdgcn_readlane(len, c);
+    auto clamp = [](int x, int lo, int hi) { return min(max(x, lo), hi); };
+    Seq s;
+    const int q_at = clamp(uq0, 0, (int)p.total_q), k_at = clamp(uk0, 0, (int)p.total_k);
+    s.q0 = q_at, s.k0 = k_at;
+    s.lq = clamp(uq1, q_at, (int)p.total_q) - q_at;
+    s.lk_slot = clamp(uk1, k_at, (int)p.total_k) - k_at;
+    s.lk = clamp(ulen, 0, s.lk_slot);
+    tile = slot - slot_start(BY_K ? s.k0 : s.q0, uniform(lo) + c, mul, size);
+    return s;
 }
 
 // ---- which tile a workgroup takes ----

@@ -84,10 +84,9 @@ __global__ void __launch_bounds__(256, __is_same(E, F32) ? 1 : 2) k_attn_dq(cons
     int hk;
     const int64_t slot = p.slots - 1 - xcd_slot(blockIdx.x, p.Hkv, p.run, hk);  // causal: a sequence's longest rows first
     if (slot < 0) return;
-    const int i = seq_of_slot(p.cu_q, p.B, p.total_q, p.grp, C::BM, slot);
-    const Seq sq = seq_at(p, i);
-    const int64_t row_end = (int64_t)sq.lq * p.grp;
-    const int64_t row_wg = (slot - slot_start(p.cu_q, i, p.total_q, p.grp, C::BM)) * C::BM;
+    int64_t tile;
+    const Seq sq = seq_of_slot<false>(p, p.grp, C::BM, slot, tile);
+    const int64_t row_end = (int64_t)sq.lq * p.grp, row_wg = tile * C::BM;
     if (row_wg < 0 || row_wg >= row_end) return;
     const int off = sq.lk - sq.lq;
     const int64_t row = row_wg + wave * 32 + (lane & 31);
@@ -235,9 +234,9 @@ __global__ void __launch_bounds__(256, __is_same(E, F32) || DP > 64 ? 1 : 2) k_a
     int hk;
     const int64_t slot = xcd_slot(blockIdx.x, p.Hkv, p.run, hk);  // causal: a sequence's first keys have most rows
     if (slot >= p.slots) return;
-    const int i = seq_of_slot(p.cu_k, p.B, p.total_k, 1, C::BK, slot);
-    const Seq sq = seq_at(p, i);
-    const int64_t key_wg = (slot - slot_start(p.cu_k, i, p.total_k, 1, C::BK)) * C::BK;
+    int64_t tile;
+    const Seq sq = seq_of_slot<true>(p, 1, C::BK, slot, tile);
+    const int64_t key_wg = tile * C::BK;
     if (key_wg < 0 || key_wg >= sq.lk_slot) return;
     const int off = sq.lk - sq.lq;
     const int key = (int)key_wg + wave * 32 + (lane & 31);

@@ -9,6 +9,23 @@ namespace {
 
 // ---- the tile kernel: 4 waves, each 32 packed rows (the columns of S^T), all over the same key tiles ----
 
+// Two shapes at DP = 128 in the half types. 64-key tiles at two waves a SIMD read V's fragments ahead of the
+// exponentials and pay the running maximum once for 64 keys (4 x 4096 tokens, 16 heads: 562 us, against 581 for the
+// other). Over few keys the launch is bound by each workgroup's chain of loads instead, and 32-key tiles, whose 16
+// score registers less let three waves share a SIMD, are faster (64 x 196 tokens, 16 heads: 62 us against 71).
+template <class E, int DP, bool SHORT>
+struct FwdCfg {
+    typedef Tile<E, DP> TL;
+    static constexpr bool kSmall = SHORT && DP == 128;
+    static constexpr int BM = 128;                                              // packed rows of a workgroup
+    static constexpr int NKB = __is_same(E, F32) || kSmall ? 1 : 2;             // 32-key blocks of a tile
+    static constexpr int BN = 32 * NKB;
+    static constexpr int WPE = __is_same(E, F32) ? 1 : kSmall ? 3 : 2;          // waves a SIMD the registers allow
+    static constexpr int kTileBytes = BN * TL::kRow;
+    static constexpr int kLds = 4 * kTileBytes;                                 // k and v, two buffers
+};
+constexpr int64_t kShortKeys = 512;  // keys a sequence on average up to which SHORT is taken
+
 // Running softmax state of a lane's column and its O^T accumulators.
 template <class E, int DP>
 struct FwdState {
@@ -30,6 +47,7 @@ __device__ __forceinline__ void fwd_block(FwdState<E, DP> &st, const uint4 *qf, 
 #pragma unroll
         for (int t = 0; t < TL::kSteps; ++t) s[kb] = mma_frag<E>(TL::row_frag(kt, L, kb, t), qf[t], s[kb]);
     }
+    if constexpr (!__is_same(E, F32) && DP == 128) read_ahead<NKB * TL::kSteps, NKB * TL::kSteps, NKB == 1 ? 4 : 6>();
     if (masked) {
 #pragma unroll
         for (int kb = 0; kb < NKB; ++kb)
@@ -74,9 +92,9 @@ __device__ __forceinline__ void fwd_block(FwdState<E, DP> &st, const uint4 *qf, 
     st.l += sum;
 }
 
-template <class E, int DP>
-__global__ void __launch_bounds__(256, __is_same(E, F32) ? 1 : 2) k_attn_fwd(const AttnParams p) {
-    typedef TileCfg<E, DP> C;
+template <class E, int DP, bool SHORT>
+__global__ void __launch_bounds__(256, (FwdCfg<E, DP, SHORT>::WPE)) k_attn_fwd(const AttnParams p) {
+    typedef FwdCfg<E, DP, SHORT> C;
     typedef Tile<E, DP> TL;
     typedef typename ElemOf<E>::type T;
     extern __shared__ __align__(16) char lds[];
@@ -84,10 +102,9 @@ __global__ void __launch_bounds__(256, __is_same(E, F32) ? 1 : 2) k_attn_fwd(con
     int hk;
     const int64_t slot = p.slots - 1 - xcd_slot(blockIdx.x, p.Hkv, p.run, hk);  // causal: a sequence's longest rows first
     if (slot < 0) return;
-    const int i = seq_of_slot(p.cu_q, p.B, p.total_q, p.grp, C::BM, slot);
-    const Seq sq = seq_at(p, i);
-    const int64_t row_end = (int64_t)sq.lq * p.grp;
-    const int64_t row_wg = (slot - slot_start(p.cu_q, i, p.total_q, p.grp, C::BM)) * C::BM;
+    int64_t tile;
+    const Seq sq = seq_of_slot<false>(p, p.grp, C::BM, slot, tile);
+    const int64_t row_end = (int64_t)sq.lq * p.grp, row_wg = tile * C::BM;
     if (row_wg < 0 || row_wg >= row_end) return;
     const int off = sq.lk - sq.lq;  // causal: token t sees keys up to t + off
 
@@ -149,20 +166,29 @@ __global__ void __launch_bounds__(256, __is_same(E, F32) ? 1 : 2) k_attn_fwd(con
         dv.issue(lds0 + buf * 2 * C::kTileBytes + C::kTileBytes, vg + (int64_t)k0 * p.vt, p.D, wave, lane);
     };
     zero_pad(lds, C::kLds, p.D, DP, tid);
-    if (k_beg < k_end) {
-        dk.offsets(p.kt, C::BN, wave, lane);
-        dv.offsets(p.vt, C::BN, wave, lane);
-        fetch(k_beg, 0);
-    }
+    dk.offsets(p.kt, C::BN, wave, lane);
+    dv.offsets(p.vt, C::BN, wave, lane);
+    if (k_beg < k_end) fetch(k_beg, 0);
     int buf = 0;
-    for (int k0 = k_beg; k0 < k_end; k0 += C::BN) {
+    // (a wave without rows or keys fetches its part of the tiles, in a loop of its own)
+    const bool works = wave_max >= k_beg;
+    auto arrive = [&](int k0) {
         dma_wait();
-        __syncthreads();  // this tile is in LDS; the other buffer's readers are done
+        __syncthreads();  // this tile is in LDS; the other buffer has no more readers
         if (k0 + C::BN < k_end) fetch(k0 + C::BN, buf ^ 1);
-        const uint32_t kt = lds0 + buf * 2 * C::kTileBytes, vt = kt + C::kTileBytes;
-        if (k0 <= wave_max)
+    };
+    if (works) {
+        for (int k0 = k_beg; k0 < k_end; k0 += C::BN) {
+            arrive(k0);
+            const uint32_t kt = lds0 + buf * 2 * C::kTileBytes, vt = kt + C::kTileBytes;
             fwd_block<E, DP, C::NKB>(st, qf, L, kt, vt, c, k0 + C::BN - 1 > wave_min, last - k0, h);
-        buf ^= 1;
+            buf ^= 1;
+        }
+    } else {
+        for (int k0 = k_beg; k0 < k_end; k0 += C::BN) {
+            arrive(k0);
+            buf ^= 1;
+        }
     }
 
     const float l = half_sum(st.l);
@@ -219,17 +245,17 @@ __global__ void __launch_bounds__(256) k_attn_join(const AttnParams p) {
     }
 }
 
-template <class E, int DP>
+template <class E, int DP, bool SHORT>
 hipError_t run_fwd(const AttnParams &p0, hipStream_t s) {
-    typedef TileCfg<E, DP> C;
+    typedef FwdCfg<E, DP, SHORT> C;
     AttnParams p = p0;
     p.slots = p.total_q * p.grp / C::BM + p.B;
     p.run = run_of(p.slots, p.B);
     if (C::kLds > 64 * 1024) {
-        hipError_t e = hipFuncSetAttribute((const void *)k_attn_fwd<E, DP>, hipFuncAttributeMaxDynamicSharedMemorySize, C::kLds);
+        hipError_t e = hipFuncSetAttribute((const void *)k_attn_fwd<E, DP, SHORT>, hipFuncAttributeMaxDynamicSharedMemorySize, C::kLds);
         if (e != hipSuccess) return e;
     }
-    hipLaunchKernelGGL((k_attn_fwd<E, DP>), dim3((unsigned)xcd_grid(p.slots, p.Hkv, p.run), 1, p.nsplit), dim3(256), C::kLds, s, p);
+    hipLaunchKernelGGL((k_attn_fwd<E, DP, SHORT>), dim3((unsigned)xcd_grid(p.slots, p.Hkv, p.run), 1, p.nsplit), dim3(256), C::kLds, s, p);
     if (p.nsplit > 1) {
         const int64_t rows = p.total_q * p.Hq;
         hipLaunchKernelGGL((k_attn_join<E>), dim3((unsigned)std::min<int64_t>((rows + 3) / 4, 1 << 20)), dim3(256), 0, s, p);
@@ -239,9 +265,10 @@ hipError_t run_fwd(const AttnParams &p0, hipStream_t s) {
 
 template <class E>
 hipError_t run_fwd_e(const AttnParams &p, hipStream_t s) {
-    if (p.D <= 32) return run_fwd<E, 32>(p, s);
-    if (p.D <= 64) return run_fwd<E, 64>(p, s);
-    return run_fwd<E, 128>(p, s);
+    if (p.D <= 32) return run_fwd<E, 32, false>(p, s);
+    if (p.D <= 64) return run_fwd<E, 64, false>(p, s);
+    if (!__is_same(E, F32) && p.total_k <= kShortKeys * p.B) return run_fwd<E, 128, true>(p, s);
+    return run_fwd<E, 128, false>(p, s);
 }
 
 // Key ranges a launch is split into: enough workgroups for two a compute unit where the rows alone do not

@@ -68,7 +68,8 @@ struct TileDma {
             off[j] = (t * (uint32_t)ts + h * (uint32_t)hs + (uint32_t)col_of(wave, lane, j)) * (uint32_t)sizeof(T);
         }
     }
-    __device__ __forceinline__ void issue(uint32_t lds, const T *base, int D, int wave, int lane) const {
+    __device__ __forceinline__ void issue(uint32_t lds, const T *tile, int D, int wave, int lane) const {
+        const T *base = (const T *)uniform((int64_t)tile);  // into scalar registers
         if (D == DP) {
 #pragma unroll
             for (int j = 0; j < N; ++j) dma_1k(lds + (j * WAVES + wave) * 1024, base, off[j]);
