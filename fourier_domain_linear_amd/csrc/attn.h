@@ -239,6 +239,37 @@ __device__ __forceinline__ Seq seq_of_slot(const AttnParams &p, int mul, int siz
     return s;
 }
 
+// packed row -> token (rows are below 2^31; most groups are powers of two)
+__device__ __forceinline__ int row_token(const AttnParams &p, int row) {
+    return p.lgrp >= 0 ? row >> p.lgrp : (int)((uint32_t)row / (uint32_t)p.grp);
+}
+
+// The packed rows of one wave (32 columns) of a row tile: this lane's row, and the keys its rows see.
+struct Rows {
+    bool live;
+    int tok, hq;         // token in the sequence, query head (of a row past the end: the last one's)
+    int last;            // last key this lane's row sees, -1: none
+    int wave_min;        // the least `last` of the wave's live rows: tiles wholly up to it need no mask
+    int wave_max;        // the largest, -1: the wave has no work
+    int k_end;           // keys that some row of the workgroup sees
+};
+__device__ __forceinline__ Rows rows_of(const AttnParams &p, const Seq &sq, int hk, int row_wg, int BM, int wave, int lane) {
+    Rows r;
+    const int end = sq.lq * p.grp, off = sq.lk - sq.lq;
+    auto last_of = [&](int row) { return p.causal ? max(-1, min(row_token(p, row) + off, sq.lk - 1)) : sq.lk - 1; };
+    const int first = row_wg + wave * 32, row = first + (lane & 31), at = min(row, end - 1);
+    r.live = row < end;
+    r.tok = row_token(p, at);
+    r.hq = hk * p.grp + (at - r.tok * p.grp);
+    r.last = !r.live ? -1 : p.causal ? max(-1, min(r.tok + off, sq.lk - 1)) : sq.lk - 1;
+    // rows see longer and longer prefixes, so the wave's ends decide
+    r.wave_min = first < end ? last_of(first) : -1;
+    if (first + 32 > end) r.wave_min = -1;  // rows past the end see nothing
+    r.wave_max = first < end ? last_of(min(first + 31, end - 1)) : -1;
+    r.k_end = last_of(min(row_wg + BM, end) - 1) + 1;
+    return r;
+}
+
 // ---- which tile a workgroup takes ----
 //
 // Workgroups go round-robin over the 8 XCDs, each with an L2 of its own, and the tiles of one sequence and head

@@ -86,49 +86,13 @@ __global__ void __launch_bounds__(256, __is_same(E, F32) ? 1 : 2) k_attn_dq(cons
     if (slot < 0) return;
     int64_t tile;
     const Seq sq = seq_of_slot<false>(p, p.grp, C::BM, slot, tile);
-    const int64_t row_end = (int64_t)sq.lq * p.grp, row_wg = tile * C::BM;
-    if (row_wg < 0 || row_wg >= row_end) return;
-    const int off = sq.lk - sq.lq;
-    const int64_t row = row_wg + wave * 32 + (lane & 31);
-    const bool live = row < row_end;
-    const int tok = live ? (int)((uint32_t)row / (uint32_t)p.grp) : 0;
-    const int hq = hk * p.grp + (live ? (int)((uint32_t)row - (uint32_t)tok * (uint32_t)p.grp) : 0);
-    const int64_t at = (sq.q0 + tok) * p.Hq + hq;
-    uint4 qf[TL::kSteps], gf[TL::kSteps];
-    {
-        const T *q = (const T *)p.q + (sq.q0 + tok) * p.qt + hq * p.qh;
-        const T *g = (const T *)p.dout + (sq.q0 + tok) * p.dot + hq * p.doh;
-#pragma unroll
-        for (int t = 0; t < TL::kSteps; ++t) {
-            const int col = (2 * t + h) * (16 / (int)sizeof(T));
-            const bool in = live && col < p.D;
-            qf[t] = in ? *(const uint4 *)(q + col) : make_uint4(0, 0, 0, 0);
-            gf[t] = in ? *(const uint4 *)(g + col) : make_uint4(0, 0, 0, 0);
-        }
-    }
-    const float lse2 = live ? p.lse[at] * kLog2e : INFINITY, delta = live ? p.ws[at] : 0.0f;
-    int last = live ? (p.causal ? min(tok + off, sq.lk - 1) : sq.lk - 1) : -1;
-    const int64_t row_last = (row_wg + C::BM < row_end ? row_wg + C::BM : row_end) - 1;
-    const int k_end = p.causal ? min((int)((uint32_t)row_last / (uint32_t)p.grp) + off + 1, sq.lk) : sq.lk;
-    int wave_min = live ? last : 0x7fffffff, wave_max = last;
-#pragma unroll
-    for (int x = 16; x >= 1; x >>= 1) {
-        wave_min = min(wave_min, __shfl_xor(wave_min, x));
-        wave_max = max(wave_max, __shfl_xor(wave_max, x));
-    }
-    wave_min = uniform(wave_min);
-    wave_max = uniform(wave_max);
-    f32x16 dq[DP / 32];
-#pragma unroll
-    for (int db = 0; db < DP / 32; ++db)
-#pragma unroll
-        for (int v = 0; v < 16; ++v) dq[db][v] = 0.0f;
-    const float c = p.scale * kLog2e;
+    const int row_wg = (int)tile * C::BM;
+    if (tile < 0 || row_wg >= sq.lq * p.grp) return;
+    const Rows r = rows_of(p, sq, hk, row_wg, C::BM, wave, lane);
     const T *kg = (const T *)p.k + sq.k0 * p.kt + hk * p.kh;
     const T *vg = (const T *)p.v + sq.k0 * p.vt + hk * p.vh;
     TileDma<E, DP, C::BN> tk, tv;
     const uint32_t lds0 = lds_offset(lds);
-    const typename TL::Lane L = TL::lane_of(lane);
     auto fetch = [&](int k0, int buf) {
         const int valid = sq.lk - k0;
         if (valid < C::BN) {
@@ -139,22 +103,39 @@ __global__ void __launch_bounds__(256, __is_same(E, F32) ? 1 : 2) k_attn_dq(cons
         tv.issue(lds0 + buf * 2 * C::kTileBytes + C::kTileBytes, vg + (int64_t)k0 * p.vt, p.D, wave, lane);
     };
     zero_pad(lds, C::kLds, p.D, DP, tid);
-    if (k_end > 0) {
-        tk.offsets(p.kt, C::BN, wave, lane);
-        tv.offsets(p.vt, C::BN, wave, lane);
-        fetch(0, 0);
-    }
+    tk.offsets(p.kt, C::BN, wave, lane);
+    tv.offsets(p.vt, C::BN, wave, lane);
+    if (r.k_end > 0) fetch(0, 0);
+    const int64_t at = (sq.q0 + r.tok) * p.Hq + r.hq;
+    uint4 qf[TL::kSteps], gf[TL::kSteps];
+    load_row<E, DP>(qf, (const T *)p.q + (sq.q0 + r.tok) * p.qt + r.hq * p.qh, p.D, h);
+    load_row<E, DP>(gf, (const T *)p.dout + (sq.q0 + r.tok) * p.dot + r.hq * p.doh, p.D, h);
+    const float lse2 = p.lse[at] * kLog2e, delta = p.ws[at];
+    f32x16 dq[DP / 32];
+#pragma unroll
+    for (int db = 0; db < DP / 32; ++db) dq[db] = zero16();
+    const float c = p.scale * kLog2e;
+    const typename TL::Lane L = TL::lane_of(lane);
     int buf = 0;
-    for (int k0 = 0; k0 < k_end; k0 += C::BN) {
+    auto arrive = [&](int k0) {
         dma_wait();
-        __syncthreads();  // this tile is in LDS; the other buffer's readers are done
-        if (k0 + C::BN < k_end) fetch(k0 + C::BN, buf ^ 1);
-        const uint32_t kt = lds0 + buf * 2 * C::kTileBytes, vt = kt + C::kTileBytes;
-        if (k0 <= wave_max)
-            dq_block<E, DP, C::NKB>(dq, qf, gf, L, kt, vt, c, lse2, delta, k0 + C::BN - 1 > wave_min, last - k0, h);
-        buf ^= 1;
+        __syncthreads();  // this tile is in LDS; the other buffer has no more readers
+        if (k0 + C::BN < r.k_end) fetch(k0 + C::BN, buf ^ 1);
+    };
+    if (r.wave_max >= 0) {
+        for (int k0 = 0; k0 < r.k_end; k0 += C::BN) {
+            arrive(k0);
+            const uint32_t kt = lds0 + buf * 2 * C::kTileBytes, vt = kt + C::kTileBytes;
+            dq_block<E, DP, C::NKB>(dq, qf, gf, L, kt, vt, c, lse2, delta, k0 + C::BN - 1 > r.wave_min, r.last - k0, h);
+            buf ^= 1;
+        }
+    } else {  // a wave without rows or keys fetches its part of the tiles
+        for (int k0 = 0; k0 < r.k_end; k0 += C::BN) {
+            arrive(k0);
+            buf ^= 1;
+        }
     }
-    if (live) store_column<E, DP>(dq, p.scale, (T *)p.dq + (sq.q0 + tok) * p.dqt + hq * p.dqh, p.D, h);
+    if (r.live) store_column<E, DP>(dq, p.scale, (T *)p.dq + (sq.q0 + r.tok) * p.dqt + r.hq * p.dqh, p.D, h);
 }
 
 // ---- dK, dV: 32 keys a wave (columns), tiles of packed rows (q and dO) through LDS ----
@@ -240,23 +221,13 @@ __global__ void __launch_bounds__(256, __is_same(E, F32) || DP > 64 ? 1 : 2) k_a
     if (key_wg < 0 || key_wg >= sq.lk_slot) return;
     const int off = sq.lk - sq.lq;
     const int key = (int)key_wg + wave * 32 + (lane & 31);
-    const bool live = key < sq.lk;
+    const int key_at = min(key, sq.lk_slot - 1);
     uint4 kf[TL::kSteps], vf[TL::kSteps];
-    {
-        const T *k = (const T *)p.k + (sq.k0 + key) * p.kt + hk * p.kh, *v = (const T *)p.v + (sq.k0 + key) * p.vt + hk * p.vh;
-#pragma unroll
-        for (int t = 0; t < TL::kSteps; ++t) {
-            const int col = (2 * t + h) * (16 / (int)sizeof(T));
-            const bool in = live && col < p.D;
-            kf[t] = in ? *(const uint4 *)(k + col) : make_uint4(0, 0, 0, 0);
-            vf[t] = in ? *(const uint4 *)(v + col) : make_uint4(0, 0, 0, 0);
-        }
-    }
+    load_row<E, DP>(kf, (const T *)p.k + (sq.k0 + key_at) * p.kt + hk * p.kh, p.D, h);
+    load_row<E, DP>(vf, (const T *)p.v + (sq.k0 + key_at) * p.vt + hk * p.vh, p.D, h);
     f32x16 dk[DP / 32], dv[DP / 32];
 #pragma unroll
-    for (int db = 0; db < DP / 32; ++db)
-#pragma unroll
-        for (int v = 0; v < 16; ++v) dk[db][v] = 0.0f, dv[db][v] = 0.0f;
+    for (int db = 0; db < DP / 32; ++db) dk[db] = zero16(), dv[db] = zero16();
     const float c = p.scale * kLog2e;
     const int64_t row_end = key_wg < sq.lk ? (int64_t)sq.lq * p.grp : 0;
     // causal: the first token that sees the workgroup's first key

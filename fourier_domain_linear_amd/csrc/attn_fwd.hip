@@ -104,58 +104,21 @@ __global__ void __launch_bounds__(256, (FwdCfg<E, DP, SHORT>::WPE)) k_attn_fwd(c
     if (slot < 0) return;
     int64_t tile;
     const Seq sq = seq_of_slot<false>(p, p.grp, C::BM, slot, tile);
-    const int64_t row_end = (int64_t)sq.lq * p.grp, row_wg = tile * C::BM;
-    if (row_wg < 0 || row_wg >= row_end) return;
-    const int off = sq.lk - sq.lq;  // causal: token t sees keys up to t + off
-
-    // this lane's row
-    const int64_t row = row_wg + wave * 32 + (lane & 31);
-    const bool live = row < row_end;
-    const int tok = live ? (int)((uint32_t)row / (uint32_t)p.grp) : 0;
-    const int hq = hk * p.grp + (live ? (int)((uint32_t)row - (uint32_t)tok * (uint32_t)p.grp) : 0);
-    uint4 qf[TL::kSteps];
-    {
-        const T *q = (const T *)p.q + (sq.q0 + tok) * p.qt + hq * p.qh;
-#pragma unroll
-        for (int t = 0; t < TL::kSteps; ++t) {
-            const int col = (2 * t + h) * (16 / (int)sizeof(T));
-            qf[t] = live && col < p.D ? *(const uint4 *)(q + col) : make_uint4(0, 0, 0, 0);
-        }
-    }
-    int last = live ? (p.causal ? min(tok + off, sq.lk - 1) : sq.lk - 1) : -1;  // last key of this row
-    // key range of the workgroup (all rows) and of this split
-    const int64_t row_last = (row_wg + C::BM < row_end ? row_wg + C::BM : row_end) - 1;
-    int k_end = p.causal ? min((int)((uint32_t)row_last / (uint32_t)p.grp) + off + 1, sq.lk) : sq.lk;
-    int k_beg = 0;
+    const int row_wg = (int)tile * C::BM;
+    if (tile < 0 || row_wg >= sq.lq * p.grp) return;
+    const Rows r = rows_of(p, sq, hk, row_wg, C::BM, wave, lane);
+    int k_beg = 0, k_end = r.k_end;
     if (p.nsplit > 1) {
         const int tiles = (k_end + C::BN - 1) / C::BN, z = blockIdx.z;
         k_beg = (int)((int64_t)tiles * z / p.nsplit) * C::BN;
         k_end = min(k_end, (int)((int64_t)tiles * (z + 1) / p.nsplit) * C::BN);
     }
-    // smallest `last` of the wave: tiles wholly below it need no mask
-    int wave_min = live ? last : 0x7fffffff, wave_max = last;
-#pragma unroll
-    for (int x = 16; x >= 1; x >>= 1) {
-        wave_min = min(wave_min, __shfl_xor(wave_min, x));
-        wave_max = max(wave_max, __shfl_xor(wave_max, x));
-    }
-    wave_min = uniform(wave_min);
-    wave_max = uniform(wave_max);
 
-    FwdState<E, DP> st;
-#pragma unroll
-    for (int db = 0; db < DP / 32; ++db)
-#pragma unroll
-        for (int v = 0; v < 16; ++v) st.o[db][v] = 0.0f;
-    st.m = -INFINITY;
-    st.l = 0.0f;
-    const float c = p.scale * kLog2e;
-
+    // the first tile's loads go first
     const T *kg = (const T *)p.k + sq.k0 * p.kt + hk * p.kh;
     const T *vg = (const T *)p.v + sq.k0 * p.vt + hk * p.vh;
     TileDma<E, DP, C::BN> dk, dv;
     const uint32_t lds0 = lds_offset(lds);
-    const typename TL::Lane L = TL::lane_of(lane);
     auto fetch = [&](int k0, int buf) {
         const int valid = sq.lk - k0;
         if (valid < C::BN) {
@@ -169,9 +132,22 @@ __global__ void __launch_bounds__(256, (FwdCfg<E, DP, SHORT>::WPE)) k_attn_fwd(c
     dk.offsets(p.kt, C::BN, wave, lane);
     dv.offsets(p.vt, C::BN, wave, lane);
     if (k_beg < k_end) fetch(k_beg, 0);
+    uint4 qf[TL::kSteps];
+    load_row<E, DP>(qf, (const T *)p.q + (sq.q0 + r.tok) * p.qt + r.hq * p.qh, p.D, h);
+
+    FwdState<E, DP> st;
+#pragma unroll
+    for (int db = 0; db < DP / 32; ++db)
+#pragma unroll
+        for (int v = 0; v < 16; ++v) st.o[db][v] = 0.0f;
+    st.m = -INFINITY;
+    st.l = 0.0f;
+    const float c = p.scale * kLog2e;
+
+    const typename TL::Lane L = TL::lane_of(lane);
     int buf = 0;
     // (a wave without rows or keys fetches its part of the tiles, in a loop of its own)
-    const bool works = wave_max >= k_beg;
+    const bool works = r.wave_max >= k_beg;
     auto arrive = [&](int k0) {
         dma_wait();
         __syncthreads();  // this tile is in LDS; the other buffer has no more readers
@@ -181,7 +157,7 @@ __global__ void __launch_bounds__(256, (FwdCfg<E, DP, SHORT>::WPE)) k_attn_fwd(c
         for (int k0 = k_beg; k0 < k_end; k0 += C::BN) {
             arrive(k0);
             const uint32_t kt = lds0 + buf * 2 * C::kTileBytes, vt = kt + C::kTileBytes;
-            fwd_block<E, DP, C::NKB>(st, qf, L, kt, vt, c, k0 + C::BN - 1 > wave_min, last - k0, h);
+            fwd_block<E, DP, C::NKB>(st, qf, L, kt, vt, c, k0 + C::BN - 1 > r.wave_min, r.last - k0, h);
             buf ^= 1;
         }
     } else {
@@ -192,9 +168,9 @@ __global__ void __launch_bounds__(256, (FwdCfg<E, DP, SHORT>::WPE)) k_attn_fwd(c
     }
 
     const float l = half_sum(st.l);
-    const bool empty = last < 0;
-    const int64_t at = (sq.q0 + tok) * p.Hq + hq;
-    if (!live) return;
+    const bool empty = r.last < 0;
+    const int64_t at = (sq.q0 + r.tok) * p.Hq + r.hq;
+    if (!r.live) return;
     if (p.nsplit > 1) {  // partial results: unnormalised o, then (m, l), for k_attn_join
         const int64_t rows = p.total_q * p.Hq;
         store_column<F32, DP>(st.o, 1.0f, p.ws + ((int64_t)blockIdx.z * rows + at) * p.D, p.D, h);
@@ -205,7 +181,7 @@ __global__ void __launch_bounds__(256, (FwdCfg<E, DP, SHORT>::WPE)) k_attn_fwd(c
         }
         return;
     }
-    store_column<E, DP>(st.o, empty ? 0.0f : 1.0f / l, (T *)p.o + (sq.q0 + tok) * p.ot + hq * p.oh, p.D, h);
+    store_column<E, DP>(st.o, empty ? 0.0f : 1.0f / l, (T *)p.o + (sq.q0 + r.tok) * p.ot + r.hq * p.oh, p.D, h);
     if (p.lse && h == 0) p.lse[at] = empty ? -INFINITY : st.m * kLn2 + logf(l);
 }
 
@@ -267,7 +243,8 @@ template <class E>
 hipError_t run_fwd_e(const AttnParams &p, hipStream_t s) {
     if (p.D <= 32) return run_fwd<E, 32, false>(p, s);
     if (p.D <= 64) return run_fwd<E, 64, false>(p, s);
-    if (!__is_same(E, F32) && p.total_k <= kShortKeys * p.B) return run_fwd<E, 128, true>(p, s);
+    if constexpr (!__is_same(E, F32))
+        if (p.total_k <= kShortKeys * p.B) return run_fwd<E, 128, true>(p, s);
     return run_fwd<E, 128, false>(p, s);
 }
 

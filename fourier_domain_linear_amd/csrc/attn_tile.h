@@ -88,23 +88,50 @@ __device__ __forceinline__ void zero_pad(char *lds, int bytes, int D, int DP, in
     __syncthreads();
 }
 
-// Stores a column's 32 db + d_row(v, h) values (o^T in D layout), scaled, to dst[0..D).
+// Stores a column's 32 db + d_row(v, h) values (o^T in D layout), scaled, to dst[0..D), 16 bytes a lane: lanes l and
+// l ^ 32 hold neighbouring fours of the same row and exchange them, so that each has eight in a row.
 template <class E, int DP>
 __device__ __forceinline__ void store_column(const f32x16 *o, float inv, typename ElemOf<E>::type *dst, int D, int h) {
 #pragma unroll
-    for (int db = 0; db < DP / 32; ++db)
+    for (int db = 0; db < DP / 32; ++db) {
+        if constexpr (__is_same(E, F32)) {
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
-            const int d = 32 * db + 8 * g + 4 * h;
-            if (d < D) {
-                if constexpr (__is_same(E, F32))
+            for (int g = 0; g < 4; ++g) {
+                const int d = 32 * db + 8 * g + 4 * h;
+                if (d < D)
                     *(float4 *)(dst + d) = make_float4(o[db][4 * g] * inv, o[db][4 * g + 1] * inv, o[db][4 * g + 2] * inv,
                                                        o[db][4 * g + 3] * inv);
-                else
-                    *(uint2 *)(dst + d) = make_uint2(pack2<E>(o[db][4 * g] * inv, o[db][4 * g + 1] * inv),
-                                                     pack2<E>(o[db][4 * g + 2] * inv, o[db][4 * g + 3] * inv));
+            }
+        } else {
+#pragma unroll
+            for (int g = 0; g < 4; g += 2) {
+                uint32_t a[2], b[2];
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const int v = 4 * g + 2 * j;
+                    const auto r = __builtin_amdgcn_permlane32_swap(pack2<E>(o[db][v] * inv, o[db][v + 1] * inv),
+                                                                    pack2<E>(o[db][v + 4] * inv, o[db][v + 5] * inv), false, false);
+                    a[j] = r[0], b[j] = r[1];
+                }
+                const int d = 32 * db + 8 * g + 8 * h;
+                if (d < D) *(uint4 *)(dst + d) = make_uint4(a[0], a[1], b[0], b[1]);
             }
         }
+    }
+}
+
+// The B-operand fragments of a lane's row (dims in 16-byte chunks, zeros from D on).
+template <class E, int DP>
+__device__ __forceinline__ void load_row(uint4 *f, const typename ElemOf<E>::type *row, int D, int h) {
+    constexpr int kPer = 16 / (int)sizeof(typename ElemOf<E>::type);
+    if (D == DP) {
+#pragma unroll
+        for (int t = 0; t < Tile<E, DP>::kSteps; ++t) f[t] = *(const uint4 *)(row + (2 * t + h) * kPer);
+    } else {
+#pragma unroll
+        for (int t = 0; t < Tile<E, DP>::kSteps; ++t)
+            f[t] = (2 * t + h) * kPer < D ? *(const uint4 *)(row + (2 * t + h) * kPer) : make_uint4(0, 0, 0, 0);
+    }
 }
 
 }  // namespace eqlin

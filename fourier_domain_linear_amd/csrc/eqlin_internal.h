@@ -193,6 +193,7 @@ struct AttnParams {
     const int *cu_q, *cu_k, *len_k;
     int64_t total_q, total_k;
     int B, Hq, Hkv, grp, D;
+    int lgrp;  // log2 of grp, or -1
     float scale;
     int causal;
     // gradients

@@ -98,6 +98,7 @@ eqlin_status_t check_attention(const eqlin_attention_args *a, eqlin::AttnParams 
     p->cu_q = a->cu_q, p->cu_k = a->cu_k, p->len_k = a->len_k;
     p->total_q = a->total_q, p->total_k = a->total_k;
     p->B = a->batch, p->Hq = a->heads_q, p->Hkv = a->heads_kv, p->grp = a->heads_q / a->heads_kv, p->D = a->dim;
+    p->lgrp = (p->grp & (p->grp - 1)) == 0 ? ilog2(p->grp) : -1;
     p->scale = a->scale, p->causal = a->causal != 0;
     p->nsplit = 1;
     return EQLIN_OK;
