@@ -437,13 +437,17 @@ def conv_forward_expanded(h: Handle, x: torch.Tensor, b: torch.Tensor | None = N
 # ---- the operators between the layers of a transformer stage ----
 
 
-def _on(device, fn, *args):
-    """fn(*args, current stream) with ``device`` current: the launch goes where the tensors are."""
-    stream = torch.cuda.current_stream(device).cuda_stream
-    if torch.cuda.current_device() == device.index:
-        return fn(*args, stream)
-    with torch.cuda.device(device):
-        return fn(*args, stream)
+# the current stream's handle without building a Stream object (microseconds a call); public API where it is missing
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _on(index: int, fn, *args):
+    """fn(*args, current stream) with device ``index`` current: the launch goes where the tensors are."""
+    if torch.cuda.current_device() == index:
+        return fn(*args, _raw_stream(index))
+    with torch.cuda.device(index):
+        return fn(*args, _raw_stream(index))
 
 
 def _ptr(t: torch.Tensor | None):
@@ -453,7 +457,7 @@ def _ptr(t: torch.Tensor | None):
 def _same(t: torch.Tensor, like: torch.Tensor, name: str, shape=None):
     """t: contiguous, on like's device, of its dtype and shape (or ``shape``)."""
     _need_cuda(t, name)
-    if t.dtype != like.dtype or t.device != like.device or tuple(t.shape) != tuple(like.shape if shape is None else shape):
+    if t.dtype != like.dtype or t.get_device() != like.get_device() or t.shape != (like.shape if shape is None else shape):
         raise ValueError(f"{name} must be {tuple(like.shape if shape is None else shape)} of {like.dtype} on {like.device}, "
                          f"got {tuple(t.shape)} {t.dtype} on {t.device}")
 
@@ -462,7 +466,7 @@ def _f32_out(t: torch.Tensor | None, shape, device, name: str):
     if t is None:
         return torch.empty(shape, dtype=torch.float32, device=device)
     _need_cuda(t, name)
-    if t.dtype != torch.float32 or tuple(t.shape) != tuple(shape) or t.device != device:
+    if t.dtype != torch.float32 or t.shape != shape or t.device != device:
         raise ValueError(f"{name} must be {tuple(shape)} of float32 on {device}")
     return t
 
@@ -490,8 +494,8 @@ def rmsnorm(x: torch.Tensor, gamma: torch.Tensor | None = None, residual: torch.
     else:
         _same(y, x, "y")
     s = x if residual is None else torch.empty_like(x)
-    rstd = torch.empty((N,), dtype=torch.float32, device=x.device)
-    st = _on(x.device, load_library().eqlin_rmsnorm, x.data_ptr(), _ptr(residual), _ptr(gamma),
+    rstd = x.new_empty(N, dtype=torch.float32)
+    st = _on(x.get_device(), load_library().eqlin_rmsnorm, x.data_ptr(), _ptr(residual), _ptr(gamma),
              None if residual is None else s.data_ptr(), y.data_ptr(), rstd.data_ptr(), N, C, G, eps, code)
     _check(st, "eqlin_rmsnorm")
     return y, s, rstd
@@ -505,9 +509,9 @@ def rmsnorm_quant(x: torch.Tensor, gamma: torch.Tensor | None = None, residual: 
     N, C, G = x.shape
     q = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=x.device)
     s = x if residual is None else torch.empty_like(x)
-    rstd = torch.empty((N,), dtype=torch.float32, device=x.device)
-    scale = torch.empty((N,), dtype=torch.float32, device=x.device)
-    st = _on(x.device, load_library().eqlin_rmsnorm_quant, x.data_ptr(), _ptr(residual), _ptr(gamma),
+    rstd = x.new_empty(N, dtype=torch.float32)
+    scale = x.new_empty(N, dtype=torch.float32)
+    st = _on(x.get_device(), load_library().eqlin_rmsnorm_quant, x.data_ptr(), _ptr(residual), _ptr(gamma),
              None if residual is None else s.data_ptr(), q.data_ptr(), scale.data_ptr(), rstd.data_ptr(), N, C, G, eps, code)
     _check(st, "eqlin_rmsnorm_quant")
     return q, scale, s, rstd
@@ -532,7 +536,7 @@ def rmsnorm_backward(dy: torch.Tensor, s: torch.Tensor, gamma: torch.Tensor | No
     dgamma = torch.empty((C,), dtype=torch.float32, device=s.device) if with_gamma else None
     need = rmsnorm_backward_workspace(N, C, G) if with_gamma else 0
     workspace = _workspace(workspace, need, s.device)
-    st = _on(s.device, load_library().eqlin_rmsnorm_backward, s.data_ptr(), _ptr(gamma), rstd.data_ptr(), dy.data_ptr(),
+    st = _on(s.get_device(), load_library().eqlin_rmsnorm_backward, s.data_ptr(), _ptr(gamma), rstd.data_ptr(), dy.data_ptr(),
              _ptr(ds), dx.data_ptr(), _ptr(dgamma), N, C, G, code, _ptr(workspace), need)
     _check(st, "eqlin_rmsnorm_backward")
     return dx, dgamma
@@ -555,10 +559,10 @@ def _heads(t: torch.Tensor, name: str):
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA (HIP) tensor")
     shape, strides = t.shape, t.stride()
-    if len(shape) == 4:
-        dim, ok = shape[2] * shape[3], (strides[3] == 1 or shape[3] == 1) and (strides[2] == shape[3] or shape[2] == 1)
-    elif len(shape) == 3:
+    if len(shape) == 3:
         dim, ok = shape[2], strides[2] == 1 or shape[2] == 1
+    elif len(shape) == 4:
+        dim, ok = shape[2] * shape[3], (strides[3] == 1 or shape[3] == 1) and (strides[2] == shape[3] or shape[2] == 1)
     else:
         raise ValueError(f"{name} must be [T, H, D] or [T, H, dc, G], got {tuple(shape)}")
     if not ok:
@@ -566,10 +570,10 @@ def _heads(t: torch.Tensor, name: str):
     return shape[0], shape[1], dim
 
 
-def _index(t: torch.Tensor, name: str, shape, device):
+def _index(t: torch.Tensor, name: str, shape, index: int):
     _need_cuda(t, name)
-    if t.dtype != torch.int32 or tuple(t.shape) != tuple(shape) or t.device != device:
-        raise ValueError(f"{name} must be {tuple(shape)} of int32 on {device}, got {tuple(t.shape)} {t.dtype}")
+    if t.dtype != torch.int32 or t.shape != shape or t.get_device() != index:
+        raise ValueError(f"{name} must be {tuple(shape)} of int32 on device {index}, got {tuple(t.shape)} {t.dtype} on {t.device}")
 
 
 def rotary(x: torch.Tensor, pos: torch.Tensor, pairs, base: float = 10000.0, group: str = "cyclic", inverse: bool = False,
@@ -582,16 +586,16 @@ def rotary(x: torch.Tensor, pos: torch.Tensor, pairs, base: float = 10000.0, gro
     N, H, D = _heads(x, "x")
     G = x.shape[3] if x.dim() == 4 else 1
     axes = len(pairs)
-    _index(pos, "pos", (N, axes), x.device)
+    _index(pos, "pos", (N, axes), x.get_device())
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        out = x.new_empty(x.shape)
     elif out is not x:
         _heads(out, "out")
         if out.shape != x.shape or out.dtype != x.dtype or out.device != x.device:
             raise ValueError(f"out must be {tuple(x.shape)} of {x.dtype} on {x.device}")
     flags = (EQLIN_ROTARY_INVERSE if inverse else 0) | (EQLIN_ROTARY_D4 if group == "d4" else 0)
     xs, ys = x.stride(), out.stride()
-    st = _on(x.device, load_library().eqlin_rotary, x.data_ptr(), xs[0], xs[1], out.data_ptr(), ys[0], ys[1],
+    st = _on(x.get_device(), load_library().eqlin_rotary, x.data_ptr(), xs[0], xs[1], out.data_ptr(), ys[0], ys[1],
              pos.data_ptr(), N, H, D // G if G else 0, G, axes, (ctypes.c_int * axes)(*pairs), base, flags,
              _dtype_code(x.dtype))
     _check(st, "eqlin_rotary")
@@ -600,14 +604,18 @@ def rotary(x: torch.Tensor, pos: torch.Tensor, pairs, base: float = 10000.0, gro
 
 def _attention_args(q, k, v, o, lse, cu_q, cu_k, len_k, causal, scale):
     Tq, Hq, D = _heads(q, "q")
-    Tk, Hkv, Dk = _heads(k, "k")
-    dev, dt = q.device, q.dtype
-    if _heads(v, "v") != (Tk, Hkv, Dk) or Dk != D:
+    Tk, Hkv, Dk = kv = _heads(k, "k")
+    dev, dt = q.get_device(), q.dtype
+    if _heads(v, "v") != kv or Dk != D:
         raise ValueError(f"k and v must be [T, heads, {D}] alike, got {tuple(k.shape)} and {tuple(v.shape)}")
-    if k.dtype != dt or v.dtype != dt or k.device != dev or v.device != dev:
+    if k.dtype != dt or v.dtype != dt or k.get_device() != dev or v.get_device() != dev:
         raise TypeError(f"q, k and v must be of one dtype on one device, got {dt}, {k.dtype}, {v.dtype}")
-    if _heads(o, "o") != (Tq, Hq, D) or o.dtype != dt or o.device != dev:
-        raise ValueError(f"o must be {tuple(q.shape)} of {dt} on {dev}")
+    if o is None:
+        o = q.new_empty(q.shape)
+    elif _heads(o, "o") != (Tq, Hq, D) or o.dtype != dt or o.get_device() != dev:
+        raise ValueError(f"o must be {tuple(q.shape)} of {dt} on {q.device}")
+    if lse is None:
+        lse = q.new_empty((Tq, Hq), dtype=torch.float32)
     _need_cuda(cu_q, "cu_q")
     B = cu_q.numel() - 1
     if B < 0:
@@ -617,9 +625,10 @@ def _attention_args(q, k, v, o, lse, cu_q, cu_k, len_k, causal, scale):
     if len_k is not None:
         _index(len_k, "len_k", (B,), dev)
     qs, ks, vs, os_ = q.stride(), k.stride(), v.stride(), o.stride()
-    return AttentionArgs(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), _ptr(lse), qs[0], qs[1], ks[0], ks[1],
-                         vs[0], vs[1], os_[0], os_[1], cu_q.data_ptr(), cu_k.data_ptr(), _ptr(len_k), Tq, Tk, B, Hq, Hkv, D,
-                         D ** -0.5 if scale is None else scale, 1 if causal else 0, _dtype_code(dt))
+    a = AttentionArgs(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(), qs[0], qs[1], ks[0], ks[1],
+                      vs[0], vs[1], os_[0], os_[1], cu_q.data_ptr(), cu_k.data_ptr(), _ptr(len_k), Tq, Tk, B, Hq, Hkv, D,
+                      D ** -0.5 if scale is None else scale, 1 if causal else 0, _dtype_code(dt))
+    return a, o, lse
 
 
 def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: torch.Tensor, cu_k: torch.Tensor,
@@ -630,14 +639,13 @@ def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: torch.Ten
     of Hkv. cu_q, cu_k: int32 [batch + 1], the sequences' bounds in tokens; len_k: int32 [batch], how many keys
     of each stretch count. causal: token t of lq sees the keys j <= t + lk - lq. scale: 1/sqrt(D) if None.
     o: like q; lse: float32 [T, Hq]."""
-    if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
-    a = _attention_args(q, k, v, out, lse, cu_q, cu_k, len_k, causal, scale)
+    a, out, lse = _attention_args(q, k, v, out, None, cu_q, cu_k, len_k, causal, scale)
     lib, pa = load_library(), ctypes.byref(a)
     need = lib.eqlin_attention_workspace(pa)
-    workspace = _workspace(workspace, need, q.device)
-    _check(_on(q.device, lib.eqlin_attention, pa, _ptr(workspace), need), "eqlin_attention")
+    workspace = _workspace(workspace, need, q.device) if need else None
+    st = _on(q.get_device(), lib.eqlin_attention, pa, _ptr(workspace), need)
+    if st != EQLIN_OK:
+        _check(st, "eqlin_attention")
     return out, lse
 
 
@@ -648,12 +656,14 @@ def attention_backward(do: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: to
                        workspace: torch.Tensor | None = None):
     """eqlin_attention_backward -> (dq, dk, dv) from do and the forward's tensors and arguments. dq, dk, dv:
     tensors to write to (views of one gradient of a qkv layer's output, say), else new ones."""
-    a = _attention_args(q, k, v, o, lse, cu_q, cu_k, len_k, causal, scale)
-    _f32_out(lse, (a.total_q, a.heads_q), q.device, "lse")
+    if o is None or lse is None:
+        raise ValueError("o and lse are the forward's")
+    _f32_out(lse, q.shape[:2], q.device, "lse")
+    a, o, lse = _attention_args(q, k, v, o, lse, cu_q, cu_k, len_k, causal, scale)
     grads = []
     for name, t, like in (("dq", dq, q), ("dk", dk, k), ("dv", dv, v)):
         if t is None:
-            t = torch.empty(like.shape, dtype=like.dtype, device=like.device)
+            t = like.new_empty(like.shape)
         elif _heads(t, name) != _heads(like, name) or t.dtype != like.dtype or t.device != like.device:
             raise ValueError(f"{name} must be {tuple(like.shape)} of {like.dtype} on {like.device}")
         grads.append(t)
@@ -665,7 +675,7 @@ def attention_backward(do: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: to
     lib, pa = load_library(), ctypes.byref(a)
     need = lib.eqlin_attention_backward_workspace(pa)
     workspace = _workspace(workspace, need, q.device)
-    _check(_on(q.device, lib.eqlin_attention_backward, pa, ctypes.byref(g), _ptr(workspace), need),
+    _check(_on(q.get_device(), lib.eqlin_attention_backward, pa, ctypes.byref(g), _ptr(workspace), need),
            "eqlin_attention_backward")
     return dq, dk, dv
 

@@ -239,6 +239,30 @@ __device__ __forceinline__ Seq seq_of_slot(const AttnParams &p, int mul, int siz
     return s;
 }
 
+// The sequence of packed query token t (the last that begins at or before it), with its index.
+__device__ __forceinline__ Seq seq_of_row(const AttnParams &p, int t, int &index) {
+    const int lane = threadIdx.x & 63;
+    int lo = 0, n = p.B;
+    while (n > 1) {
+        const int step = (n + 63) / 64, i = lo + lane * step;
+        const bool in = lane * step < n && p.cu_q[i < p.B ? i : p.B] <= t;
+        int c = __popcll(__ballot(in));
+        c = c < 1 ? 1 : c;
+        const int skip = (c - 1) * step;
+        lo += skip;
+        n = n - skip < step ? n - skip : step;
+    }
+    index = uniform(lo);
+    auto clamp = [](int x, int a, int b) { return min(max(x, a), b); };
+    Seq s;
+    const int q0 = clamp(p.cu_q[index], 0, (int)p.total_q), k0 = clamp(p.cu_k[index], 0, (int)p.total_k);
+    s.q0 = q0, s.k0 = k0;
+    s.lq = clamp(p.cu_q[index + 1], q0, (int)p.total_q) - q0;
+    s.lk_slot = clamp(p.cu_k[index + 1], k0, (int)p.total_k) - k0;
+    s.lk = p.len_k ? clamp(p.len_k[index], 0, s.lk_slot) : s.lk_slot;
+    return s;
+}
+
 // packed row -> token (rows are below 2^31; most groups are powers of two)
 __device__ __forceinline__ int row_token(const AttnParams &p, int row) {
     return p.lgrp >= 0 ? row >> p.lgrp : (int)((uint32_t)row / (uint32_t)p.grp);

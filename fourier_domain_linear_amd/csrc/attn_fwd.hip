@@ -1,7 +1,7 @@
 // attn_fwd.hip -- attention over packed sequences: o = softmax(scale q k^T) v, one pass over the keys with
 // the running maximum and sum.
 #include "attn.h"
-#include "attn_tile.h"
+#include "attn_fwd.h"
 
 namespace eqlin {
 
@@ -25,72 +25,6 @@ struct FwdCfg {
     static constexpr int kLds = 4 * kTileBytes;                                 // k and v, two buffers
 };
 constexpr int64_t kShortKeys = 512;  // keys a sequence on average up to which SHORT is taken
-
-// Running softmax state of a lane's column and its O^T accumulators.
-template <class E, int DP>
-struct FwdState {
-    f32x16 o[DP / 32];
-    float m, l;  // m: running maximum in log2 units (scaled); l: this lane's half of the sum
-};
-
-// One tile of 32 NKB keys against a wave's 32 columns. lim: last key (within the tile) the column may see;
-// masked: some key of the tile is beyond some column's lim. (The test wraps the masking alone: accumulators that
-// two branches write cost a second set of registers.)
-template <class E, int DP, int NKB>
-__device__ __forceinline__ void fwd_block(FwdState<E, DP> &st, const uint4 *qf, const typename Tile<E, DP>::Lane &L, uint32_t kt,
-                                          uint32_t vt, float c, bool masked, int lim, int h) {
-    typedef Tile<E, DP> TL;
-    f32x16 s[NKB];
-#pragma unroll
-    for (int kb = 0; kb < NKB; ++kb) {
-        s[kb] = zero16();
-#pragma unroll
-        for (int t = 0; t < TL::kSteps; ++t) s[kb] = mma_frag<E>(TL::row_frag(kt, L, kb, t), qf[t], s[kb]);
-    }
-    if constexpr (!__is_same(E, F32) && DP == 128) read_ahead<NKB * TL::kSteps, NKB * TL::kSteps, NKB == 1 ? 4 : 6>();
-    if (masked) {
-#pragma unroll
-        for (int kb = 0; kb < NKB; ++kb)
-#pragma unroll
-            for (int v = 0; v < 16; ++v) s[kb][v] = 32 * kb + d_row(v, 0) <= lim - 4 * h ? s[kb][v] : -INFINITY;
-    }
-    float mx = -INFINITY;
-#pragma unroll
-    for (int kb = 0; kb < NKB; ++kb)
-#pragma unroll
-        for (int v = 0; v < 16; ++v) mx = fmaxf(mx, s[kb][v]);
-    mx = half_max(mx) * c;
-    // The maximum is only raised when it grew by more than 8 (in log2 units): a stale one keeps every
-    // p <= 2^8, exact in the sums' fp32 and in range of fp16, and saves the pass over the accumulators.
-    if (__any(mx > st.m + 8.0f)) {
-        const float mn = fmaxf(st.m, mx);
-        const float a = mn == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(st.m - mn);
-        st.m = mn;
-        st.l *= a;
-#pragma unroll
-        for (int db = 0; db < DP / 32; ++db)
-#pragma unroll
-            for (int v = 0; v < 16; ++v) st.o[db][v] *= a;
-    }
-    const float mm = st.m == -INFINITY ? 0.0f : st.m;
-    float sum = 0.0f;
-#pragma unroll
-    for (int kb = 0; kb < NKB; ++kb) {
-#pragma unroll
-        for (int v = 0; v < 16; ++v) {
-            s[kb][v] = __builtin_amdgcn_exp2f(fmaf(s[kb][v], c, -mm));
-            sum += s[kb][v];
-        }
-        WFrags<E> w;
-        w.set(s[kb]);
-#pragma unroll
-        for (int f = 0; f < WFrags<E>::NF; ++f)
-#pragma unroll
-            for (int db = 0; db < DP / 32; ++db)
-                st.o[db] = mma_frag<E>(TL::col_frag(vt, L, kb, f, db), w.f[f], st.o[db]);
-    }
-    st.l += sum;
-}
 
 template <class E, int DP, bool SHORT>
 __global__ void __launch_bounds__(256, (FwdCfg<E, DP, SHORT>::WPE)) k_attn_fwd(const AttnParams p) {
@@ -136,12 +70,7 @@ __global__ void __launch_bounds__(256, (FwdCfg<E, DP, SHORT>::WPE)) k_attn_fwd(c
     load_row<E, DP>(qf, (const T *)p.q + (sq.q0 + r.tok) * p.qt + r.hq * p.qh, p.D, h);
 
     FwdState<E, DP> st;
-#pragma unroll
-    for (int db = 0; db < DP / 32; ++db)
-#pragma unroll
-        for (int v = 0; v < 16; ++v) st.o[db][v] = 0.0f;
-    st.m = -INFINITY;
-    st.l = 0.0f;
+    st.clear();
     const float c = p.scale * kLog2e;
 
     const typename TL::Lane L = TL::lane_of(lane);
@@ -167,22 +96,19 @@ __global__ void __launch_bounds__(256, (FwdCfg<E, DP, SHORT>::WPE)) k_attn_fwd(c
         }
     }
 
-    const float l = half_sum(st.l);
-    const bool empty = r.last < 0;
-    const int64_t at = (sq.q0 + r.tok) * p.Hq + r.hq;
-    if (!r.live) return;
     if (p.nsplit > 1) {  // partial results: unnormalised o, then (m, l), for k_attn_join
-        const int64_t rows = p.total_q * p.Hq;
+        const float l = half_sum(st.l);
+        if (!r.live) return;
+        const int64_t at = (sq.q0 + r.tok) * p.Hq + r.hq, rows = p.total_q * p.Hq;
         store_column<F32, DP>(st.o, 1.0f, p.ws + ((int64_t)blockIdx.z * rows + at) * p.D, p.D, h);
         if (h == 0) {
             float *ml = p.ws + p.nsplit * rows * p.D + ((int64_t)blockIdx.z * rows + at) * 2;
             ml[0] = st.m;
-            ml[1] = empty ? -1.0f : l;  // negative: a row that sees no key
+            ml[1] = r.last < 0 ? -1.0f : l;  // negative: a row that sees no key
         }
         return;
     }
-    store_column<E, DP>(st.o, empty ? 0.0f : 1.0f / l, (T *)p.o + (sq.q0 + r.tok) * p.ot + r.hq * p.oh, p.D, h);
-    if (p.lse && h == 0) p.lse[at] = empty ? -INFINITY : st.m * kLn2 + logf(l);
+    finish_rows<E, DP>(p, sq, st, r, h);
 }
 
 // ---- joining the key ranges of a row: one wave a row ----
@@ -259,14 +185,17 @@ int pick_nsplit(const AttnParams &p) {
 
 }  // namespace
 
-size_t attention_workspace_bytes(const AttnParams &p, eqlin_dtype_t) {
+size_t attention_workspace_bytes(const AttnParams &p0, eqlin_dtype_t) {
+    AttnParams p = p0;
     if (p.total_q <= 0 || p.B <= 0) return 0;
+    if (plan_step(p)) return step_workspace_bytes(p);
     const int n = pick_nsplit(p);
     return n <= 1 ? 0 : (size_t)n * p.total_q * p.Hq * (p.D + 2) * sizeof(float);
 }
 
 hipError_t launch_attention(const AttnParams &p0, eqlin_dtype_t dtype, hipStream_t s) {
     AttnParams p = p0;
+    if (plan_step(p)) return launch_step(p, dtype, s);
     p.nsplit = pick_nsplit(p);
     if (dtype == EQLIN_F32) return run_fwd_e<F32>(p, s);
     if (dtype == EQLIN_F16) return run_fwd_e<F16>(p, s);

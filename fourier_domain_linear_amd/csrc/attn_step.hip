@@ -1,0 +1,204 @@
+// attn_step.hip -- attention of few query rows over many keys (a new token over a cache): the keys of a sequence
+// are split into chunks, one wave takes a chunk, and the partial results are joined.
+//
+// Bound by reading k and v once. A workgroup is one wave: it keeps two 32-key tiles of k and v in flight straight
+// into LDS (32 KB at 128 dims in a half type, so five waves share a CU and 160 KB are on their way), with no barrier
+// and no other wave to wait for. The group's rows are the 32 columns of its products.
+#include "attn.h"
+#include "attn_fwd.h"
+
+namespace eqlin {
+
+namespace {
+
+template <class E, int DP>
+struct StepCfg {
+    typedef Tile<E, DP> TL;
+    static constexpr int BN = 32;
+    static constexpr int kTileBytes = BN * TL::kRow;
+    static constexpr int kLds = 4 * kTileBytes;
+    typedef TileDma<E, DP, BN, 1> Dma;
+};
+
+// Rows of 32 (columns of the products) from packed row `row0` on over the keys [k_beg, k_end).
+template <class E, int DP>
+__device__ __forceinline__ void step_rows(const AttnParams &p, const Seq &sq, int hk, int row0, int k_beg, int k_end, uint32_t lds0,
+                                          int lane, FwdState<E, DP> &st, Rows &r) {
+    typedef StepCfg<E, DP> C;
+    typedef Tile<E, DP> TL;
+    typedef typename ElemOf<E>::type T;
+    const int h = lane >> 5;
+    r = rows_of(p, sq, hk, row0, 32, 0, lane);
+    k_end = min(k_end, r.k_end);
+    const T *kg = (const T *)p.k + sq.k0 * p.kt + hk * p.kh;
+    const T *vg = (const T *)p.v + sq.k0 * p.vt + hk * p.vh;
+    typename C::Dma dk, dv;
+    auto fetch = [&](int k0, int buf) {
+        const int valid = sq.lk - k0;
+        if (valid < C::BN) {
+            dk.offsets(p.kt, valid, 0, lane);
+            dv.offsets(p.vt, valid, 0, lane);
+        }
+        dk.issue(lds0 + buf * 2 * C::kTileBytes, kg + (int64_t)k0 * p.kt, p.D, 0, lane);
+        dv.issue(lds0 + buf * 2 * C::kTileBytes + C::kTileBytes, vg + (int64_t)k0 * p.vt, p.D, 0, lane);
+    };
+    dk.offsets(p.kt, C::BN, 0, lane);
+    dv.offsets(p.vt, C::BN, 0, lane);
+    uint4 qf[TL::kSteps];
+    load_row<E, DP>(qf, (const T *)p.q + (sq.q0 + r.tok) * p.qt + r.hq * p.qh, p.D, h);
+    if (k_beg < k_end) fetch(k_beg, 0);
+    if (k_beg + C::BN < k_end) fetch(k_beg + C::BN, 1);
+    st.clear();
+    const float c = p.scale * kLog2e;
+    const typename TL::Lane L = TL::lane_of(lane);
+    int buf = 0;
+    for (int k0 = k_beg; k0 < k_end; k0 += C::BN) {
+        // whole heads: the younger tile's loads may stay on their way
+        if (p.D == DP && k0 + C::BN < k_end) dma_wait_but<2 * C::Dma::N>();
+        else dma_wait();
+        const uint32_t kt = lds0 + buf * 2 * C::kTileBytes, vt = kt + C::kTileBytes;
+        fwd_block<E, DP, 1>(st, qf, L, kt, vt, c, k0 + C::BN - 1 > r.wave_min, r.last - k0, h);
+        lds_read_wait();  // this tile's reads are done before its place is written again
+        if (k0 + 2 * C::BN < k_end) fetch(k0 + 2 * C::BN, buf);
+        buf ^= 1;
+    }
+}
+
+template <class E, int DP>
+__global__ void __launch_bounds__(64, DP > 64 ? 1 : 2) k_attn_step(const AttnParams p) {
+    typedef StepCfg<E, DP> C;
+    extern __shared__ __align__(16) char lds[];
+    const int lane = threadIdx.x, h = lane >> 5;
+    const int hk = (int)(blockIdx.x % (uint32_t)p.Hkv);
+    const int64_t slot = blockIdx.x / (uint32_t)p.Hkv;
+    int64_t tile;
+    const Seq sq = seq_of_slot<true>(p, 1, p.chunk, slot, tile);
+    const int64_t k_at = tile * p.chunk;
+    if (tile < 0 || k_at >= sq.lk) return;
+    zero_pad<64>(lds, C::kLds, p.D, DP, lane);
+    const int rows = sq.lq * p.grp, chunks = (sq.lk + p.chunk - 1) / p.chunk;
+    const uint32_t lds0 = lds_offset(lds);
+    FwdState<E, DP> st;
+    Rows r;
+    // one chunk, or more rows than a partial result has room for: whole rows, shared out over the chunks' waves
+    const bool split = rows <= p.rcap && chunks > 1;
+    const int k_beg = split ? (int)k_at : 0, k_end = split ? (int)min(k_at + p.chunk, (int64_t)sq.lk) : sq.lk;
+    for (int row0 = split ? 0 : (int)tile * 32; row0 < rows; row0 += split ? 32 : chunks * 32) {
+        step_rows<E, DP>(p, sq, hk, row0, k_beg, k_end, lds0, lane, st, r);
+        if (split) {
+            const float l = half_sum(st.l);
+            if (r.live) {
+                const int64_t at = (slot * p.Hkv + hk) * p.rcap + (lane & 31);
+                store_column<F32, DP>(st.o, 1.0f, p.ws + at * p.D, p.D, h);
+                if (h == 0) {
+                    float *ml = p.ws + p.slots * p.Hkv * p.rcap * p.D + at * 2;
+                    ml[0] = st.m;
+                    ml[1] = l;
+                }
+            }
+        } else {
+            finish_rows<E, DP>(p, sq, st, r, h);
+        }
+        lds_read_wait();
+    }
+}
+
+// One workgroup a row: its 16 waves share the chunks, then join over LDS.
+constexpr int kJoinWaves = 16;
+template <class E>
+__global__ void __launch_bounds__(64 * kJoinWaves) k_attn_step_join(const AttnParams p) {
+    typedef typename ElemOf<E>::type T;
+    __shared__ float so[kJoinWaves][128], sm[kJoinWaves], sl[kJoinWaves];
+    const int lane = threadIdx.x & 63, wave = uniform((int)(threadIdx.x >> 6));
+    const int64_t rows = p.total_q * p.Hq;
+    for (int64_t at = blockIdx.x; at < rows; at += gridDim.x) {
+        const int tok_at = (int)(at / p.Hq), hq = (int)(at - (int64_t)tok_at * p.Hq), hk = hq / p.grp;
+        int seq;
+        const Seq sq = seq_of_row(p, tok_at, seq);
+        const int nr = sq.lq * p.grp, chunks = (sq.lk + p.chunk - 1) / p.chunk;
+        const int tok = tok_at - (int)sq.q0, last = p.causal ? tok + sq.lk - sq.lq : sq.lk - 1;
+        if (tok < 0 || tok >= sq.lq) continue;  // outside every sequence
+        if (chunks == 1 || (nr > p.rcap && chunks > 0)) continue;  // written by the step itself
+        const int64_t slot0 = slot_start(sq.k0, seq, 1, p.chunk);
+        const int64_t base = (slot0 * p.Hkv + hk) * p.rcap + tok * p.grp + (hq - hk * p.grp), step = (int64_t)p.Hkv * p.rcap;
+        const float *ml = p.ws + p.slots * p.Hkv * p.rcap * p.D;
+        float m = -INFINITY;
+        for (int z = wave * 64 + lane; z < chunks; z += 64 * kJoinWaves) m = fmaxf(m, ml[(base + z * step) * 2]);
+        m = wave_max(m);
+        __syncthreads();
+        if (lane == 0) sm[wave] = m;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < kJoinWaves; ++w) m = fmaxf(m, sm[w]);
+        const float mm = m == -INFINITY ? 0.0f : m;
+        float l = 0.0f, o0 = 0.0f, o1 = 0.0f;
+#pragma unroll 4
+        for (int z = wave; z < chunks; z += kJoinWaves) {
+            const int64_t i = base + z * step;
+            const float w = __builtin_amdgcn_exp2f(ml[i * 2] - mm);
+            l = fmaf(w, ml[i * 2 + 1], l);
+            if (lane < p.D) o0 = fmaf(w, p.ws[i * p.D + lane], o0);
+            if (lane + 64 < p.D) o1 = fmaf(w, p.ws[i * p.D + 64 + lane], o1);
+        }
+        so[wave][lane] = o0;
+        so[wave][lane + 64] = o1;
+        if (lane == 0) sl[wave] = l;
+        __syncthreads();
+        if (threadIdx.x < 128) {
+            l = 0.0f, o0 = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kJoinWaves; ++w) {
+                l += sl[w];
+                o0 += so[w][threadIdx.x];
+            }
+            const bool empty = last < 0 || sq.lk == 0;
+            if ((int)threadIdx.x < p.D)
+                ((T *)p.o + tok_at * p.ot + hq * p.oh)[threadIdx.x] = Elem<E>::put(empty ? 0.0f : o0 / l);
+            if (p.lse && threadIdx.x == 0) p.lse[at] = empty ? -INFINITY : m * kLn2 + logf(l);
+        }
+    }
+}
+
+template <class E, int DP>
+hipError_t run_step(const AttnParams &p, hipStream_t s) {
+    typedef StepCfg<E, DP> C;
+    hipLaunchKernelGGL((k_attn_step<E, DP>), dim3((unsigned)(p.slots * p.Hkv)), dim3(64), C::kLds, s, p);
+    const int64_t rows = p.total_q * p.Hq;
+    hipLaunchKernelGGL((k_attn_step_join<E>), dim3((unsigned)std::min<int64_t>(rows, 1 << 20)), dim3(64 * kJoinWaves), 0, s, p);
+    return hipGetLastError();
+}
+
+template <class E>
+hipError_t run_step_e(const AttnParams &p, hipStream_t s) {
+    if (p.D <= 32) return run_step<E, 32>(p, s);
+    if (p.D <= 64) return run_step<E, 64>(p, s);
+    return run_step<E, 128>(p, s);
+}
+
+}  // namespace
+
+bool plan_step(AttnParams &p) {
+    // few rows a sequence (they fit the 32 columns on average) over enough keys that a chunk is worth a join
+    if (p.total_q * p.grp > 32 * (int64_t)p.B || p.total_k <= 256 * (int64_t)p.B) return false;
+    // Four waves a compute unit are resident at once (registers at 128 dims in a half type). Where a chunk a wave
+    // keeps them all busy in one go, chunks have that length (8 sequences, 100000 keys in all, 2 heads: 35 us,
+    // against 46 us in one and a half goes); with sequences and heads enough by themselves, a third of a
+    // sequence (64 x 4096 keys, 8 heads: 243 us; a half 293 us, whole sequences 257 us).
+    const int64_t waves = 4 * (int64_t)device_num_cus(), own = (int64_t)p.B * p.Hkv;
+    int64_t chunk = 2 * own < waves ? (p.total_k * p.Hkv + waves - own - 1) / (waves - own) : (p.total_k / p.B + 2) / 3;
+    chunk = std::min<int64_t>(std::max<int64_t>((chunk + 31) / 32 * 32, 128), 1 << 20);
+    p.chunk = (int)chunk;
+    p.rcap = (int)std::min<int64_t>(32, (p.total_q + p.B - 1) / p.B * p.grp);
+    p.slots = p.total_k / chunk + p.B;
+    return true;
+}
+
+size_t step_workspace_bytes(const AttnParams &p) { return (size_t)p.slots * p.Hkv * p.rcap * (p.D + 2) * sizeof(float); }
+
+hipError_t launch_step(const AttnParams &p, eqlin_dtype_t dtype, hipStream_t s) {
+    if (dtype == EQLIN_F32) return run_step_e<F32>(p, s);
+    if (dtype == EQLIN_F16) return run_step_e<F16>(p, s);
+    return run_step_e<BF16>(p, s);
+}
+
+}  // namespace eqlin

@@ -37,6 +37,14 @@ __device__ __forceinline__ void dma_1k(uint32_t lds, const void *base, uint32_t 
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(lds), "v"(off), "s"(base) : "memory", "m0");
 }
 __device__ __forceinline__ void dma_wait() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+// All but the youngest N loads of the wave (they arrive in order).
+template <int N>
+__device__ __forceinline__ void dma_wait_but() {
+    static_assert(N < 64, "six bits");
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+// The wave's LDS reads so far have their values.
+__device__ __forceinline__ void lds_read_wait() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
 
 // A tile of ROWS rows, moved by the workgroup's WAVES waves. Chunks are permuted on the way (a lane fetches the
 // chunk that the swizzle puts at its place). Rows past the last valid one repeat it; columns from D on are
@@ -82,9 +90,10 @@ struct TileDma {
 };
 
 // Clears LDS where heads are padded to DP: the columns from D on stay zero.
+template <int THREADS = 256>
 __device__ __forceinline__ void zero_pad(char *lds, int bytes, int D, int DP, int tid) {
     if (D == DP) return;
-    for (int i = tid * 16; i < bytes; i += 256 * 16) *(uint4 *)(lds + i) = make_uint4(0, 0, 0, 0);
+    for (int i = tid * 16; i < bytes; i += THREADS * 16) *(uint4 *)(lds + i) = make_uint4(0, 0, 0, 0);
     __syncthreads();
 }
 

@@ -201,11 +201,15 @@ struct AttnParams {
     void *dq, *dk, *dv;
     int64_t dot, doh, dqt, dqh, dkt, dkh, dvt, dvh;
     float *ws;   // workspace
-    int chunk;   // keys a workgroup of the split kernel takes (0: not split)
+    int chunk, rcap;  // the step kernel: keys of a chunk, rows a chunk's partial result has room for
     int nsplit;  // key ranges the tile kernel's rows are split into
     int64_t slots;  // tile slots of a launch (a sequence's, then the next one's), and units a run of an XCD
     int run;
 };
+// Few rows over many keys (attn_step.hip): fills in the plan where that kernel is taken.
+bool plan_step(AttnParams &p);
+size_t step_workspace_bytes(const AttnParams &p);
+hipError_t launch_step(const AttnParams &p, eqlin_dtype_t dtype, hipStream_t s);
 size_t attention_workspace_bytes(const AttnParams &p, eqlin_dtype_t dtype);
 hipError_t launch_attention(const AttnParams &p, eqlin_dtype_t dtype, hipStream_t s);
 size_t attention_backward_workspace_bytes(const AttnParams &p);
