@@ -201,19 +201,17 @@ __device__ __forceinline__ int64_t clamp64(int64_t x, int64_t lo, int64_t hi) { 
 // the host.
 __device__ __forceinline__ int64_t slot_start(int64_t cu, int i, int mul, int size) { return cu * mul / size + i; }
 
-// The sequence of a slot and the slot's tile in it, by a 64-way search of the wave. The last level's lanes load
-// all that is asked of a sequence at once, so up to 64 sequences cost one round trip to memory. Every bound
-// is forced into the tensors whatever the arrays hold. BY_K: slots over the keys, else over the queries.
-template <bool BY_K>
-__device__ __forceinline__ Seq seq_of_slot(const AttnParams &p, int mul, int size, int64_t slot, int64_t &tile) {
+// The last sequence i with before(i, cu[i]) (true up to it, false after), by a 64-way search of the wave. The last
+// level's lanes load all that is asked of a sequence at once, so up to 64 sequences cost one round trip to memory.
+// Every bound is forced into the tensors whatever the arrays hold. BY_K: cu is the keys', else the queries'.
+template <bool BY_K, class Before>
+__device__ __forceinline__ Seq find_seq(const AttnParams &p, Before before, int &index) {
     const int lane = threadIdx.x & 63;
     const int *cu = BY_K ? p.cu_k : p.cu_q;
-    const int64_t total = BY_K ? p.total_k : p.total_q;
     int lo = 0, n = p.B;
     while (n > 64) {
-        const int step = (n + 63) / 64;
-        const int i = lo + lane * step;
-        const bool in = lane * step < n && slot_start(clamp64(cu[i < p.B ? i : p.B], 0, total), i, mul, size) <= slot;
+        const int step = (n + 63) / 64, i = lo + lane * step;
+        const bool in = lane * step < n && before(i, cu[i < p.B ? i : p.B]);
         int c = __popcll(__ballot(in));
         c = c < 1 ? 1 : c;
         const int skip = (c - 1) * step;
@@ -222,45 +220,34 @@ __device__ __forceinline__ Seq seq_of_slot(const AttnParams &p, int mul, int siz
     }
     const int i = lo + (lane < n ? lane : n - 1);
     const int q0 = p.cu_q[i], q1 = p.cu_q[i + 1], k0 = p.cu_k[i], k1 = p.cu_k[i + 1], len = p.len_k ? p.len_k[i] : 0x7fffffff;
-    const bool in = lane < n && slot_start(clamp64(BY_K ? k0 : q0, 0, total), i, mul, size) <= slot;
+    const bool in = lane < n && before(i, BY_K ? k0 : q0);
     int c = __popcll(__ballot(in));
     c = uniform(c < 1 ? 0 : c - 1);
-    const int uq0 = __builtin_amdgcn_readlane(q0, c), uq1 = __builtin_amdgcn_readlane(q1, c);
-    const int uk0 = __builtin_amdgcn_readlane(k0, c), uk1 = __builtin_amdgcn_readlane(k1, c);
-    const int ulen = __builtin_amdgcn_readlane(len, c);
-    auto clamp = [](int x, int lo, int hi) { return min(max(x, lo), hi); };
+    index = uniform(lo) + c;
+    auto clamp = [](int x, int a, int b) { return min(max(x, a), b); };
+    const int q_at = clamp(__builtin_amdgcn_readlane(q0, c), 0, (int)p.total_q);
+    const int k_at = clamp(__builtin_amdgcn_readlane(k0, c), 0, (int)p.total_k);
     Seq s;
-    const int q_at = clamp(uq0, 0, (int)p.total_q), k_at = clamp(uk0, 0, (int)p.total_k);
     s.q0 = q_at, s.k0 = k_at;
-    s.lq = clamp(uq1, q_at, (int)p.total_q) - q_at;
-    s.lk_slot = clamp(uk1, k_at, (int)p.total_k) - k_at;
-    s.lk = clamp(ulen, 0, s.lk_slot);
-    tile = slot - slot_start(BY_K ? s.k0 : s.q0, uniform(lo) + c, mul, size);
+    s.lq = clamp(__builtin_amdgcn_readlane(q1, c), q_at, (int)p.total_q) - q_at;
+    s.lk_slot = clamp(__builtin_amdgcn_readlane(k1, c), k_at, (int)p.total_k) - k_at;
+    s.lk = clamp(__builtin_amdgcn_readlane(len, c), 0, s.lk_slot);
     return s;
 }
 
-// The sequence of packed query token t (the last that begins at or before it), with its index.
-__device__ __forceinline__ Seq seq_of_row(const AttnParams &p, int t, int &index) {
-    const int lane = threadIdx.x & 63;
-    int lo = 0, n = p.B;
-    while (n > 1) {
-        const int step = (n + 63) / 64, i = lo + lane * step;
-        const bool in = lane * step < n && p.cu_q[i < p.B ? i : p.B] <= t;
-        int c = __popcll(__ballot(in));
-        c = c < 1 ? 1 : c;
-        const int skip = (c - 1) * step;
-        lo += skip;
-        n = n - skip < step ? n - skip : step;
-    }
-    index = uniform(lo);
-    auto clamp = [](int x, int a, int b) { return min(max(x, a), b); };
-    Seq s;
-    const int q0 = clamp(p.cu_q[index], 0, (int)p.total_q), k0 = clamp(p.cu_k[index], 0, (int)p.total_k);
-    s.q0 = q0, s.k0 = k0;
-    s.lq = clamp(p.cu_q[index + 1], q0, (int)p.total_q) - q0;
-    s.lk_slot = clamp(p.cu_k[index + 1], k0, (int)p.total_k) - k0;
-    s.lk = p.len_k ? clamp(p.len_k[index], 0, s.lk_slot) : s.lk_slot;
+// The sequence of a slot and the slot's tile in it. BY_K: slots over the keys, else over the queries.
+template <bool BY_K>
+__device__ __forceinline__ Seq seq_of_slot(const AttnParams &p, int mul, int size, int64_t slot, int64_t &tile) {
+    const int64_t total = BY_K ? p.total_k : p.total_q;
+    int i;
+    const Seq s = find_seq<BY_K>(p, [&](int j, int cu) { return slot_start(clamp64(cu, 0, total), j, mul, size) <= slot; }, i);
+    tile = slot - slot_start(BY_K ? s.k0 : s.q0, i, mul, size);
     return s;
+}
+
+// The sequence of packed query token t (the last that begins at or before it).
+__device__ __forceinline__ Seq seq_of_row(const AttnParams &p, int t, int &index) {
+    return find_seq<false>(p, [&](int, int cu) { return cu <= t; }, index);
 }
 
 // packed row -> token (rows are below 2^31; most groups are powers of two)

@@ -13,34 +13,6 @@ namespace eqlin {
 
 namespace {
 
-// delta[token][head] = sum over d of dO O: 16 lanes a row.
-template <class E>
-__global__ void __launch_bounds__(256) k_attn_delta(const AttnParams p) {
-    typedef Elem<E> EL;
-    typedef typename EL::T T;
-    const int64_t rows = p.total_q * p.Hq;
-    const int l = threadIdx.x & 15;
-    for (int64_t at0 = (int64_t)blockIdx.x * 16; at0 < rows; at0 += (int64_t)gridDim.x * 16) {
-    const int64_t at = at0 + (threadIdx.x >> 4);
-    float sum = 0.0f;
-    if (at < rows) {
-        const int64_t tok = at / p.Hq;
-        const int hq = (int)(at - tok * p.Hq);
-        const T *o = (const T *)p.o + tok * p.ot + hq * p.oh, *g = (const T *)p.dout + tok * p.dot + hq * p.doh;
-        for (int e = l * EL::V; e < p.D; e += 16 * EL::V) {
-            float a[EL::V], b[EL::V];
-            EL::unpack(*(const uint4 *)(o + e), a);
-            EL::unpack(*(const uint4 *)(g + e), b);
-#pragma unroll
-            for (int j = 0; j < EL::V; ++j) sum = fmaf(a[j], b[j], sum);
-        }
-    }
-#pragma unroll
-    for (int m = 8; m >= 1; m >>= 1) sum += __shfl_xor(sum, m);
-    if (at < rows && l == 0) p.ws[at] = sum;
-    }
-}
-
 // ---- dQ: as the forward, 32 rows a wave (columns), key tiles through LDS ----
 
 template <class E, int DP, int NKB>
@@ -110,7 +82,23 @@ __global__ void __launch_bounds__(256, __is_same(E, F32) ? 1 : 2) k_attn_dq(cons
     uint4 qf[TL::kSteps], gf[TL::kSteps];
     load_row<E, DP>(qf, (const T *)p.q + (sq.q0 + r.tok) * p.qt + r.hq * p.qh, p.D, h);
     load_row<E, DP>(gf, (const T *)p.dout + (sq.q0 + r.tok) * p.dot + r.hq * p.doh, p.D, h);
-    const float lse2 = p.lse[at] * kLog2e, delta = p.ws[at];
+    const float lse2 = p.lse[at] * kLog2e;
+    // delta = sum over d of dO O, here and for the other pass
+    float delta = 0.0f;
+    {
+        uint4 of[TL::kSteps];
+        load_row<E, DP>(of, (const T *)p.o + (sq.q0 + r.tok) * p.ot + r.hq * p.oh, p.D, h);
+#pragma unroll
+        for (int t = 0; t < TL::kSteps; ++t) {
+            float a[Elem<E>::V], b[Elem<E>::V];
+            Elem<E>::unpack(of[t], a);
+            Elem<E>::unpack(gf[t], b);
+#pragma unroll
+            for (int j = 0; j < Elem<E>::V; ++j) delta = fmaf(a[j], b[j], delta);
+        }
+        delta = half_sum(delta);
+        if (r.live && h == 0) p.ws[at] = delta;
+    }
     f32x16 dq[DP / 32];
 #pragma unroll
     for (int db = 0; db < DP / 32; ++db) dq[db] = zero16();
@@ -137,6 +125,9 @@ __global__ void __launch_bounds__(256, __is_same(E, F32) ? 1 : 2) k_attn_dq(cons
     }
     if (r.live) store_column<E, DP>(dq, p.scale, (T *)p.dq + (sq.q0 + r.tok) * p.dqt + r.hq * p.dqh, p.D, h);
 }
+
+// the shares of dk and dv lie behind delta in the workspace
+__host__ __device__ __forceinline__ int64_t share_offset(const AttnParams &p) { return (p.total_q * p.Hq + 63) / 64 * 64; }
 
 // ---- dK, dV: 32 keys a wave (columns), tiles of packed rows (q and dO) through LDS ----
 
@@ -212,8 +203,9 @@ __global__ void __launch_bounds__(256, __is_same(E, F32) || DP > 64 ? 1 : 2) k_a
     typedef typename ElemOf<E>::type T;
     extern __shared__ __align__(16) char lds[];
     const int tid = threadIdx.x, lane = tid & 63, wave = uniform(tid >> 6), h = lane >> 5;
-    int hk;
-    const int64_t slot = xcd_slot(blockIdx.x, p.Hkv, p.run, hk);  // causal: a sequence's first keys have most rows
+    int hz;
+    const int64_t slot = xcd_slot(blockIdx.x, p.Hkv * p.nsplit, p.run, hz);  // causal: a sequence's first keys have most rows
+    const int hk = hz % p.Hkv, z = hz / p.Hkv;
     if (slot >= p.slots) return;
     int64_t tile;
     const Seq sq = seq_of_slot<true>(p, 1, C::BK, slot, tile);
@@ -229,10 +221,17 @@ __global__ void __launch_bounds__(256, __is_same(E, F32) || DP > 64 ? 1 : 2) k_a
 #pragma unroll
     for (int db = 0; db < DP / 32; ++db) dk[db] = zero16(), dv[db] = zero16();
     const float c = p.scale * kLog2e;
-    const int64_t row_end = key_wg < sq.lk ? (int64_t)sq.lq * p.grp : 0;
+    const int64_t rows = key_wg < sq.lk ? (int64_t)sq.lq * p.grp : 0;
     // causal: the first token that sees the workgroup's first key
     int64_t row_beg = p.causal && key_wg > off ? (key_wg - off) * p.grp : 0;
     row_beg -= row_beg % C::BR;
+    // this workgroup's share of the rows, in whole tiles
+    int64_t row_end = rows;
+    if (p.nsplit > 1 && row_beg < rows) {
+        const int64_t tiles = (rows - row_beg + C::BR - 1) / C::BR;
+        row_end = min(rows, row_beg + tiles * (z + 1) / p.nsplit * C::BR);
+        row_beg += tiles * z / p.nsplit * C::BR;
+    }
     const T *qg = (const T *)p.q + sq.q0 * p.qt + (int64_t)hk * p.grp * p.qh;
     const T *gg = (const T *)p.dout + sq.q0 * p.dot + (int64_t)hk * p.grp * p.doh;
     const float *lse = p.lse + sq.q0 * p.Hq + hk * p.grp, *del = p.ws + sq.q0 * p.Hq + hk * p.grp;
@@ -290,10 +289,51 @@ __global__ void __launch_bounds__(256, __is_same(E, F32) || DP > 64 ? 1 : 2) k_a
         if (more) store(buf ^ 1);
         buf ^= 1;
     }
-    if (key < sq.lk_slot) {  // keys beyond the sequence's length in its slot get zeros
-        store_column<E, DP>(dk, p.scale, (T *)p.dk + (sq.k0 + key) * p.dkt + hk * p.dkh, p.D, h);
-        store_column<E, DP>(dv, 1.0f, (T *)p.dv + (sq.k0 + key) * p.dvt + hk * p.dvh, p.D, h);
+    if (key >= sq.lk_slot) return;
+    if (p.nsplit > 1) {  // a share: fp32, for k_attn_dkv_sum
+        const int64_t heads = p.total_k * p.Hkv, at = (sq.k0 + key) * p.Hkv + hk;
+        float *part = p.ws + share_offset(p);
+        store_column<F32, DP>(dk, p.scale, part + (z * heads + at) * p.D, p.D, h);
+        store_column<F32, DP>(dv, 1.0f, part + ((p.nsplit + z) * heads + at) * p.D, p.D, h);
+        return;
     }
+    // keys beyond the sequence's length in its slot get zeros
+    store_column<E, DP>(dk, p.scale, (T *)p.dk + (sq.k0 + key) * p.dkt + hk * p.dkh, p.D, h);
+    store_column<E, DP>(dv, 1.0f, (T *)p.dv + (sq.k0 + key) * p.dvt + hk * p.dvh, p.D, h);
+}
+
+// dk and dv of the shares, in order: four values a thread.
+template <class E>
+__global__ void __launch_bounds__(256) k_attn_dkv_sum(const AttnParams p) {
+    typedef typename ElemOf<E>::type T;
+    const int per = p.D / 4;
+    const int64_t heads = p.total_k * p.Hkv, n = heads * per;
+    const float *part = p.ws + share_offset(p);
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < 2 * n; i += (int64_t)gridDim.x * 256) {
+        const bool v = i >= n;
+        const int64_t e = v ? i - n : i, at = e / per;
+        const int d = (int)(e - at * per) * 4;
+        const float *src = part + (v ? p.nsplit * heads * p.D : 0) + at * p.D + d;
+        float4 s = *(const float4 *)src;
+        for (int z = 1; z < p.nsplit; ++z) {
+            const float4 a = *(const float4 *)(src + z * heads * p.D);
+            s.x += a.x, s.y += a.y, s.z += a.z, s.w += a.w;
+        }
+        const int64_t key = at / p.Hkv;
+        const int hk = (int)(at - key * p.Hkv);
+        T *dst = v ? (T *)p.dv + key * p.dvt + hk * p.dvh + d : (T *)p.dk + key * p.dkt + hk * p.dkh + d;
+        if constexpr (__is_same(E, F32)) *(float4 *)dst = s;
+        else *(uint2 *)dst = make_uint2(pack2<E>(s.x, s.y), pack2<E>(s.z, s.w));
+    }
+}
+
+// Shares that the rows of a key tile are split into, where the key tiles alone do not fill the card: a tile of a
+// causal sequence's first keys with grouped heads has thousands of rows, and one workgroup with them all is the
+// launch's whole time (4 sequences up to 4096, 16 heads on 4: 886 us in one share).
+int pick_shares(const AttnParams &p) {
+    const int64_t wgs = (p.total_k / 128 + p.B) * p.Hkv, want = 4 * (int64_t)device_num_cus();
+    const int64_t rows = p.total_q * p.grp / std::max(1, p.B);  // of a sequence on average
+    return (int)std::min<int64_t>(std::min<int64_t>(want / std::max<int64_t>(1, wgs), rows / 512), 8);
 }
 
 template <class K>
@@ -311,7 +351,6 @@ hipError_t run_bwd(const AttnParams &p0, hipStream_t s) {
     if (e == hipSuccess) e = set_lds(k_attn_dkv<E, DP>, CK::kLds);
     if (e != hipSuccess) return e;
     if (p.total_q > 0) {
-        hipLaunchKernelGGL((k_attn_delta<E>), dim3((unsigned)std::min<int64_t>((p.total_q * p.Hq + 15) / 16, 1 << 20)), dim3(256), 0, s, p);
         p.slots = p.total_q * p.grp / CQ::BM + p.B;
         p.run = run_of(p.slots, p.B);
         hipLaunchKernelGGL((k_attn_dq<E, DP>), dim3((unsigned)xcd_grid(p.slots, p.Hkv, p.run)), dim3(256), CQ::kLds, s, p);
@@ -319,7 +358,12 @@ hipError_t run_bwd(const AttnParams &p0, hipStream_t s) {
     if (p.total_k > 0) {
         p.slots = p.total_k / CK::BK + p.B;
         p.run = run_of(p.slots, p.B);
-        hipLaunchKernelGGL((k_attn_dkv<E, DP>), dim3((unsigned)xcd_grid(p.slots, p.Hkv, p.run)), dim3(256), CK::kLds, s, p);
+        p.nsplit = std::max(1, pick_shares(p));
+        hipLaunchKernelGGL((k_attn_dkv<E, DP>), dim3((unsigned)xcd_grid(p.slots, p.Hkv * p.nsplit, p.run)), dim3(256), CK::kLds, s, p);
+        if (p.nsplit > 1) {
+            const int64_t n = p.total_k * p.Hkv * (p.D / 4) * 2;
+            hipLaunchKernelGGL((k_attn_dkv_sum<E>), dim3((unsigned)std::min<int64_t>((n + 255) / 256, 1 << 16)), dim3(256), 0, s, p);
+        }
     }
     return hipGetLastError();
 }
@@ -333,7 +377,12 @@ hipError_t run_bwd_e(const AttnParams &p, hipStream_t s) {
 
 }  // namespace
 
-size_t attention_backward_workspace_bytes(const AttnParams &p) { return (size_t)p.total_q * p.Hq * sizeof(float); }
+size_t attention_backward_workspace_bytes(const AttnParams &p) {
+    if (p.B <= 0) return 0;
+    const int n = pick_shares(p);
+    const size_t shares = n > 1 ? (size_t)2 * n * p.total_k * p.Hkv * p.D : 0;
+    return ((size_t)share_offset(p) + shares) * sizeof(float);
+}
 
 hipError_t launch_attention_backward(const AttnParams &p, eqlin_dtype_t dtype, hipStream_t s) {
     if (dtype == EQLIN_F32) return run_bwd_e<F32>(p, s);

@@ -108,7 +108,7 @@ constexpr int kJoinWaves = 16;
 template <class E>
 __global__ void __launch_bounds__(64 * kJoinWaves) k_attn_step_join(const AttnParams p) {
     typedef typename ElemOf<E>::type T;
-    __shared__ float so[kJoinWaves][128], sm[kJoinWaves], sl[kJoinWaves];
+    __shared__ float2 so[kJoinWaves][64], sml[kJoinWaves];
     const int lane = threadIdx.x & 63, wave = uniform((int)(threadIdx.x >> 6));
     const int64_t rows = p.total_q * p.Hq;
     for (int64_t at = blockIdx.x; at < rows; at += gridDim.x) {
@@ -121,40 +121,60 @@ __global__ void __launch_bounds__(64 * kJoinWaves) k_attn_step_join(const AttnPa
         if (chunks == 1 || (nr > p.rcap && chunks > 0)) continue;  // written by the step itself
         const int64_t slot0 = slot_start(sq.k0, seq, 1, p.chunk);
         const int64_t base = (slot0 * p.Hkv + hk) * p.rcap + tok * p.grp + (hq - hk * p.grp), step = (int64_t)p.Hkv * p.rcap;
-        const float *ml = p.ws + p.slots * p.Hkv * p.rcap * p.D;
-        float m = -INFINITY;
-        for (int z = wave * 64 + lane; z < chunks; z += 64 * kJoinWaves) m = fmaxf(m, ml[(base + z * step) * 2]);
-        m = wave_max(m);
-        __syncthreads();
-        if (lane == 0) sm[wave] = m;
-        __syncthreads();
+        const float2 *ml = (const float2 *)(p.ws + p.slots * p.Hkv * p.rcap * p.D);
+        // each wave joins its own chunks (their loads wait for nothing), then the waves join
+        constexpr int N = 8;
+        float m = -INFINITY, l = 0.0f;
+        float2 o = make_float2(0.0f, 0.0f);
+        const bool mine = 2 * lane < p.D;
+        for (int z0 = wave; z0 < chunks; z0 += N * kJoinWaves) {
+            float2 st[N], v[N];
 #pragma unroll
-        for (int w = 0; w < kJoinWaves; ++w) m = fmaxf(m, sm[w]);
-        const float mm = m == -INFINITY ? 0.0f : m;
-        float l = 0.0f, o0 = 0.0f, o1 = 0.0f;
-#pragma unroll 4
-        for (int z = wave; z < chunks; z += kJoinWaves) {
-            const int64_t i = base + z * step;
-            const float w = __builtin_amdgcn_exp2f(ml[i * 2] - mm);
-            l = fmaf(w, ml[i * 2 + 1], l);
-            if (lane < p.D) o0 = fmaf(w, p.ws[i * p.D + lane], o0);
-            if (lane + 64 < p.D) o1 = fmaf(w, p.ws[i * p.D + 64 + lane], o1);
+            for (int j = 0; j < N; ++j) {
+                const int z = z0 + j * kJoinWaves;
+                const int64_t i = base + min(z, chunks - 1) * step;
+                st[j] = z < chunks ? ml[i] : make_float2(-INFINITY, 0.0f);
+                v[j] = z < chunks && mine ? *(const float2 *)(p.ws + i * p.D + 2 * lane) : make_float2(0.0f, 0.0f);
+            }
+            float mn = m;
+#pragma unroll
+            for (int j = 0; j < N; ++j) mn = fmaxf(mn, st[j].x);
+            const float mm = mn == -INFINITY ? 0.0f : mn, a = __builtin_amdgcn_exp2f(m - mm);
+            l *= a, o.x *= a, o.y *= a;
+            m = mn;
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+                const float w = __builtin_amdgcn_exp2f(st[j].x - mm);
+                l = fmaf(w, st[j].y, l);
+                o.x = fmaf(w, v[j].x, o.x);
+                o.y = fmaf(w, v[j].y, o.y);
+            }
         }
-        so[wave][lane] = o0;
-        so[wave][lane + 64] = o1;
-        if (lane == 0) sl[wave] = l;
         __syncthreads();
-        if (threadIdx.x < 128) {
-            l = 0.0f, o0 = 0.0f;
+        so[wave][lane] = o;
+        if (lane == 0) sml[wave] = make_float2(m, l);
+        __syncthreads();
+        if (wave == 0) {
+            float mx = -INFINITY, total = 0.0f;
+            float2 sum = make_float2(0.0f, 0.0f);
+#pragma unroll
+            for (int w = 0; w < kJoinWaves; ++w) mx = fmaxf(mx, sml[w].x);
+            const float mm = mx == -INFINITY ? 0.0f : mx;
 #pragma unroll
             for (int w = 0; w < kJoinWaves; ++w) {
-                l += sl[w];
-                o0 += so[w][threadIdx.x];
+                const float a = __builtin_amdgcn_exp2f(sml[w].x - mm);
+                total = fmaf(a, sml[w].y, total);
+                sum.x = fmaf(a, so[w][lane].x, sum.x);
+                sum.y = fmaf(a, so[w][lane].y, sum.y);
             }
             const bool empty = last < 0 || sq.lk == 0;
-            if ((int)threadIdx.x < p.D)
-                ((T *)p.o + tok_at * p.ot + hq * p.oh)[threadIdx.x] = Elem<E>::put(empty ? 0.0f : o0 / l);
-            if (p.lse && threadIdx.x == 0) p.lse[at] = empty ? -INFINITY : m * kLn2 + logf(l);
+            const float inv = empty ? 0.0f : 1.0f / total;
+            T *dst = (T *)p.o + tok_at * p.ot + hq * p.oh + 2 * lane;
+            if (mine) {
+                if constexpr (__is_same(E, F32)) *(float2 *)dst = make_float2(sum.x * inv, sum.y * inv);
+                else *(uint32_t *)dst = pack2<E>(sum.x * inv, sum.y * inv);
+            }
+            if (p.lse && lane == 0) p.lse[at] = empty ? -INFINITY : mx * kLn2 + logf(total);
         }
     }
 }
