@@ -31,7 +31,8 @@ CXXFLAGS = [
 # Per-file device flags. fwd_res8.hip: matrix-core results in ordinary vector registers (the weight ring
 # and plane operands, which loads can fill directly, take the accumulator registers instead), so the
 # epilogue reads its eleven accumulators without a copy per value and no register is spilled.
-FILE_FLAGS = {"fwd_res8.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"], "attn_step.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
+# The attention kernels: matrix-core results in ordinary vector registers too, where the softmax reads every one.
+FILE_FLAGS = {f: ["-mllvm", "-amdgpu-mfma-vgpr-form"] for f in ("fwd_res8.hip", "attn_fwd.hip", "attn_step.hip", "attn_bwd.hip")}
 SOURCES = ["eqlin_api.cpp", "prepare.hip", "fwd_bf16.hip", "fwd_big.hip", "fwd_res.hip", "fwd_res8.hip", "fwd_f32.hip", "bwd.hip", "conv.hip",
            "stage_api.cpp", "norm.hip", "rotary.hip", "attn_fwd.hip", "attn_step.hip", "attn_bwd.hip"]
 

@@ -172,18 +172,19 @@ __device__ __forceinline__ int64_t uniform(int64_t x) {
 // D-layout row of value v for lane half h
 __device__ __forceinline__ constexpr int d_row(int v, int h) { return (v & 3) + 8 * (v >> 2) + 4 * h; }
 
-// Order of a block that multiplies LDS fragments: AHEAD reads first, then one read a product, so that no product
-// waits for its own read (left alone, the compiler reuses one register quad: read, wait, multiply).
+// Order of a block that multiplies LDS fragments: AHEAD reads first, then the others spread over the products, so
+// that no product waits for its own read (left alone, the compiler reuses one register quad: read, wait, multiply).
 template <int READS, int PRODUCTS, int AHEAD>
 __device__ __forceinline__ void read_ahead() {
-    constexpr int kRead = 0x100, kMfma = 0x8, kPer = PRODUCTS / READS > 0 ? PRODUCTS / READS : 1;
+    constexpr int kRead = 0x100, kMfma = 0x8, kPer = READS / PRODUCTS;  // reads a product
+    static_assert(READS % PRODUCTS == 0 && AHEAD % kPer == 0 && AHEAD <= READS, "whole products");
     __builtin_amdgcn_sched_group_barrier(kRead, AHEAD, 0);
 #pragma unroll
-    for (int i = 0; i < READS - AHEAD; ++i) {
-        __builtin_amdgcn_sched_group_barrier(kMfma, kPer, 0);
-        __builtin_amdgcn_sched_group_barrier(kRead, 1, 0);
+    for (int i = 0; i < PRODUCTS - AHEAD / kPer; ++i) {
+        __builtin_amdgcn_sched_group_barrier(kMfma, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(kRead, kPer, 0);
     }
-    __builtin_amdgcn_sched_group_barrier(kMfma, PRODUCTS - kPer * (READS - AHEAD), 0);
+    __builtin_amdgcn_sched_group_barrier(kMfma, AHEAD / kPer, 0);
 }
 
 // ---- sequences ----

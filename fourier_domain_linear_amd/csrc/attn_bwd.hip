@@ -131,29 +131,56 @@ __host__ __device__ __forceinline__ int64_t share_offset(const AttnParams &p) { 
 
 // ---- dK, dV: 32 keys a wave (columns), tiles of packed rows (q and dO) through LDS ----
 
+// One group of the products that reduce over the tile's rows: the DP / 32 A fragments of reduction step f.
+template <class E, int DP>
+struct ColGroup {
+    uint4 a[DP / 32];
+    __device__ __forceinline__ void load(uint32_t tile, const typename Tile<E, DP>::Lane &L, int blk, int f) {
+#pragma unroll
+        for (int db = 0; db < DP / 32; ++db) a[db] = Tile<E, DP>::col_frag(tile, L, blk, f, db);
+    }
+    __device__ __forceinline__ void multiply(f32x16 *acc, const uint4 &w) const {
+#pragma unroll
+        for (int db = 0; db < DP / 32; ++db) acc[db] = mma_frag<E>(a[db], w, acc[db]);
+    }
+};
+
 template <class E, int DP, int NRB>
 __device__ __forceinline__ void dkv_block(f32x16 *dk, f32x16 *dv, const uint4 *kf, const uint4 *vf,
                                           const typename Tile<E, DP>::Lane &L, uint32_t qt, uint32_t gt, uint32_t stats, float c,
                                           bool masked, int key, int h) {
     typedef Tile<E, DP> TL;
-    constexpr int BR = 32 * NRB;
+    constexpr int BR = 32 * NRB, NF = WFrags<E>::NF;
 #pragma unroll
     for (int rb = 0; rb < NRB; ++rb) {
+        const uint32_t at = stats + 16 * h + 32 * rb * 4;
         f32x16 s = zero16(), dp = zero16();
+        f32x4 ls[4], de[4];
+        uint4 qa[TL::kSteps], ga[TL::kSteps];
 #pragma unroll
         for (int t = 0; t < TL::kSteps; ++t) {
-            s = mma_frag<E>(TL::row_frag(qt, L, rb, t), kf[t], s);
-            dp = mma_frag<E>(TL::row_frag(gt, L, rb, t), vf[t], dp);
+            qa[t] = TL::row_frag(qt, L, rb, t);
+            ga[t] = TL::row_frag(gt, L, rb, t);
         }
-        const uint32_t at = stats + 16 * h + 32 * rb * 4;
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
-            const f32x4 ls = TL::template lds_at<f32x4>(at + 32 * g), de = TL::template lds_at<f32x4>(at + 32 * g + BR * 4);
+            ls[g] = TL::template lds_at<f32x4>(at + 32 * g);
+            de[g] = TL::template lds_at<f32x4>(at + 32 * g + BR * 4);
+        }
+#pragma unroll
+        for (int t = 0; t < TL::kSteps; ++t) {
+            s = mma_frag<E>(qa[t], kf[t], s);
+            dp = mma_frag<E>(ga[t], vf[t], dp);
+        }
+        ColGroup<E, DP> g0, g1;
+        g0.load(gt, L, rb, 0);
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const int v = 4 * g + j;
-                s[v] = __builtin_amdgcn_exp2f(fmaf(s[v], c, -ls[j]));
-                dp[v] = s[v] * (dp[v] - de[j]);
+                s[v] = __builtin_amdgcn_exp2f(fmaf(s[v], c, -ls[g][j]));
+                dp[v] = s[v] * (dp[v] - de[g][j]);
             }
         }
         if (masked) {
@@ -169,19 +196,16 @@ __device__ __forceinline__ void dkv_block(f32x16 *dk, f32x16 *dv, const uint4 *k
                 }
             }
         }
-        WFrags<E> w;
+        WFrags<E> w, w2;
         w.set(s);
+        w2.set(dp);
 #pragma unroll
-        for (int f = 0; f < WFrags<E>::NF; ++f)
-#pragma unroll
-            for (int db = 0; db < DP / 32; ++db)
-                dv[db] = mma_frag<E>(TL::col_frag(gt, L, rb, f, db), w.f[f], dv[db]);
-        w.set(dp);
-#pragma unroll
-        for (int f = 0; f < WFrags<E>::NF; ++f)
-#pragma unroll
-            for (int db = 0; db < DP / 32; ++db)
-                dk[db] = mma_frag<E>(TL::col_frag(qt, L, rb, f, db), w.f[f], dk[db]);
+        for (int i = 0; i < 2 * NF; ++i) {  // dv over dO's fragments, then dk over q's
+            if (i + 1 < 2 * NF) g1.load(i + 1 < NF ? gt : qt, L, rb, (i + 1) % NF);
+            if (i < NF) g0.multiply(dv, w.f[i]);
+            else g0.multiply(dk, w2.f[i - NF]);
+            g0 = g1;
+        }
     }
 }
 
@@ -329,9 +353,9 @@ __global__ void __launch_bounds__(256) k_attn_dkv_sum(const AttnParams p) {
 
 // Shares that the rows of a key tile are split into, where the key tiles alone do not fill the card: a tile of a
 // causal sequence's first keys with grouped heads has thousands of rows, and one workgroup with them all is the
-// launch's whole time (4 sequences up to 4096, 16 heads on 4: 886 us in one share).
+// launch's whole time (4 sequences up to 4096, 16 heads on 4: 975 us in one share, 947 in 3, 888 in 6).
 int pick_shares(const AttnParams &p) {
-    const int64_t wgs = (p.total_k / 128 + p.B) * p.Hkv, want = 4 * (int64_t)device_num_cus();
+    const int64_t wgs = (p.total_k / 128 + p.B) * p.Hkv, want = 8 * (int64_t)device_num_cus();
     const int64_t rows = p.total_q * p.grp / std::max(1, p.B);  // of a sequence on average
     return (int)std::min<int64_t>(std::min<int64_t>(want / std::max<int64_t>(1, wgs), rows / 512), 8);
 }
