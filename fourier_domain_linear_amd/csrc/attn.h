@@ -264,6 +264,7 @@ struct Rows {
     int wave_min;        // the least `last` of the wave's live rows: tiles wholly up to it need no mask
     int wave_max;        // the largest, -1: the wave has no work
     int k_end;           // keys that some row of the workgroup sees
+    int all;             // the last key that every row of the workgroup sees
 };
 __device__ __forceinline__ Rows rows_of(const AttnParams &p, const Seq &sq, int hk, int row_wg, int BM, int wave, int lane) {
     Rows r;
@@ -279,6 +280,7 @@ __device__ __forceinline__ Rows rows_of(const AttnParams &p, const Seq &sq, int 
     if (first + 32 > end) r.wave_min = -1;  // rows past the end see nothing
     r.wave_max = first < end ? last_of(min(first + 31, end - 1)) : -1;
     r.k_end = last_of(min(row_wg + BM, end) - 1) + 1;
+    r.all = last_of(row_wg);
     return r;
 }
 

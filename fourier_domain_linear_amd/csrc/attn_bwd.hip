@@ -105,10 +105,23 @@ __global__ void __launch_bounds__(256, __is_same(E, F32) ? 1 : 2) k_attn_dq(cons
     const float c = p.scale * kLog2e;
     const typename TL::Lane L = TL::lane_of(lane);
     int buf = 0;
+    int *flags = (int *)(lds + C::kLds);
+    bool bad = false;  // some tile was cleared
     auto arrive = [&](int k0) {
         dma_wait();
         __syncthreads();  // this tile is in LDS; the other buffer has no more readers
         if (k0 + C::BN < r.k_end) fetch(k0 + C::BN, buf ^ 1);
+        if (k0 + C::BN - 1 > r.all) {  // some row sees only part of it (uniform in the workgroup)
+            char *kt = lds + 2 * buf * C::kTileBytes;
+            const bool mine = __any(tile_nonfinite<E, 256>(kt, C::kTileBytes, tid));
+            if (lane == 0) flags[4 * buf + wave] = mine;
+            __syncthreads();
+            if (uniform(flags[4 * buf] | flags[4 * buf + 1] | flags[4 * buf + 2] | flags[4 * buf + 3])) {
+                bad = true;
+                clear_nonfinite<E, 256>(kt, C::kTileBytes, tid);
+                __syncthreads();
+            }
+        }
     };
     if (r.wave_max >= 0) {
         for (int k0 = 0; k0 < r.k_end; k0 += C::BN) {
@@ -123,6 +136,9 @@ __global__ void __launch_bounds__(256, __is_same(E, F32) ? 1 : 2) k_attn_dq(cons
             buf ^= 1;
         }
     }
+    if (bad)
+        poison_columns<E, DP>(dq, max(0, r.all + 1) / C::BN * C::BN, min(r.wave_max, r.k_end - 1), p.D, h,
+                              [&](int j) { return kg + (int64_t)j * p.kt; }, [&](int j) { return j <= r.last; });
     if (r.live) store_column<E, DP>(dq, p.scale, (T *)p.dq + (sq.q0 + r.tok) * p.dqt + r.hq * p.dqh, p.D, h);
 }
 
@@ -217,7 +233,8 @@ struct DkvCfg {
     static constexpr int BR = 32 * NRB;  // packed rows of a tile
     static constexpr int kTileBytes = BR * TL::kRow;
     static constexpr int kStats = 3 * BR * 4;                    // lse, delta, last key of each row
-    static constexpr int kLds = 4 * kTileBytes + 2 * kStats;     // q and dO, two buffers; then the rows' values
+    static constexpr int kFlags = 4 * 4;                         // a word a wave
+    static constexpr int kLds = 4 * kTileBytes + 2 * (kStats + kFlags);  // q and dO, two buffers; then the rows' values
 };
 
 template <class E, int DP>
@@ -286,7 +303,7 @@ __global__ void __launch_bounds__(256, __is_same(E, F32) || DP > 64 ? 1 : 2) k_a
     };
     auto store = [&](int buf) {
         if (tid < C::BR) {
-            float *f = (float *)(lds + 4 * C::kTileBytes + buf * C::kStats);
+            float *f = (float *)(lds + 4 * C::kTileBytes + buf * (C::kStats + C::kFlags));
             f[tid] = st_lse;
             f[C::BR + tid] = st_del;
             ((int *)f)[2 * C::BR + tid] = st_last;
@@ -301,19 +318,46 @@ __global__ void __launch_bounds__(256, __is_same(E, F32) || DP > 64 ? 1 : 2) k_a
     }
     int buf = 0;
     const int wave_last = (int)key_wg + wave * 32 + 31;  // the wave's last key
+    const int wg_last = min((int)key_wg + C::BK, sq.lk) - 1;  // the workgroup's last key that counts
+    int bad_from = -1, bad_to = -1;  // rows of tiles that were cleared
     for (int64_t r0 = row_beg; r0 < row_end; r0 += C::BR) {
         dma_wait();
         __syncthreads();
         const bool more = r0 + C::BR < row_end;
         if (more) load(r0 + C::BR, buf ^ 1);
-        const uint32_t qt = lds0 + 2 * buf * C::kTileBytes, gt = qt + C::kTileBytes, stats = lds0 + 4 * C::kTileBytes + buf * C::kStats;
+        const uint32_t qt = lds0 + 2 * buf * C::kTileBytes, gt = qt + C::kTileBytes, stats = lds0 + 4 * C::kTileBytes + buf * (C::kStats + C::kFlags);
         // rows see a prefix of the keys, longer for later rows: the tile's first row decides
-        const bool whole = uniform(TL::template lds_at<int>(stats + 2 * C::BR * 4)) >= wave_last && r0 + C::BR <= row_end;
+        const int first_sees = uniform(TL::template lds_at<int>(stats + 2 * C::BR * 4));
+        const bool whole = first_sees >= wave_last && r0 + C::BR <= row_end;
+        if (first_sees < wg_last || r0 + C::BR > row_end) {  // some key is not seen by all its rows (uniform in the workgroup)
+            int *flags = (int *)(lds + 4 * C::kTileBytes + buf * (C::kStats + C::kFlags) + C::kStats);
+            char *tile = lds + 2 * buf * C::kTileBytes;
+            const bool mine = __any(tile_nonfinite<E, 256>(tile, 2 * C::kTileBytes, tid));
+            if (lane == 0) flags[wave] = mine;
+            __syncthreads();
+            if (uniform(flags[0] | flags[1] | flags[2] | flags[3])) {
+                if (bad_from < 0) bad_from = (int)r0;
+                bad_to = (int)min(r0 + C::BR, row_end) - 1;
+                clear_nonfinite<E, 256>(tile, 2 * C::kTileBytes, tid);
+                __syncthreads();
+            }
+        }
         dkv_block<E, DP, C::NRB>(dk, dv, kf, vf, L, qt, gt, stats, c, !whole, key, h);
         if (more) store(buf ^ 1);
         buf ^= 1;
     }
+    if (bad_from >= 0)  // (q's values that are not finite reach dk and dv through lse, dO's reach dk through delta)
+        add_nonfinite<E, DP>(dv, bad_from, bad_to, p.D, h,
+                             [&](int row) {
+                                 const int t = row_token(p, row);
+                                 return gg + (int64_t)t * p.dot + (row - t * p.grp) * p.doh;
+                             },
+                             [&](int row) { return !p.causal || key <= row_token(p, row) + off; });
     if (key >= sq.lk_slot) return;
+    if (key >= sq.lk) {  // beyond the sequence's length in its slot: zeros
+#pragma unroll
+        for (int db = 0; db < DP / 32; ++db) dk[db] = zero16(), dv[db] = zero16();
+    }
     if (p.nsplit > 1) {  // a share: fp32, for k_attn_dkv_sum
         const int64_t heads = p.total_k * p.Hkv, at = (sq.k0 + key) * p.Hkv + hk;
         float *part = p.ws + share_offset(p);
@@ -321,7 +365,6 @@ __global__ void __launch_bounds__(256, __is_same(E, F32) || DP > 64 ? 1 : 2) k_a
         store_column<F32, DP>(dv, 1.0f, part + ((p.nsplit + z) * heads + at) * p.D, p.D, h);
         return;
     }
-    // keys beyond the sequence's length in its slot get zeros
     store_column<E, DP>(dk, p.scale, (T *)p.dk + (sq.k0 + key) * p.dkt + hk * p.dkh, p.D, h);
     store_column<E, DP>(dv, 1.0f, (T *)p.dv + (sq.k0 + key) * p.dvt + hk * p.dvh, p.D, h);
 }
@@ -371,13 +414,13 @@ hipError_t run_bwd(const AttnParams &p0, hipStream_t s) {
     AttnParams p = p0;
     typedef TileCfg<E, DP> CQ;
     typedef DkvCfg<E, DP> CK;
-    hipError_t e = set_lds(k_attn_dq<E, DP>, CQ::kLds);
+    hipError_t e = set_lds(k_attn_dq<E, DP>, CQ::kLds + CQ::kFlags);
     if (e == hipSuccess) e = set_lds(k_attn_dkv<E, DP>, CK::kLds);
     if (e != hipSuccess) return e;
     if (p.total_q > 0) {
         p.slots = p.total_q * p.grp / CQ::BM + p.B;
         p.run = run_of(p.slots, p.B);
-        hipLaunchKernelGGL((k_attn_dq<E, DP>), dim3((unsigned)xcd_grid(p.slots, p.Hkv, p.run)), dim3(256), CQ::kLds, s, p);
+        hipLaunchKernelGGL((k_attn_dq<E, DP>), dim3((unsigned)xcd_grid(p.slots, p.Hkv, p.run)), dim3(256), CQ::kLds + CQ::kFlags, s, p);
     }
     if (p.total_k > 0) {
         p.slots = p.total_k / CK::BK + p.B;

@@ -49,7 +49,7 @@ __device__ __forceinline__ void fwd_block(FwdState<E, DP> &st, const uint4 *qf, 
     // p <= 2^8, exact in the sums' fp32 and in range of fp16, and saves the pass over the accumulators.
     if (__any(mx > st.m + 8.0f)) {
         const float mn = fmaxf(st.m, mx);
-        const float a = mn == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(st.m - mn);
+        const float a = st.m == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(st.m - mn);  // (nothing summed yet: 1)
         st.m = mn;
         st.l *= a;
 #pragma unroll

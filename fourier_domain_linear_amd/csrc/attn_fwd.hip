@@ -20,9 +20,10 @@ struct FwdCfg {
     static constexpr int BM = 128;                                              // packed rows of a workgroup
     static constexpr int NKB = __is_same(E, F32) || kSmall ? 1 : 2;             // 32-key blocks of a tile
     static constexpr int BN = 32 * NKB;
-    static constexpr int WPE = __is_same(E, F32) ? 1 : kSmall ? 3 : 2;          // waves a SIMD the registers allow
+    static constexpr int WPE = __is_same(E, F32) ? 1 : DP < 128 ? 4 : kSmall ? 3 : 2;          // waves a SIMD the registers allow
     static constexpr int kTileBytes = BN * TL::kRow;
-    static constexpr int kLds = 4 * kTileBytes;                                 // k and v, two buffers
+    static constexpr int kLds = 4 * kTileBytes;                                 // k and v, two buffers;
+    static constexpr int kFlags = 2 * 4 * 4;                                    // a word a wave, two sets
 };
 constexpr int64_t kShortKeys = 512;  // keys a sequence on average up to which SHORT is taken
 
@@ -77,10 +78,23 @@ __global__ void __launch_bounds__(256, (FwdCfg<E, DP, SHORT>::WPE)) k_attn_fwd(c
     int buf = 0;
     // (a wave without rows or keys fetches its part of the tiles, in a loop of its own)
     const bool works = r.wave_max >= k_beg;
+    int *flags = (int *)(lds + C::kLds);
+    bool bad = false;  // some tile was cleared
     auto arrive = [&](int k0) {
         dma_wait();
         __syncthreads();  // this tile is in LDS; the other buffer has no more readers
         if (k0 + C::BN < k_end) fetch(k0 + C::BN, buf ^ 1);
+        if (k0 + C::BN - 1 > r.all) {  // some row sees only part of it (uniform in the workgroup)
+            char *vt = lds + (2 * buf + 1) * C::kTileBytes;
+            const bool mine = __any(tile_nonfinite<E, 256>(vt, C::kTileBytes, tid));
+            if (lane == 0) flags[4 * buf + wave] = mine;
+            __syncthreads();
+            if (uniform(flags[4 * buf] | flags[4 * buf + 1] | flags[4 * buf + 2] | flags[4 * buf + 3])) {
+                bad = true;
+                clear_nonfinite<E, 256>(vt, C::kTileBytes, tid);
+                __syncthreads();
+            }
+        }
     };
     if (works) {
         for (int k0 = k_beg; k0 < k_end; k0 += C::BN) {
@@ -96,6 +110,9 @@ __global__ void __launch_bounds__(256, (FwdCfg<E, DP, SHORT>::WPE)) k_attn_fwd(c
         }
     }
 
+    if (bad)  // tiles begin at k_beg + BN i, and they were looked over from the one that holds key r.all + 1 on
+        add_nonfinite<E, DP>(st.o, k_beg + max(0, r.all + 1 - k_beg) / C::BN * C::BN, min(r.wave_max, k_end - 1), p.D, h,
+                             [&](int j) { return vg + (int64_t)j * p.vt; }, [&](int j) { return j <= r.last; });
     if (p.nsplit > 1) {  // partial results: unnormalised o, then (m, l), for k_attn_join
         const float l = half_sum(st.l);
         if (!r.live) return;
@@ -153,11 +170,12 @@ hipError_t run_fwd(const AttnParams &p0, hipStream_t s) {
     AttnParams p = p0;
     p.slots = p.total_q * p.grp / C::BM + p.B;
     p.run = run_of(p.slots, p.B);
-    if (C::kLds > 64 * 1024) {
-        hipError_t e = hipFuncSetAttribute((const void *)k_attn_fwd<E, DP, SHORT>, hipFuncAttributeMaxDynamicSharedMemorySize, C::kLds);
+    if (C::kLds + C::kFlags > 64 * 1024) {
+        hipError_t e = hipFuncSetAttribute((const void *)k_attn_fwd<E, DP, SHORT>, hipFuncAttributeMaxDynamicSharedMemorySize,
+                                            C::kLds + C::kFlags);
         if (e != hipSuccess) return e;
     }
-    hipLaunchKernelGGL((k_attn_fwd<E, DP, SHORT>), dim3((unsigned)xcd_grid(p.slots, p.Hkv, p.run), 1, p.nsplit), dim3(256), C::kLds, s, p);
+    hipLaunchKernelGGL((k_attn_fwd<E, DP, SHORT>), dim3((unsigned)xcd_grid(p.slots, p.Hkv, p.run), 1, p.nsplit), dim3(256), C::kLds + C::kFlags, s, p);
     if (p.nsplit > 1) {
         const int64_t rows = p.total_q * p.Hq;
         hipLaunchKernelGGL((k_attn_join<E>), dim3((unsigned)std::min<int64_t>((rows + 3) / 4, 1 << 20)), dim3(256), 0, s, p);

@@ -22,12 +22,13 @@ struct StepCfg {
 
 // Rows of 32 (columns of the products) from packed row `row0` on over the keys [k_beg, k_end).
 template <class E, int DP>
-__device__ __forceinline__ void step_rows(const AttnParams &p, const Seq &sq, int hk, int row0, int k_beg, int k_end, uint32_t lds0,
+__device__ __forceinline__ void step_rows(const AttnParams &p, const Seq &sq, int hk, int row0, int k_beg, int k_end, char *lds,
                                           int lane, FwdState<E, DP> &st, Rows &r) {
     typedef StepCfg<E, DP> C;
     typedef Tile<E, DP> TL;
     typedef typename ElemOf<E>::type T;
     const int h = lane >> 5;
+    const uint32_t lds0 = lds_offset(lds);
     r = rows_of(p, sq, hk, row0, 32, 0, lane);
     k_end = min(k_end, r.k_end);
     const T *kg = (const T *)p.k + sq.k0 * p.kt + hk * p.kh;
@@ -52,16 +53,27 @@ __device__ __forceinline__ void step_rows(const AttnParams &p, const Seq &sq, in
     const float c = p.scale * kLog2e;
     const typename TL::Lane L = TL::lane_of(lane);
     int buf = 0;
+    bool bad = false;  // some tile was cleared
     for (int k0 = k_beg; k0 < k_end; k0 += C::BN) {
         // whole heads: the younger tile's loads may stay on their way
         if (p.D == DP && k0 + C::BN < k_end) dma_wait_but<2 * C::Dma::N>();
         else dma_wait();
         const uint32_t kt = lds0 + buf * 2 * C::kTileBytes, vt = kt + C::kTileBytes;
+        if (k0 + C::BN - 1 > r.all) {
+            char *v = lds + (2 * buf + 1) * C::kTileBytes;
+            if (__any(tile_nonfinite<E, 64>(v, C::kTileBytes, lane))) {
+                bad = true;
+                clear_nonfinite<E, 64>(v, C::kTileBytes, lane);
+            }
+        }
         fwd_block<E, DP, 1>(st, qf, L, kt, vt, c, k0 + C::BN - 1 > r.wave_min, r.last - k0, h);
         lds_read_wait();  // this tile's reads are done before its place is written again
         if (k0 + 2 * C::BN < k_end) fetch(k0 + 2 * C::BN, buf);
         buf ^= 1;
     }
+    if (bad)  // tiles begin at k_beg + 32 i, and they were looked over from the one that holds key r.all + 1 on
+        add_nonfinite<E, DP>(st.o, k_beg + max(0, r.all + 1 - k_beg) / C::BN * C::BN, min(r.wave_max, k_end - 1), p.D, h,
+                             [&](int j) { return vg + (int64_t)j * p.vt; }, [&](int j) { return j <= r.last; });
 }
 
 template <class E, int DP>
@@ -77,14 +89,13 @@ __global__ void __launch_bounds__(64, DP > 64 ? 1 : 2) k_attn_step(const AttnPar
     if (tile < 0 || k_at >= sq.lk) return;
     zero_pad<64>(lds, C::kLds, p.D, DP, lane);
     const int rows = sq.lq * p.grp, chunks = (sq.lk + p.chunk - 1) / p.chunk;
-    const uint32_t lds0 = lds_offset(lds);
     FwdState<E, DP> st;
     Rows r;
     // one chunk, or more rows than a partial result has room for: whole rows, shared out over the chunks' waves
     const bool split = rows <= p.rcap && chunks > 1;
     const int k_beg = split ? (int)k_at : 0, k_end = split ? (int)min(k_at + p.chunk, (int64_t)sq.lk) : sq.lk;
     for (int row0 = split ? 0 : (int)tile * 32; row0 < rows; row0 += split ? 32 : chunks * 32) {
-        step_rows<E, DP>(p, sq, hk, row0, k_beg, k_end, lds0, lane, st, r);
+        step_rows<E, DP>(p, sq, hk, row0, k_beg, k_end, lds, lane, st, r);
         if (split) {
             const float l = half_sum(st.l);
             if (r.live) {

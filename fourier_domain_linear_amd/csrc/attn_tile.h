@@ -19,6 +19,7 @@ struct TileCfg {
     static constexpr int BN = 32 * NKB;
     static constexpr int kTileBytes = BN * TL::kRow;
     static constexpr int kLds = 4 * kTileBytes;                // k and v, two buffers
+    static constexpr int kFlags = 2 * 4 * 4;                   // a word a wave, two sets
 };
 
 // Units an XCD takes in a run: the tiles of a sequence where they are few, else one.
@@ -141,6 +142,85 @@ __device__ __forceinline__ void load_row(uint4 *f, const typename ElemOf<E>::typ
         for (int t = 0; t < Tile<E, DP>::kSteps; ++t)
             f[t] = (2 * t + h) * kPer < D ? *(const uint4 *)(row + (2 * t + h) * kPer) : make_uint4(0, 0, 0, 0);
     }
+}
+
+// ---- values of tokens that a row must not see ----
+//
+// A masked probability is 0, but the second product multiplies it with whatever the masked token holds, and 0 times
+// an infinity or NaN is NaN. Tiles that some row sees only in part are therefore looked over, and where one holds such
+// a value, the tile's place is cleared and the rows that do see it get it added at the end (finite everywhere
+// else: the products are unchanged). A tile is looked over once or twice a workgroup; the rest never runs in ordinary use.
+
+template <class E>
+__device__ __forceinline__ uint32_t nonfinite_mask(uint32_t w) {  // the bits of the word's values that are not finite
+    if constexpr (__is_same(E, F32)) {
+        return (w & 0x7f800000u) == 0x7f800000u ? 0xffffffffu : 0u;
+    } else {
+        constexpr uint32_t e = __is_same(E, F16) ? 0x7c00u : 0x7f80u;
+        return ((w & e) == e ? 0xffffu : 0u) | ((w & (e << 16)) == (e << 16) ? 0xffff0000u : 0u);
+    }
+}
+// Whether this thread's share of a tile holds such a value.
+template <class E, int THREADS>
+__device__ __forceinline__ bool tile_nonfinite(const char *tile, int bytes, int tid) {
+    uint32_t any = 0;
+#pragma unroll 1
+    for (int i = tid * 16; i < bytes; i += THREADS * 16) {
+        const uint4 v = *(const uint4 *)(tile + i);
+        any |= nonfinite_mask<E>(v.x) | nonfinite_mask<E>(v.y) | nonfinite_mask<E>(v.z) | nonfinite_mask<E>(v.w);
+    }
+    return any != 0;
+}
+template <class E, int THREADS>
+__device__ __forceinline__ void clear_nonfinite(char *tile, int bytes, int tid) {
+#pragma unroll 1
+    for (int i = tid * 16; i < bytes; i += THREADS * 16) {
+        uint4 v = *(const uint4 *)(tile + i);
+        v.x &= ~nonfinite_mask<E>(v.x), v.y &= ~nonfinite_mask<E>(v.y), v.z &= ~nonfinite_mask<E>(v.z), v.w &= ~nonfinite_mask<E>(v.w);
+        *(uint4 *)(tile + i) = v;
+    }
+}
+// After the tiles: acc[d] += X[r][d] for the rows r of [from, to] that the lane's column sees and the values that are
+// not finite, from global memory (row(r): the row's first element).
+template <class E, int DP, class Row, class Sees>
+__device__ __forceinline__ void add_nonfinite(f32x16 *acc, int from, int to, int D, int h, Row row, Sees sees) {
+    typedef typename ElemOf<E>::type T;
+#pragma unroll 1
+    for (int r = from; r <= to; ++r) {
+        const bool see = sees(r);
+        const T *x = row(r);
+#pragma unroll
+        for (int db = 0; db < DP / 32; ++db)
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                const int d = 32 * db + 8 * g + 4 * h;
+                if (d < D)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float v = Elem<E>::get(x[d + j]);
+                        acc[db][4 * g + j] += see && !(fabsf(v) < INFINITY) ? v : 0.0f;
+                    }
+            }
+    }
+}
+
+// The same for a tile that also made the scores: a column that sees a row with such a value becomes NaN whole.
+template <class E, int DP, class Row, class Sees>
+__device__ __forceinline__ void poison_columns(f32x16 *acc, int from, int to, int D, int h, Row row, Sees sees) {
+    typedef typename ElemOf<E>::type T;
+    float add = 0.0f;
+#pragma unroll 1
+    for (int r = from; r <= to; ++r) {
+        const T *x = row(r);
+        bool bad = false;
+        for (int d = h; d < D; d += 2) bad |= !(fabsf(Elem<E>::get(x[d])) < INFINITY);
+        bad = (__ballot(bad) & (1ull | 1ull << 32)) != 0;  // the row's two halves of values, the same for every lane
+        if (bad && sees(r)) add = NAN;
+    }
+#pragma unroll
+    for (int db = 0; db < DP / 32; ++db)
+#pragma unroll
+        for (int v = 0; v < 16; ++v) acc[db][v] += add;
 }
 
 }  // namespace eqlin

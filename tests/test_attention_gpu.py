@@ -213,6 +213,62 @@ def test_attention_nan_stays_in_its_sequence(cuda_device):
         assert torch.equal(a[keep], b[keep]) and bool(b[~keep].isnan().all())
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("lens", [([150], [150]), ([4], [700]), ([70, 33], [90, 33]), ([2, 3], [600, 900])],
+                         ids=["prompt", "step", "longer", "steps"])
+def test_attention_values_of_later_tokens(lens, dtype, cuda_device):
+    """Infinities and NaN in tokens that a causal row must not see leave it alone, in o, lse and every gradient;
+    the rows that see them get what the sums give."""
+    dev, (lq, lk) = cuda_device, lens
+    q, k, v, do, cu_q, cu_k = _inputs(lq, lk, 4, 2, 64, dtype, dev, seed=9)
+    o, lse = eq.attention(q, k, v, cu_q, cu_k, causal=True)
+    g = eq.attention_backward(do, q, k, v, o, lse, cu_q, cu_k, causal=True)
+    n_q, n_k = lq[0], lk[0]
+    for late in (1, 2, n_q - 1):  # the last `late` tokens of the first sequence
+        q2, k2, v2, do2 = (t.clone() for t in (q, k, v, do))
+        v2[n_k - late, 0, 3] = float("inf")
+        v2[n_k - late, 0, 5] = float("-inf")
+        v2[n_k - late, 1, 7] = float("nan")
+        o2, lse2 = eq.attention(q2, k2, v2, cu_q, cu_k, causal=True)
+        torch.cuda.synchronize()
+        keep = torch.ones(sum(lq), dtype=torch.bool)
+        keep[n_q - late:n_q] = False
+        assert torch.equal(lse, lse2) and torch.equal(o[keep], o2[keep])
+        assert bool((o2[~keep][:, :2, 3] == float("inf")).all()) and bool((o2[~keep][:, :2, 5] == float("-inf")).all())
+        assert bool(o2[~keep][:, 2:, 7].isnan().all())
+        rest = [d for d in range(64) if d not in (3, 5, 7)]
+        assert torch.equal(o2[:, :, rest], o[:, :, rest])
+        k2[n_k - late:n_k] = float("nan")
+        v2[n_k - late:n_k] = float("-inf")
+        q2[n_q - late:n_q] = float("inf")
+        do2[n_q - late:n_q] = float("nan")
+        o2, lse2 = eq.attention(q2, k2, v2, cu_q, cu_k, causal=True)
+        g2 = eq.attention_backward(do2, q2, k2, v2, o2, lse2, cu_q, cu_k, causal=True)
+        torch.cuda.synchronize()
+        assert torch.equal(o[keep], o2[keep]) and torch.equal(lse[keep], lse2[keep])
+        assert bool(o2[~keep].isnan().all()) and bool(lse2[~keep].isnan().all())
+        assert torch.equal(g[0][keep], g2[0][keep]) and bool(g2[0][~keep].isnan().all())
+        # every key of the first sequence is seen by a row of NaN; the other sequences' are not
+        for a, b in zip(g[1:], g2[1:]):
+            assert bool(b[:n_k].isnan().all()) and torch.equal(a[n_k:], b[n_k:])
+    # early rows of NaN reach only the keys they see
+    do2, q2 = do.clone(), q.clone()
+    do2[0], q2[0] = float("nan"), float("inf")
+    o2, lse2 = eq.attention(q2, k, v, cu_q, cu_k, causal=True)
+    g2 = eq.attention_backward(do2, q2, k, v, o2, lse2, cu_q, cu_k, causal=True)
+    torch.cuda.synchronize()
+    sees = n_k - n_q + 1
+    for a, b in zip(g[1:], g2[1:]):
+        assert bool(b[:sees].isnan().all()) and torch.equal(a[sees:], b[sees:])
+    assert torch.equal(g[0][1:], g2[0][1:])
+    do2 = do.clone()
+    do2[0, 0, 11] = float("inf")  # one value: dv's column, and dk through delta
+    g2 = eq.attention_backward(do2, q, k, v, o, lse, cu_q, cu_k, causal=True)
+    torch.cuda.synchronize()
+    assert bool((g2[2][:sees, 0, 11] == float("inf")).all()) and torch.equal(g2[2][sees:], g[2][sees:])
+    assert torch.equal(g2[1][sees:], g[1][sees:]) and bool(torch.isfinite(g2[2][:sees, 0, :11]).all())
+
+
 def test_attention_streams_and_repeats(cuda_device):
     """The same bits every time, on another stream than the tensors' own, and with the caller's workspace."""
     dev = cuda_device
