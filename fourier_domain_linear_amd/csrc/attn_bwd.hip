@@ -46,6 +46,30 @@ __device__ __forceinline__ void dq_block(f32x16 *dq, const uint4 *qf, const uint
     }
 }
 
+// delta of rows that see one tile of keys only: sum over its keys of P dP, in fp32 throughout. Over a handful of keys
+// the sum of dO O carries o's rounding into the gradients about as far as their own rounding; over more it is lost
+// among the terms.
+template <class E, int DP, int NKB>
+__device__ __forceinline__ float delta_of_tile(const uint4 *qf, const uint4 *gf, const typename Tile<E, DP>::Lane &L, uint32_t kt,
+                                               uint32_t vt, float c, float lse2, int lim, int h) {
+    typedef Tile<E, DP> TL;
+    float sum = 0.0f;
+#pragma unroll 1
+    for (int kb = 0; kb < NKB; ++kb) {
+        const uint32_t at = kb * 32 * TL::kRow;
+        f32x16 s = zero16(), dp = zero16();
+#pragma unroll
+        for (int t = 0; t < TL::kSteps; ++t) {
+            s = mma_frag<E>(TL::row_frag(kt + at, L, 0, t), qf[t], s);
+            dp = mma_frag<E>(TL::row_frag(vt + at, L, 0, t), gf[t], dp);
+        }
+#pragma unroll
+        for (int v = 0; v < 16; ++v)
+            sum += 32 * kb + d_row(v, 0) <= lim - 4 * h ? __builtin_amdgcn_exp2f(fmaf(s[v], c, -lse2)) * dp[v] : 0.0f;
+    }
+    return half_sum(sum);
+}
+
 template <class E, int DP>
 __global__ void __launch_bounds__(256, __is_same(E, F32) ? 1 : 2) k_attn_dq(const AttnParams p) {
     typedef TileCfg<E, DP> C;
@@ -97,7 +121,6 @@ __global__ void __launch_bounds__(256, __is_same(E, F32) ? 1 : 2) k_attn_dq(cons
             for (int j = 0; j < Elem<E>::V; ++j) delta = fmaf(a[j], b[j], delta);
         }
         delta = half_sum(delta);
-        if (r.live && h == 0) p.ws[at] = delta;
     }
     f32x16 dq[DP / 32];
 #pragma unroll
@@ -127,6 +150,7 @@ __global__ void __launch_bounds__(256, __is_same(E, F32) ? 1 : 2) k_attn_dq(cons
         for (int k0 = 0; k0 < r.k_end; k0 += C::BN) {
             arrive(k0);
             const uint32_t kt = lds0 + buf * 2 * C::kTileBytes, vt = kt + C::kTileBytes;
+            if (r.k_end <= C::BN) delta = delta_of_tile<E, DP, C::NKB>(qf, gf, L, kt, vt, c, lse2, r.last, h);
             dq_block<E, DP, C::NKB>(dq, qf, gf, L, kt, vt, c, lse2, delta, k0 + C::BN - 1 > r.wave_min, r.last - k0, h);
             buf ^= 1;
         }
@@ -136,6 +160,7 @@ __global__ void __launch_bounds__(256, __is_same(E, F32) ? 1 : 2) k_attn_dq(cons
             buf ^= 1;
         }
     }
+    if (r.live && h == 0) p.ws[at] = delta;
     if (bad)
         poison_columns<E, DP>(dq, max(0, r.all + 1) / C::BN * C::BN, min(r.wave_max, r.k_end - 1), p.D, h,
                               [&](int j) { return kg + (int64_t)j * p.kt; }, [&](int j) { return j <= r.last; });
