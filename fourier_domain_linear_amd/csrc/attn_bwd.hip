@@ -48,7 +48,7 @@ __device__ __forceinline__ void dq_block(f32x16 *dq, const uint4 *qf, const uint
 
 // delta of rows that see one tile of keys only: sum over its keys of P dP, in fp32 throughout. Over a handful of keys
 // the sum of dO O carries o's rounding into the gradients about as far as their own rounding; over more it is lost
-// among the terms.
+// among the terms. A row that sees one key has P = 1 and so dS = 0, exactly.
 template <class E, int DP, int NKB>
 __device__ __forceinline__ float delta_of_tile(const uint4 *qf, const uint4 *gf, const typename Tile<E, DP>::Lane &L, uint32_t kt,
                                                uint32_t vt, float c, float lse2, int lim, int h) {
@@ -65,7 +65,7 @@ __device__ __forceinline__ float delta_of_tile(const uint4 *qf, const uint4 *gf,
         }
 #pragma unroll
         for (int v = 0; v < 16; ++v)
-            sum += 32 * kb + d_row(v, 0) <= lim - 4 * h ? __builtin_amdgcn_exp2f(fmaf(s[v], c, -lse2)) * dp[v] : 0.0f;
+            sum += 32 * kb + d_row(v, 0) <= lim - 4 * h ? (lim == 0 ? 1.0f : __builtin_amdgcn_exp2f(fmaf(s[v], c, -lse2))) * dp[v] : 0.0f;
     }
     return half_sum(sum);
 }

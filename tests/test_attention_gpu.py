@@ -180,6 +180,17 @@ def test_attention_of_a_qkv_layer_output(dtype, cuda_device):
     assert float((o2.double() - o.roll(3, 3).double()).norm() / o.double().norm()) <= 2 * U[dtype]
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("D", [24, 64, 128])
+def test_attention_one_key_has_no_score_gradient(D, dtype, cuda_device):
+    """Softmax over one key is 1 whatever the score: dq and dk are zeros, to the bit."""
+    q, k, v, do, cu_q, cu_k = _inputs([1, 1, 5], [1, 1, 1], 4, 2, D, dtype, cuda_device, seed=8)
+    o, lse = eq.attention(q, k, v, cu_q, cu_k)
+    dq, dk, dv = eq.attention_backward(do, q, k, v, o, lse, cu_q, cu_k)
+    torch.cuda.synchronize()
+    assert not dq.any() and not dk.any() and dv.any()
+
+
 def test_attention_scores_far_apart(cuda_device):
     """Scores in the thousands and one dominating key: no overflow, the maximum moves from tile to tile."""
     dev = cuda_device
