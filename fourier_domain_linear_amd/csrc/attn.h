@@ -17,8 +17,6 @@
 
 namespace eqlin {
 
-
-
 template <class E>
 struct ElemOf {
     typedef uint16_t type;
@@ -47,8 +45,6 @@ __device__ __forceinline__ f32x16 mma_frag(const uint4 &a, const uint4 &b, f32x1
     }
 }
 
-// W (a 32x32 product's D layout, 16 values a lane) -> B-operand fragments of the next product: NF = 2
-// (half types, rounded to nearest even) or 4 (fp32, exact).
 __device__ __forceinline__ f32x16 zero16() {
     f32x16 z;
 #pragma unroll
@@ -56,6 +52,8 @@ __device__ __forceinline__ f32x16 zero16() {
     return z;
 }
 
+// W (a 32x32 product's D layout, 16 values a lane) -> B-operand fragments of the next product: NF = 2
+// (half types, rounded to nearest even) or 4 (fp32, exact).
 template <class E>
 struct WFrags {
     static constexpr int NF = __is_same(E, F32) ? 4 : 2;
@@ -249,6 +247,18 @@ __device__ __forceinline__ Seq seq_of_slot(const AttnParams &p, int mul, int siz
 // The sequence of packed query token t (the last that begins at or before it).
 __device__ __forceinline__ Seq seq_of_row(const AttnParams &p, int t, int &index) {
     return find_seq<false>(p, [&](int, int cu) { return cu <= t; }, index);
+}
+
+// Sequence i.
+__device__ __forceinline__ Seq seq_at(const AttnParams &p, int i) {
+    auto clamp = [](int x, int a, int b) { return min(max(x, a), b); };
+    const int q_at = clamp(p.cu_q[i], 0, (int)p.total_q), k_at = clamp(p.cu_k[i], 0, (int)p.total_k);
+    Seq s;
+    s.q0 = q_at, s.k0 = k_at;
+    s.lq = clamp(p.cu_q[i + 1], q_at, (int)p.total_q) - q_at;
+    s.lk_slot = clamp(p.cu_k[i + 1], k_at, (int)p.total_k) - k_at;
+    s.lk = p.len_k ? clamp(p.len_k[i], 0, s.lk_slot) : s.lk_slot;
+    return s;
 }
 
 // packed row -> token (rows are below 2^31; most groups are powers of two)

@@ -40,7 +40,7 @@ __global__ void __launch_bounds__(256, (FwdCfg<E, DP, SHORT>::WPE)) k_attn_fwd(c
     int64_t tile;
     const Seq sq = seq_of_slot<false>(p, p.grp, C::BM, slot, tile);
     const int row_wg = (int)tile * C::BM;
-    if (tile < 0 || row_wg >= sq.lq * p.grp) return;
+    if (tile < 0 || row_wg >= sq.lq * p.grp || sq.lq * p.grp <= p.rcap) return;  // (so few rows: the step kernel's)
     const Rows r = rows_of(p, sq, hk, row_wg, C::BM, wave, lane);
     int k_beg = 0, k_end = r.k_end;
     if (p.nsplit > 1) {
@@ -128,39 +128,36 @@ __global__ void __launch_bounds__(256, (FwdCfg<E, DP, SHORT>::WPE)) k_attn_fwd(c
     finish_rows<E, DP>(p, sq, st, r, h);
 }
 
-// ---- joining the key ranges of a row: one wave a row ----
+// ---- joining the key ranges of a row: one wave a row (of a sequence that the tile kernel took) ----
 
 template <class E>
 __global__ void __launch_bounds__(256) k_attn_join(const AttnParams p) {
     typedef typename ElemOf<E>::type T;
     const int lane = threadIdx.x & 63;
     const int64_t rows = p.total_q * p.Hq;
-    for (int64_t at = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); at < rows; at += (int64_t)gridDim.x * 4) {
-    const float *ml = p.ws + p.nsplit * rows * p.D;
-    float m = -INFINITY;
-    for (int z = 0; z < p.nsplit; ++z) m = fmaxf(m, ml[(z * rows + at) * 2]);
-    const float mm = m == -INFINITY ? 0.0f : m;
-    float l = 0.0f, o0 = 0.0f, o1 = 0.0f;
-    for (int z = 0; z < p.nsplit; ++z) {
-        const float w = __builtin_amdgcn_exp2f(ml[(z * rows + at) * 2] - mm);
-        const float *o = p.ws + (z * rows + at) * p.D;
-        l = fmaf(w, ml[(z * rows + at) * 2 + 1], l);
-        if (lane < p.D) o0 = fmaf(w, o[lane], o0);
-        if (lane + 64 < p.D) o1 = fmaf(w, o[lane + 64], o1);
-    }
-    const int64_t tok = at / p.Hq;
-    const int hq = (int)(at - tok * p.Hq);
-    T *dst = (T *)p.o + tok * p.ot + hq * p.oh;
-    const bool empty = ml[at * 2 + 1] < 0.0f;  // the same in every range
-    const float inv = empty ? 0.0f : 1.0f / l;
-    if constexpr (__is_same(E, F32)) {
-        if (lane < p.D) dst[lane] = o0 * inv;
-        if (lane + 64 < p.D) dst[lane + 64] = o1 * inv;
-    } else {
-        if (lane < p.D) dst[lane] = pack1<E>(o0 * inv);
-        if (lane + 64 < p.D) dst[lane + 64] = pack1<E>(o1 * inv);
-    }
-    if (p.lse && lane == 0) p.lse[at] = empty ? -INFINITY : m * kLn2 + logf(l);
+    for (int64_t at = (int64_t)blockIdx.x * 4 + uniform((int)(threadIdx.x >> 6)); at < rows; at += (int64_t)gridDim.x * 4) {
+        const int tok = (int)(at / p.Hq), hq = (int)(at - (int64_t)tok * p.Hq);
+        int seq;
+        const Seq sq = seq_of_row(p, tok, seq);
+        if (tok < sq.q0 || tok >= sq.q0 + sq.lq || sq.lq * p.grp <= p.rcap) continue;
+        const float *ml = p.ws + p.nsplit * rows * p.D;
+        float m = -INFINITY;
+        for (int z = 0; z < p.nsplit; ++z) m = fmaxf(m, ml[(z * rows + at) * 2]);
+        const float mm = m == -INFINITY ? 0.0f : m;
+        float l = 0.0f, o0 = 0.0f, o1 = 0.0f;
+        for (int z = 0; z < p.nsplit; ++z) {
+            const float w = __builtin_amdgcn_exp2f(ml[(z * rows + at) * 2] - mm);
+            const float *o = p.ws + (z * rows + at) * p.D;
+            l = fmaf(w, ml[(z * rows + at) * 2 + 1], l);
+            if (lane < p.D) o0 = fmaf(w, o[lane], o0);
+            if (lane + 64 < p.D) o1 = fmaf(w, o[lane + 64], o1);
+        }
+        T *dst = (T *)p.o + tok * p.ot + hq * p.oh;
+        const bool empty = ml[at * 2 + 1] < 0.0f;  // the same in every range
+        const float inv = empty ? 0.0f : 1.0f / l;
+        if (lane < p.D) dst[lane] = Elem<E>::put(o0 * inv);
+        if (lane + 64 < p.D) dst[lane + 64] = Elem<E>::put(o1 * inv);
+        if (p.lse && lane == 0) p.lse[at] = empty ? -INFINITY : m * kLn2 + logf(l);
     }
 }
 
@@ -206,18 +203,23 @@ int pick_nsplit(const AttnParams &p) {
 size_t attention_workspace_bytes(const AttnParams &p0, eqlin_dtype_t) {
     AttnParams p = p0;
     if (p.total_q <= 0 || p.B <= 0) return 0;
-    if (plan_step(p)) return step_workspace_bytes(p);
+    const bool step = plan_step(p);
     const int n = pick_nsplit(p);
-    return n <= 1 ? 0 : (size_t)n * p.total_q * p.Hq * (p.D + 2) * sizeof(float);
+    const size_t parts = n <= 1 || (step && !p.tiled) ? 0 : (size_t)n * p.total_q * p.Hq * (p.D + 2) * sizeof(float);
+    return parts + (step ? step_workspace_bytes(p) : 0);
 }
 
 hipError_t launch_attention(const AttnParams &p0, eqlin_dtype_t dtype, hipStream_t s) {
     AttnParams p = p0;
-    if (plan_step(p)) return launch_step(p, dtype, s);
-    p.nsplit = pick_nsplit(p);
-    if (dtype == EQLIN_F32) return run_fwd_e<F32>(p, s);
-    if (dtype == EQLIN_F16) return run_fwd_e<F16>(p, s);
-    return run_fwd_e<BF16>(p, s);
+    const bool step = plan_step(p);
+    if (!step || p.tiled) {
+        AttnParams t = p;
+        t.nsplit = pick_nsplit(p);
+        if (step) t.ws += step_workspace_bytes(p) / sizeof(float);
+        const hipError_t e = dtype == EQLIN_F32 ? run_fwd_e<F32>(t, s) : dtype == EQLIN_F16 ? run_fwd_e<F16>(t, s) : run_fwd_e<BF16>(t, s);
+        if (e != hipSuccess || !step) return e;
+    }
+    return launch_step(p, dtype, s);
 }
 
 }  // namespace eqlin

@@ -2,8 +2,11 @@
 // are split into chunks, one wave takes a chunk, and the partial results are joined.
 //
 // Bound by reading k and v once. A workgroup is one wave: it keeps two 32-key tiles of k and v in flight straight
-// into LDS (32 KB at 128 dims in a half type, so five waves share a CU and 160 KB are on their way), with no barrier
-// and no other wave to wait for. The group's rows are the 32 columns of its products.
+// into LDS (32 KB at 128 dims in a half type; the registers let four waves share a CU, 128 KB on their way), with no
+// barrier and no other wave to wait for. The group's rows are the 32 columns of its products. 8 tokens over
+// 100000 keys in all, 16 heads on 2 of 128 dims in bf16 (103 MB): 29.3 us with the join, 3.5 TB/s; the chunks' kernel
+// alone 24 us, 4.3 TB/s, against 5.1 TB/s of a large copy. Sequences of more rows than the columns hold are the tile
+// kernel's, launched before.
 #include "attn.h"
 #include "attn_fwd.h"
 
@@ -91,6 +94,7 @@ __global__ void __launch_bounds__(64, DP > 64 ? 1 : 2) k_attn_step(const AttnPar
     const int rows = sq.lq * p.grp, chunks = (sq.lk + p.chunk - 1) / p.chunk;
     FwdState<E, DP> st;
     Rows r;
+    if (rows > p.rcap && p.tiled) return;
     // one chunk, or more rows than a partial result has room for: whole rows, shared out over the chunks' waves
     const bool split = rows <= p.rcap && chunks > 1;
     const int k_beg = split ? (int)k_at : 0, k_end = split ? (int)min(k_at + p.chunk, (int64_t)sq.lk) : sq.lk;
@@ -114,78 +118,80 @@ __global__ void __launch_bounds__(64, DP > 64 ? 1 : 2) k_attn_step(const AttnPar
     }
 }
 
-// One workgroup a row: its 16 waves share the chunks, then join over LDS.
+// A workgroup a sequence and head (and token, blockIdx.y): its 16 waves share the chunks, then join over LDS.
 constexpr int kJoinWaves = 16;
 template <class E>
 __global__ void __launch_bounds__(64 * kJoinWaves) k_attn_step_join(const AttnParams p) {
     typedef typename ElemOf<E>::type T;
     __shared__ float2 so[kJoinWaves][64], sml[kJoinWaves];
     const int lane = threadIdx.x & 63, wave = uniform((int)(threadIdx.x >> 6));
-    const int64_t rows = p.total_q * p.Hq;
-    for (int64_t at = blockIdx.x; at < rows; at += gridDim.x) {
-        const int tok_at = (int)(at / p.Hq), hq = (int)(at - (int64_t)tok_at * p.Hq), hk = hq / p.grp;
-        int seq;
-        const Seq sq = seq_of_row(p, tok_at, seq);
+    // (the loop over units: one turn, but for more than a million of them)
+    for (int64_t unit = blockIdx.x, step_u = gridDim.x; unit < (int64_t)p.B * p.Hq; unit += step_u) {
+        const int seq = (int)(unit / p.Hq), hq = (int)(unit - (int64_t)seq * p.Hq), hk = hq / p.grp;
+        const Seq sq = seq_at(p, seq);
         const int nr = sq.lq * p.grp, chunks = (sq.lk + p.chunk - 1) / p.chunk;
-        const int tok = tok_at - (int)sq.q0, last = p.causal ? tok + sq.lk - sq.lq : sq.lk - 1;
-        if (tok < 0 || tok >= sq.lq) continue;  // outside every sequence
+        if (nr > p.rcap && p.tiled) continue;                      // the tile kernel's
         if (chunks == 1 || (nr > p.rcap && chunks > 0)) continue;  // written by the step itself
-        const int64_t slot0 = slot_start(sq.k0, seq, 1, p.chunk);
-        const int64_t base = (slot0 * p.Hkv + hk) * p.rcap + tok * p.grp + (hq - hk * p.grp), step = (int64_t)p.Hkv * p.rcap;
-        const float2 *ml = (const float2 *)(p.ws + p.slots * p.Hkv * p.rcap * p.D);
-        // each wave joins its own chunks (their loads wait for nothing), then the waves join
-        constexpr int N = 8;
-        float m = -INFINITY, l = 0.0f;
-        float2 o = make_float2(0.0f, 0.0f);
-        const bool mine = 2 * lane < p.D;
-        for (int z0 = wave; z0 < chunks; z0 += N * kJoinWaves) {
-            float2 st[N], v[N];
+        for (int tok = blockIdx.y; tok < sq.lq; tok += gridDim.y) {
+            const int last = p.causal ? tok + sq.lk - sq.lq : sq.lk - 1;
+            const int64_t at = (sq.q0 + tok) * p.Hq + hq;
+            const int64_t slot0 = slot_start(sq.k0, seq, 1, p.chunk);
+            const int64_t base = (slot0 * p.Hkv + hk) * p.rcap + tok * p.grp + (hq - hk * p.grp), step = (int64_t)p.Hkv * p.rcap;
+            const float2 *ml = (const float2 *)(p.ws + p.slots * p.Hkv * p.rcap * p.D);
+            // each wave joins its own chunks (their loads wait for nothing), then the waves join
+            constexpr int N = 8;
+            float m = -INFINITY, l = 0.0f;
+            float2 o = make_float2(0.0f, 0.0f);
+            const bool mine = 2 * lane < p.D;
+            for (int z0 = wave; z0 < chunks; z0 += N * kJoinWaves) {
+                float2 st[N], v[N];
 #pragma unroll
-            for (int j = 0; j < N; ++j) {
-                const int z = z0 + j * kJoinWaves;
-                const int64_t i = base + min(z, chunks - 1) * step;
-                st[j] = z < chunks ? ml[i] : make_float2(-INFINITY, 0.0f);
-                v[j] = z < chunks && mine ? *(const float2 *)(p.ws + i * p.D + 2 * lane) : make_float2(0.0f, 0.0f);
+                for (int j = 0; j < N; ++j) {
+                    const int z = z0 + j * kJoinWaves;
+                    const int64_t i = base + min(z, chunks - 1) * step;
+                    st[j] = z < chunks ? ml[i] : make_float2(-INFINITY, 0.0f);
+                    v[j] = z < chunks && mine ? *(const float2 *)(p.ws + i * p.D + 2 * lane) : make_float2(0.0f, 0.0f);
+                }
+                float mn = m;
+#pragma unroll
+                for (int j = 0; j < N; ++j) mn = fmaxf(mn, st[j].x);
+                const float mm = mn == -INFINITY ? 0.0f : mn, a = __builtin_amdgcn_exp2f(m - mm);
+                l *= a, o.x *= a, o.y *= a;
+                m = mn;
+#pragma unroll
+                for (int j = 0; j < N; ++j) {
+                    const float w = __builtin_amdgcn_exp2f(st[j].x - mm);
+                    l = fmaf(w, st[j].y, l);
+                    o.x = fmaf(w, v[j].x, o.x);
+                    o.y = fmaf(w, v[j].y, o.y);
+                }
             }
-            float mn = m;
+            __syncthreads();
+            so[wave][lane] = o;
+            if (lane == 0) sml[wave] = make_float2(m, l);
+            __syncthreads();
+            if (wave == 0) {
+                float mx = -INFINITY, total = 0.0f;
+                float2 sum = make_float2(0.0f, 0.0f);
 #pragma unroll
-            for (int j = 0; j < N; ++j) mn = fmaxf(mn, st[j].x);
-            const float mm = mn == -INFINITY ? 0.0f : mn, a = __builtin_amdgcn_exp2f(m - mm);
-            l *= a, o.x *= a, o.y *= a;
-            m = mn;
+                for (int w = 0; w < kJoinWaves; ++w) mx = fmaxf(mx, sml[w].x);
+                const float mm = mx == -INFINITY ? 0.0f : mx;
 #pragma unroll
-            for (int j = 0; j < N; ++j) {
-                const float w = __builtin_amdgcn_exp2f(st[j].x - mm);
-                l = fmaf(w, st[j].y, l);
-                o.x = fmaf(w, v[j].x, o.x);
-                o.y = fmaf(w, v[j].y, o.y);
+                for (int w = 0; w < kJoinWaves; ++w) {
+                    const float a = __builtin_amdgcn_exp2f(sml[w].x - mm);
+                    total = fmaf(a, sml[w].y, total);
+                    sum.x = fmaf(a, so[w][lane].x, sum.x);
+                    sum.y = fmaf(a, so[w][lane].y, sum.y);
+                }
+                const bool empty = last < 0 || sq.lk == 0;
+                const float inv = empty ? 0.0f : 1.0f / total;
+                T *dst = (T *)p.o + (sq.q0 + tok) * p.ot + hq * p.oh + 2 * lane;
+                if (mine) {
+                    if constexpr (__is_same(E, F32)) *(float2 *)dst = make_float2(sum.x * inv, sum.y * inv);
+                    else *(uint32_t *)dst = pack2<E>(sum.x * inv, sum.y * inv);
+                }
+                if (p.lse && lane == 0) p.lse[at] = empty ? -INFINITY : mx * kLn2 + logf(total);
             }
-        }
-        __syncthreads();
-        so[wave][lane] = o;
-        if (lane == 0) sml[wave] = make_float2(m, l);
-        __syncthreads();
-        if (wave == 0) {
-            float mx = -INFINITY, total = 0.0f;
-            float2 sum = make_float2(0.0f, 0.0f);
-#pragma unroll
-            for (int w = 0; w < kJoinWaves; ++w) mx = fmaxf(mx, sml[w].x);
-            const float mm = mx == -INFINITY ? 0.0f : mx;
-#pragma unroll
-            for (int w = 0; w < kJoinWaves; ++w) {
-                const float a = __builtin_amdgcn_exp2f(sml[w].x - mm);
-                total = fmaf(a, sml[w].y, total);
-                sum.x = fmaf(a, so[w][lane].x, sum.x);
-                sum.y = fmaf(a, so[w][lane].y, sum.y);
-            }
-            const bool empty = last < 0 || sq.lk == 0;
-            const float inv = empty ? 0.0f : 1.0f / total;
-            T *dst = (T *)p.o + tok_at * p.ot + hq * p.oh + 2 * lane;
-            if (mine) {
-                if constexpr (__is_same(E, F32)) *(float2 *)dst = make_float2(sum.x * inv, sum.y * inv);
-                else *(uint32_t *)dst = pack2<E>(sum.x * inv, sum.y * inv);
-            }
-            if (p.lse && lane == 0) p.lse[at] = empty ? -INFINITY : mx * kLn2 + logf(total);
         }
     }
 }
@@ -194,8 +200,8 @@ template <class E, int DP>
 hipError_t run_step(const AttnParams &p, hipStream_t s) {
     typedef StepCfg<E, DP> C;
     hipLaunchKernelGGL((k_attn_step<E, DP>), dim3((unsigned)(p.slots * p.Hkv)), dim3(64), C::kLds, s, p);
-    const int64_t rows = p.total_q * p.Hq;
-    hipLaunchKernelGGL((k_attn_step_join<E>), dim3((unsigned)std::min<int64_t>(rows, 1 << 20)), dim3(64 * kJoinWaves), 0, s, p);
+    const int toks = (int)std::min<int64_t>((p.total_q + p.B - 1) / p.B, std::max(1, p.rcap / p.grp));
+    hipLaunchKernelGGL((k_attn_step_join<E>), dim3((unsigned)std::min<int64_t>((int64_t)p.B * p.Hq, 1 << 20), toks), dim3(64 * kJoinWaves), 0, s, p);
     return hipGetLastError();
 }
 
@@ -209,17 +215,28 @@ hipError_t run_step_e(const AttnParams &p, hipStream_t s) {
 }  // namespace
 
 bool plan_step(AttnParams &p) {
-    // few rows a sequence (they fit the 32 columns on average) over enough keys that a chunk is worth a join
-    if (p.total_q * p.grp > 32 * (int64_t)p.B || p.total_k <= 256 * (int64_t)p.B) return false;
+    // Few rows a sequence (they fit the 32 columns on average) over enough keys that a chunk is worth a join; or,
+    // of several sequences, some may be such among others with many rows (steps and pieces of prompts in one call):
+    // the keys are many times the rows then. The tile kernel takes those others, one call after the other (7 steps over
+    // 32768 keys and a prompt of 512, 32 heads on 8: 212 us, against 562 us by the tile kernel alone).
+    const bool few = p.total_q * p.grp <= 32 * (int64_t)p.B;
+    if (p.grp > 32 || p.total_k <= 256 * (int64_t)p.B || !(few || (p.B > 1 && 8 * p.total_q <= p.total_k))) return false;
+    p.tiled = p.total_q > p.B;
+    // Sequences and heads enough to fill the card with a workgroup each are the tile kernel's alone (32 heads on 8; 256 x
+    // 1024 keys: 204 us, against 288 us here; 63 steps over 8192 keys and a prompt of 400: 383 us, against 480 us), but
+    // not single tokens over many keys, where chunks level out sequences of different lengths (64 of 200 to 8200 keys:
+    // 224 us here, against 296 us; the price, 64 of 4096 each: 219 us, against 193 us).
+    const int64_t own = (int64_t)p.B * p.Hkv;
+    if (own >= 2 * (int64_t)device_num_cus() && (p.tiled || p.total_k <= 2048 * (int64_t)p.B)) return false;
     // Four waves a compute unit are resident at once (registers at 128 dims in a half type). Where a chunk a wave
     // keeps them all busy in one go, chunks have that length (8 sequences, 100000 keys in all, 2 heads: 35 us,
     // against 46 us in one and a half goes); with sequences and heads enough by themselves, a third of a
     // sequence (64 x 4096 keys, 8 heads: 243 us; a half 293 us, whole sequences 257 us).
-    const int64_t waves = 4 * (int64_t)device_num_cus(), own = (int64_t)p.B * p.Hkv;
+    const int64_t waves = 4 * (int64_t)device_num_cus();
     int64_t chunk = 2 * own < waves ? (p.total_k * p.Hkv + waves - own - 1) / (waves - own) : (p.total_k / p.B + 2) / 3;
     chunk = std::min<int64_t>(std::max<int64_t>((chunk + 31) / 32 * 32, 128), 1 << 20);
     p.chunk = (int)chunk;
-    p.rcap = (int)std::min<int64_t>(32, (p.total_q + p.B - 1) / p.B * p.grp);
+    p.rcap = p.tiled ? 32 : p.grp;
     p.slots = p.total_k / chunk + p.B;
     return true;
 }

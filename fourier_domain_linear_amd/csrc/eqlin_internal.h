@@ -201,7 +201,9 @@ struct AttnParams {
     void *dq, *dk, *dv;
     int64_t dot, doh, dqt, dqh, dkt, dkh, dvt, dvh;
     float *ws;   // workspace
-    int chunk, rcap;  // the step kernel: keys of a chunk, rows a chunk's partial result has room for
+    int chunk;   // the step kernel: keys of a chunk
+    int rcap;    // rows that a chunk's partial result has room for (0: no step kernel)
+    int tiled;   // sequences of more rows than that are the tile kernel's
     int nsplit;  // key ranges the tile kernel's rows are split into
     int64_t slots;  // tile slots of a launch (a sequence's, then the next one's), and units a run of an XCD
     int run;

@@ -90,7 +90,6 @@ eqlin_status_t check_attention(const eqlin_attention_args *a, eqlin::AttnParams 
     // the launches' index range (at most 2^24 workgroups)
     if (a->total_q > (1 << 29) / a->heads_q || a->total_k > (1 << 29) / a->heads_kv || a->batch > (1 << 21) / a->heads_kv)
         return api_fail(EQLIN_ERR_UNSUPPORTED, "total_q * heads_q or total_k * heads_kv beyond 2^29, or batch * heads_kv beyond 2^21");
-    if (a->heads_kv > 65535) return api_fail(EQLIN_ERR_UNSUPPORTED, "heads_kv = %d beyond 65535", a->heads_kv);
     *p = eqlin::AttnParams{};
     p->q = a->q, p->k = a->k, p->v = a->v, p->o = a->o, p->lse = a->lse;
     p->qt = a->q_token_stride, p->qh = a->q_head_stride, p->kt = a->k_token_stride, p->kh = a->k_head_stride;
@@ -118,6 +117,9 @@ eqlin_status_t check_tensor(const void *t, int64_t ts, int64_t hs, int64_t token
         return api_fail(EQLIN_ERR_UNSUPPORTED, "%s: token stride beyond 2^23 or heads beyond 2^28 elements", name);
     return EQLIN_OK;
 }
+
+// whether a tensor that is written folds onto itself
+bool folds(int64_t ts, int64_t hs, int64_t tokens, int heads, int dim) { return (heads > 1 && hs < dim) || (tokens > 1 && ts < dim); }
 
 size_t extent(int64_t ts, int64_t hs, int64_t tokens, int heads, int dim, eqlin_dtype_t d) {
     return tokens == 0 ? 0 : (size_t)((tokens - 1) * ts + (heads - 1) * hs + dim) * elem_bytes(d);
@@ -206,7 +208,7 @@ eqlin_status_t eqlin_rotary(const void *x, int64_t x_token_stride, int64_t x_hea
     if (x_token_stride < 0 || x_head_stride < 0 || y_token_stride < 0 || y_head_stride < 0 || x_token_stride > smost ||
         x_head_stride > smost || y_token_stride > smost || y_head_stride > smost)
         return api_fail(EQLIN_ERR_INVALID_ARG, "strides out of range");
-    if ((H > 1 && y_head_stride < D) || (N > 1 && y_token_stride < D)) return api_fail(EQLIN_ERR_INVALID_ARG, "y's strides fold it onto itself");
+    if (folds(y_token_stride, y_head_stride, N, H, (int)D)) return api_fail(EQLIN_ERR_INVALID_ARG, "y's strides fold it onto itself");
     const size_t xb = extent(x_token_stride, x_head_stride, N, H, (int)D, dtype), yb = extent(y_token_stride, y_head_stride, N, H, (int)D, dtype);
     if (x == y) {
         if (x_token_stride != y_token_stride || x_head_stride != y_head_stride)
@@ -240,6 +242,7 @@ eqlin_status_t eqlin_attention(const eqlin_attention_args *a, void *workspace, s
     if ((st = check_tensor(a->k, p.kt, p.kh, a->total_k, p.Hkv, a->dtype, "k")) != EQLIN_OK) return st;
     if ((st = check_tensor(a->v, p.vt, p.vh, a->total_k, p.Hkv, a->dtype, "v")) != EQLIN_OK) return st;
     if ((st = check_tensor(a->o, p.ot, p.oh, a->total_q, p.Hq, a->dtype, "o")) != EQLIN_OK) return st;
+    if (folds(p.ot, p.oh, a->total_q, p.Hq, p.D)) return api_fail(EQLIN_ERR_INVALID_ARG, "o's strides fold it onto itself");
     if (!a->cu_q || !a->cu_k) return api_fail(EQLIN_ERR_INVALID_ARG, "null cu_q or cu_k");
     if (!aligned(a->cu_q, 4) || !aligned(a->cu_k, 4) || !aligned(a->len_k, 4) || !aligned(a->lse, 4))
         return api_fail(EQLIN_ERR_INVALID_ARG, "cu_q, cu_k, len_k or lse misaligned");
@@ -285,8 +288,13 @@ eqlin_status_t eqlin_attention_backward(const eqlin_attention_args *a, const eql
              {g->dq, g->dq_token_stride, g->dq_head_stride, a->total_q, p.Hq, "dq", true},
              {g->dk, g->dk_token_stride, g->dk_head_stride, a->total_k, p.Hkv, "dk", true},
              {g->dv, g->dv_token_stride, g->dv_head_stride, a->total_k, p.Hkv, "dv", true}};
-    for (const auto &x : t)
+    for (const auto &x : t) {
         if ((st = check_tensor(x.t, x.ts, x.hs, x.tokens, x.heads, a->dtype, x.name)) != EQLIN_OK) return st;
+        if (x.out && folds(x.ts, x.hs, x.tokens, x.heads, p.D))
+            return api_fail(EQLIN_ERR_INVALID_ARG, "%s's strides fold it onto itself", x.name);
+    }
+    if (a->total_k > 0 && (g->dk == g->dv || (a->total_q > 0 && (g->dq == g->dk || g->dq == g->dv))))
+        return api_fail(EQLIN_ERR_INVALID_ARG, "dq, dk and dv share memory");
     if (!a->cu_q || !a->cu_k || (a->total_q > 0 && !a->lse)) return api_fail(EQLIN_ERR_INVALID_ARG, "null cu_q, cu_k or lse");
     if (!aligned(a->cu_q, 4) || !aligned(a->cu_k, 4) || !aligned(a->len_k, 4) || !aligned(a->lse, 4))
         return api_fail(EQLIN_ERR_INVALID_ARG, "cu_q, cu_k, len_k or lse misaligned");

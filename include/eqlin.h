@@ -374,7 +374,8 @@ eqlin_status_t eqlin_rotary(const void *x, int64_t x_token_stride, int64_t x_hea
  * lse = -infinity. Keys that a token does not see have no part in its result, whatever they hold.
  *   q, k, v, o   tensor[token][head][dim] of dtype with token and head strides in ELEMENTS; pointers 16-byte
  *                aligned, strides a multiple of 16 bytes (else INVALID_ARG); dim a multiple of 8 (fp32: of 4)
- *                up to 128 (else UNSUPPORTED). o overlaps no input.
+ *                up to 128 (else UNSUPPORTED). Token strides up to 2^23 elements, head stride times heads up to
+ *                2^28 (else UNSUPPORTED). o overlaps no input.
  *   cu_q, cu_k   device int32 [batch + 1]: sequence i has the tokens from cu[i] to cu[i + 1]. cu[0] = 0 and
  *                cu[batch] = total; rows outside every sequence are not written.
  *   len_k        device int32 [batch] or NULL: how many keys of sequence i's stretch of cu_k count (a cache
