@@ -46,9 +46,10 @@ __device__ __forceinline__ void dq_block(f32x16 *dq, const uint4 *qf, const uint
     }
 }
 
-// delta of rows that see one tile of keys only: sum over its keys of P dP, in fp32 throughout. Over a handful of keys
-// the sum of dO O carries o's rounding into the gradients about as far as their own rounding; over more it is lost
-// among the terms. A row that sees one key has P = 1 and so dS = 0, exactly.
+// delta of rows that see no key past the first tile: sum over its keys of P dP, in fp32 throughout. Over a handful of
+// keys (short sequences, a causal sequence's first rows) the sum of dO O carries o's rounding into the gradients about
+// as far as their own rounding; over more it is lost among the terms. A row that sees one key has P = 1 and so dS = 0,
+// exactly.
 template <class E, int DP, int NKB>
 __device__ __forceinline__ float delta_of_tile(const uint4 *qf, const uint4 *gf, const typename Tile<E, DP>::Lane &L, uint32_t kt,
                                                uint32_t vt, float c, float lse2, int lim, int h) {
@@ -147,12 +148,17 @@ __global__ void __launch_bounds__(256, __is_same(E, F32) ? 1 : 2) k_attn_dq(cons
         }
     };
     if (r.wave_max >= 0) {
-        for (int k0 = 0; k0 < r.k_end; k0 += C::BN) {
-            arrive(k0);
+        arrive(0);
+        if (uniform(r.last) < C::BN) {  // the wave's first row, which sees least
+            const float d = delta_of_tile<E, DP, C::NKB>(qf, gf, L, lds0, lds0 + C::kTileBytes, c, lse2, r.last, h);
+            delta = r.last < C::BN ? d : delta;
+        }
+        for (int k0 = 0;;) {
             const uint32_t kt = lds0 + buf * 2 * C::kTileBytes, vt = kt + C::kTileBytes;
-            if (r.k_end <= C::BN) delta = delta_of_tile<E, DP, C::NKB>(qf, gf, L, kt, vt, c, lse2, r.last, h);
             dq_block<E, DP, C::NKB>(dq, qf, gf, L, kt, vt, c, lse2, delta, k0 + C::BN - 1 > r.wave_min, r.last - k0, h);
             buf ^= 1;
+            if ((k0 += C::BN) >= r.k_end) break;
+            arrive(k0);
         }
     } else {  // a wave without rows or keys fetches its part of the tiles
         for (int k0 = 0; k0 < r.k_end; k0 += C::BN) {
