@@ -3,9 +3,14 @@
 //
 //   dS = P (dP - delta);  dV = P^T dO;  dK = scale dS^T Q;  dQ = scale dS K
 //
-// Two passes, each owning its outputs: one over key tiles (dK, dV: every row that sees them, all heads of the
-// group, in order) and one over row tiles (dQ). S and dP are formed in both, 7 products instead of 5, and
-// nothing is added by atomics: the same bits every time, and no fp32 image of dQ in memory.
+// Two passes, each owning its outputs: one over row tiles (dQ, and delta for the other) and one over key tiles (dK,
+// dV: every row that sees them, all heads of the group, in order). S and dP are formed in both, 7 products instead of
+// 5, and nothing is added by atomics: the same bits every time, and no fp32 image of dQ in memory. P and dS are rounded to
+// the half types as operands of their products, dS after the subtraction; all else is fp32.
+//
+// Bound by the matrix cores and, at 128 dims, by the LDS reads that feed them. 4 x 4096 tokens, 16 heads, bf16, every key
+// seen: 2190 us at 128 dims (627 TFLOP/s of the formula's 5 products, 878 of the 7 formed; a large matrix product 1100),
+// 963 us at 64 (713 and 998).
 #include "attn.h"
 #include "attn_tile.h"
 
@@ -14,6 +19,7 @@ namespace eqlin {
 namespace {
 
 // ---- dQ: as the forward, 32 rows a wave (columns), key tiles through LDS ----
+// (16 heads on 4 of 128 dims, bf16, 4 causal sequences up to 4096, 3000 on average: 289 us of the backward's 890)
 
 template <class E, int DP, int NKB>
 __device__ __forceinline__ void dq_block(f32x16 *dq, const uint4 *qf, const uint4 *gf, const typename Tile<E, DP>::Lane &L, uint32_t kt,
@@ -177,6 +183,11 @@ __global__ void __launch_bounds__(256, __is_same(E, F32) ? 1 : 2) k_attn_dq(cons
 __host__ __device__ __forceinline__ int64_t share_offset(const AttnParams &p) { return (p.total_q * p.Hq + 63) / 64 * 64; }
 
 // ---- dK, dV: 32 keys a wave (columns), tiles of packed rows (q and dO) through LDS ----
+//
+// The keys' operands and dk and dv stay in a wave's registers: at 128 dims all of the 512, one wave a SIMD. A block of
+// 32 rows and 32 keys then reads 32 KB of q's and dO's fragments, for the four waves 1024 clocks of LDS, as long as its
+// 32 products of 32 clocks. (Two waves a SIMD with the keys in LDS read 48 KB and take the same time: 2171 us for the
+// backward above, against 2196 us.) The sequences above: 550 us of 890, and 45 us for the sum of the shares.
 
 // One group of the products that reduce over the tile's rows: the DP / 32 A fragments of reduction step f.
 template <class E, int DP>

@@ -1,5 +1,11 @@
 // attn_fwd.hip -- attention over packed sequences: o = softmax(scale q k^T) v, one pass over the keys with
 // the running maximum and sum.
+//
+// Bound by the matrix cores at 128 dims, and by the vector work beside them below: a 32 x 32 block of scores costs
+// 16 products of 32 clocks at 128 dims and 8 at 64, and at both 16 exponentials of 16 clocks and about 100 other vector
+// instructions of 4. 4 x 4096 tokens, 16 heads, bf16, every key seen: 520 to 600 us at 128 dims (0.92 to 1.05 PFLOP/s, by the
+// card's clock; a large matrix product reaches 1.1), 306 to 335 us at 64 (0.82 to 0.90), 248 us at 32 (0.55). fp32, 4096
+// tokens, 8 heads of 128: 613 us, 112 TFLOP/s (a matrix product: 153).
 #include "attn.h"
 #include "attn_fwd.h"
 
@@ -8,6 +14,10 @@ namespace eqlin {
 namespace {
 
 // ---- the tile kernel: 4 waves, each 32 packed rows (the columns of S^T), all over the same key tiles ----
+//
+// A wave's rows stay in registers as operands, its results as accumulators; k and v tiles pass through two LDS buffers,
+// the next one on its way while this one is multiplied. Four waves share a tile, so that its LDS reads (a fragment is
+// read once a wave) stay below the products' time, and short sequences do not lose a larger tile's padding.
 
 // Two shapes at DP = 128 in the half types. 64-key tiles at two waves a SIMD read V's fragments ahead of the
 // exponentials and pay the running maximum once for 64 keys (4 x 4096 tokens, 16 heads: 562 us, against 581 for the

