@@ -77,7 +77,12 @@ __device__ __forceinline__ float delta_of_tile(const uint4 *qf, const uint4 *gf,
     return half_sum(sum);
 }
 
-template <class E, int DP>
+// Partial sums in fp32 (shares of dq, or of dk and then dv) lie behind delta in the workspace.
+__host__ __device__ __forceinline__ int64_t share_offset(const AttnParams &p) { return (p.total_q * p.Hq + 63) / 64 * 64; }
+
+// SPLIT: a workgroup takes one of p.nsplit ranges of its keys. (Its own instance: the range's registers cost the launches
+// that fill the card without it 8 % at 128 dims.)
+template <class E, int DP, bool SPLIT>
 __global__ void __launch_bounds__(256, __is_same(E, F32) ? 1 : 2) k_attn_dq(const AttnParams p) {
     typedef TileCfg<E, DP> C;
     typedef Tile<E, DP> TL;
@@ -92,6 +97,13 @@ __global__ void __launch_bounds__(256, __is_same(E, F32) ? 1 : 2) k_attn_dq(cons
     const int row_wg = (int)tile * C::BM;
     if (tile < 0 || row_wg >= sq.lq * p.grp) return;
     const Rows r = rows_of(p, sq, hk, row_wg, C::BM, wave, lane);
+    int beg = 0, end = r.k_end;
+    if constexpr (SPLIT) {
+        const int tiles = (end + C::BN - 1) / C::BN, z = blockIdx.z;
+        beg = (int)((int64_t)tiles * z / p.nsplit) * C::BN;
+        end = min(end, (int)((int64_t)tiles * (z + 1) / p.nsplit) * C::BN);
+    }
+    const int k_beg = SPLIT ? beg : 0, k_end = SPLIT ? end : r.k_end;
     const T *kg = (const T *)p.k + sq.k0 * p.kt + hk * p.kh;
     const T *vg = (const T *)p.v + sq.k0 * p.vt + hk * p.vh;
     TileDma<E, DP, C::BN> tk, tv;
@@ -108,7 +120,7 @@ __global__ void __launch_bounds__(256, __is_same(E, F32) ? 1 : 2) k_attn_dq(cons
     zero_pad(lds, C::kLds, p.D, DP, tid);
     tk.offsets(p.kt, C::BN, wave, lane);
     tv.offsets(p.vt, C::BN, wave, lane);
-    if (r.k_end > 0) fetch(0, 0);
+    if (k_beg < k_end) fetch(k_beg, 0);
     const int64_t at = (sq.q0 + r.tok) * p.Hq + r.hq;
     uint4 qf[TL::kSteps], gf[TL::kSteps];
     load_row<E, DP>(qf, (const T *)p.q + (sq.q0 + r.tok) * p.qt + r.hq * p.qh, p.D, h);
@@ -140,7 +152,7 @@ __global__ void __launch_bounds__(256, __is_same(E, F32) ? 1 : 2) k_attn_dq(cons
     auto arrive = [&](int k0) {
         dma_wait();
         __syncthreads();  // this tile is in LDS; the other buffer has no more readers
-        if (k0 + C::BN < r.k_end) fetch(k0 + C::BN, buf ^ 1);
+        if (k0 + C::BN < k_end) fetch(k0 + C::BN, buf ^ 1);
         if (k0 + C::BN - 1 > r.all) {  // some row sees only part of it (uniform in the workgroup)
             char *kt = lds + 2 * buf * C::kTileBytes;
             const bool mine = __any(tile_nonfinite<E, 256>(kt, C::kTileBytes, tid));
@@ -153,34 +165,35 @@ __global__ void __launch_bounds__(256, __is_same(E, F32) ? 1 : 2) k_attn_dq(cons
             }
         }
     };
-    if (r.wave_max >= 0) {
-        arrive(0);
-        if (uniform(r.last) < C::BN) {  // the wave's first row, which sees least
+    if (k_beg < k_end && r.wave_max >= k_beg) {
+        arrive(k_beg);
+        if (k_beg == 0 && uniform(r.last) < C::BN) {  // the wave's first row, which sees least
             const float d = delta_of_tile<E, DP, C::NKB>(qf, gf, L, lds0, lds0 + C::kTileBytes, c, lse2, r.last, h);
             delta = r.last < C::BN ? d : delta;
         }
-        for (int k0 = 0;;) {
+        for (int k0 = k_beg;;) {
             const uint32_t kt = lds0 + buf * 2 * C::kTileBytes, vt = kt + C::kTileBytes;
             dq_block<E, DP, C::NKB>(dq, qf, gf, L, kt, vt, c, lse2, delta, k0 + C::BN - 1 > r.wave_min, r.last - k0, h);
             buf ^= 1;
-            if ((k0 += C::BN) >= r.k_end) break;
+            if ((k0 += C::BN) >= k_end) break;
             arrive(k0);
         }
     } else {  // a wave without rows or keys fetches its part of the tiles
-        for (int k0 = 0; k0 < r.k_end; k0 += C::BN) {
+        for (int k0 = k_beg; k0 < k_end; k0 += C::BN) {
             arrive(k0);
             buf ^= 1;
         }
     }
-    if (r.live && h == 0) p.ws[at] = delta;
+    if (r.live && h == 0 && (!SPLIT || blockIdx.z == 0)) p.ws[at] = delta;
     if (bad)
-        poison_columns<E, DP>(dq, max(0, r.all + 1) / C::BN * C::BN, min(r.wave_max, r.k_end - 1), p.D, h,
+        poison_columns<E, DP>(dq, k_beg + max(0, r.all + 1 - k_beg) / C::BN * C::BN, min(r.wave_max, k_end - 1), p.D, h,
                               [&](int j) { return kg + (int64_t)j * p.kt; }, [&](int j) { return j <= r.last; });
-    if (r.live) store_column<E, DP>(dq, p.scale, (T *)p.dq + (sq.q0 + r.tok) * p.dqt + r.hq * p.dqh, p.D, h);
+    if (!r.live) return;
+    if constexpr (SPLIT)  // fp32, for k_attn_sum
+        store_column<F32, DP>(dq, p.scale, p.ws + share_offset(p) + (blockIdx.z * p.total_q * p.Hq + at) * p.D, p.D, h);
+    else
+        store_column<E, DP>(dq, p.scale, (T *)p.dq + (sq.q0 + r.tok) * p.dqt + r.hq * p.dqh, p.D, h);
 }
-
-// the shares of dk and dv lie behind delta in the workspace
-__host__ __device__ __forceinline__ int64_t share_offset(const AttnParams &p) { return (p.total_q * p.Hq + 63) / 64 * 64; }
 
 // ---- dK, dV: 32 keys a wave (columns), tiles of packed rows (q and dO) through LDS ----
 //
@@ -400,7 +413,7 @@ __global__ void __launch_bounds__(256, __is_same(E, F32) || DP > 64 ? 1 : 2) k_a
 #pragma unroll
         for (int db = 0; db < DP / 32; ++db) dk[db] = zero16(), dv[db] = zero16();
     }
-    if (p.nsplit > 1) {  // a share: fp32, for k_attn_dkv_sum
+    if (p.nsplit > 1) {  // a share: fp32, for k_attn_sum
         const int64_t heads = p.total_k * p.Hkv, at = (sq.k0 + key) * p.Hkv + hk;
         float *part = p.ws + share_offset(p);
         store_column<F32, DP>(dk, p.scale, part + (z * heads + at) * p.D, p.D, h);
@@ -411,38 +424,60 @@ __global__ void __launch_bounds__(256, __is_same(E, F32) || DP > 64 ? 1 : 2) k_a
     store_column<E, DP>(dv, 1.0f, (T *)p.dv + (sq.k0 + key) * p.dvt + hk * p.dvh, p.D, h);
 }
 
-// dk and dv of the shares, in order: four values a thread.
+// out[token][head][.] = sum of the n partial results, in order: four values a thread. The parts of a second tensor lie
+// behind those of the first.
+struct Sum {
+    const float *part;
+    int64_t heads;  // tokens * H
+    int n, H, D;
+    void *out[2];
+    int64_t ts[2], hs[2];
+};
 template <class E>
-__global__ void __launch_bounds__(256) k_attn_dkv_sum(const AttnParams p) {
+__global__ void __launch_bounds__(256) k_attn_sum(const Sum p) {
     typedef typename ElemOf<E>::type T;
-    const int per = p.D / 4;
-    const int64_t heads = p.total_k * p.Hkv, n = heads * per;
-    const float *part = p.ws + share_offset(p);
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < 2 * n; i += (int64_t)gridDim.x * 256) {
-        const bool v = i >= n;
-        const int64_t e = v ? i - n : i, at = e / per;
-        const int d = (int)(e - at * per) * 4;
-        const float *src = part + (v ? p.nsplit * heads * p.D : 0) + at * p.D + d;
+    const int per = p.D / 4, w = blockIdx.y;
+    const int64_t n = p.heads * per, part = p.heads * p.D;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
+        const int64_t at = i / per;
+        const int d = (int)(i - at * per) * 4;
+        const float *src = p.part + w * p.n * part + at * p.D + d;
         float4 s = *(const float4 *)src;
-        for (int z = 1; z < p.nsplit; ++z) {
-            const float4 a = *(const float4 *)(src + z * heads * p.D);
+        for (int z = 1; z < p.n; ++z) {
+            const float4 a = *(const float4 *)(src + z * part);
             s.x += a.x, s.y += a.y, s.z += a.z, s.w += a.w;
         }
-        const int64_t key = at / p.Hkv;
-        const int hk = (int)(at - key * p.Hkv);
-        T *dst = v ? (T *)p.dv + key * p.dvt + hk * p.dvh + d : (T *)p.dk + key * p.dkt + hk * p.dkh + d;
+        const int64_t t = at / p.H;
+        T *dst = (T *)p.out[w] + t * p.ts[w] + (at - t * p.H) * p.hs[w] + d;
         if constexpr (__is_same(E, F32)) *(float4 *)dst = s;
         else *(uint2 *)dst = make_uint2(pack2<E>(s.x, s.y), pack2<E>(s.z, s.w));
     }
 }
+template <class E>
+void run_sum(const Sum &p, int tensors, hipStream_t s) {
+    const int64_t n = p.heads * (p.D / 4);
+    hipLaunchKernelGGL((k_attn_sum<E>), dim3((unsigned)std::min<int64_t>((n + 255) / 256, 1 << 16), tensors), dim3(256), 0, s, p);
+}
+
+// Key ranges that dq's row tiles are split into, where those do not fill the card: none shorter than 256 keys on average
+// (fp32, whose products take eight times as long: 64). One sequence of 1454, 2 heads on 1 of 40 dims, fp16: the backward in
+// 36 us, against 56 us unsplit; of 2827, 3 heads of 128, fp32: 461 us, against 809 us.
+int pick_ranges(const AttnParams &p, bool half) {
+    const int64_t wgs = std::max<int64_t>(1, (p.total_q * p.grp / 128 + p.B) * p.Hkv), want = 2 * (int64_t)device_num_cus();
+    const int64_t most = p.total_k / std::max(1, p.B) / (half ? 256 : 64);
+    return (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(want / wgs, most), 8));
+}
 
 // Shares that the rows of a key tile are split into, where the key tiles alone do not fill the card: a tile of a
 // causal sequence's first keys with grouped heads has thousands of rows, and one workgroup with them all is the
-// launch's whole time (4 sequences up to 4096, 16 heads on 4: 975 us in one share, 947 in 3, 888 in 6).
+// launch's whole time (4 sequences up to 4096, 16 heads on 4: 975 us in one share, 947 in 3, 888 in 6; shares of one
+// length instead, fewer for a tile of fewer rows, leave a longer tail: 900 to 920 us). Up to two workgroups a compute unit
+// shares go down to 64 rows (4 sequences up to 597, 8 heads on 2 of 64: 40 us, against 82 us in one).
 int pick_shares(const AttnParams &p) {
-    const int64_t wgs = (p.total_k / 128 + p.B) * p.Hkv, want = 8 * (int64_t)device_num_cus();
+    const int64_t wgs = std::max<int64_t>(1, (p.total_k / 128 + p.B) * p.Hkv), cus = device_num_cus();
     const int64_t rows = p.total_q * p.grp / std::max(1, p.B);  // of a sequence on average
-    return (int)std::min<int64_t>(std::min<int64_t>(want / std::max<int64_t>(1, wgs), rows / 512), 8);
+    const int64_t n = std::max(std::min(8 * cus / wgs, rows / 512), std::min(2 * cus / wgs, rows / 64));
+    return (int)std::max<int64_t>(1, std::min<int64_t>(n, 8));
 }
 
 template <class K>
@@ -456,23 +491,29 @@ hipError_t run_bwd(const AttnParams &p0, hipStream_t s) {
     AttnParams p = p0;
     typedef TileCfg<E, DP> CQ;
     typedef DkvCfg<E, DP> CK;
-    hipError_t e = set_lds(k_attn_dq<E, DP>, CQ::kLds + CQ::kFlags);
+    hipError_t e = set_lds(k_attn_dq<E, DP, false>, CQ::kLds + CQ::kFlags);
+    if (e == hipSuccess) e = set_lds(k_attn_dq<E, DP, true>, CQ::kLds + CQ::kFlags);
     if (e == hipSuccess) e = set_lds(k_attn_dkv<E, DP>, CK::kLds);
     if (e != hipSuccess) return e;
     if (p.total_q > 0) {
         p.slots = p.total_q * p.grp / CQ::BM + p.B;
         p.run = run_of(p.slots, p.B);
-        hipLaunchKernelGGL((k_attn_dq<E, DP>), dim3((unsigned)xcd_grid(p.slots, p.Hkv, p.run)), dim3(256), CQ::kLds + CQ::kFlags, s, p);
+        p.nsplit = pick_ranges(p, !__is_same(E, F32));
+        const dim3 grid((unsigned)xcd_grid(p.slots, p.Hkv, p.run), 1, p.nsplit);
+        if (p.nsplit > 1) {
+            hipLaunchKernelGGL((k_attn_dq<E, DP, true>), grid, dim3(256), CQ::kLds + CQ::kFlags, s, p);
+            run_sum<E>({p.ws + share_offset(p), p.total_q * p.Hq, p.nsplit, p.Hq, p.D, {p.dq}, {p.dqt}, {p.dqh}}, 1, s);
+        } else {
+            hipLaunchKernelGGL((k_attn_dq<E, DP, false>), grid, dim3(256), CQ::kLds + CQ::kFlags, s, p);
+        }
     }
     if (p.total_k > 0) {
         p.slots = p.total_k / CK::BK + p.B;
         p.run = run_of(p.slots, p.B);
-        p.nsplit = std::max(1, pick_shares(p));
+        p.nsplit = pick_shares(p);
         hipLaunchKernelGGL((k_attn_dkv<E, DP>), dim3((unsigned)xcd_grid(p.slots, p.Hkv * p.nsplit, p.run)), dim3(256), CK::kLds, s, p);
-        if (p.nsplit > 1) {
-            const int64_t n = p.total_k * p.Hkv * (p.D / 4) * 2;
-            hipLaunchKernelGGL((k_attn_dkv_sum<E>), dim3((unsigned)std::min<int64_t>((n + 255) / 256, 1 << 16)), dim3(256), 0, s, p);
-        }
+        if (p.nsplit > 1)
+            run_sum<E>({p.ws + share_offset(p), p.total_k * p.Hkv, p.nsplit, p.Hkv, p.D, {p.dk, p.dv}, {p.dkt, p.dvt}, {p.dkh, p.dvh}}, 2, s);
     }
     return hipGetLastError();
 }
@@ -486,11 +527,11 @@ hipError_t run_bwd_e(const AttnParams &p, hipStream_t s) {
 
 }  // namespace
 
-size_t attention_backward_workspace_bytes(const AttnParams &p) {
+size_t attention_backward_workspace_bytes(const AttnParams &p, eqlin_dtype_t dtype) {
     if (p.B <= 0) return 0;
-    const int n = pick_shares(p);
-    const size_t shares = n > 1 ? (size_t)2 * n * p.total_k * p.Hkv * p.D : 0;
-    return ((size_t)share_offset(p) + shares) * sizeof(float);
+    const size_t n = pick_shares(p), shares = n > 1 ? 2 * n * p.total_k * p.Hkv * p.D : 0;
+    const size_t m = pick_ranges(p, dtype != EQLIN_F32), ranges = m > 1 ? m * p.total_q * p.Hq * p.D : 0;
+    return ((size_t)share_offset(p) + std::max(shares, ranges)) * sizeof(float);
 }
 
 hipError_t launch_attention_backward(const AttnParams &p, eqlin_dtype_t dtype, hipStream_t s) {

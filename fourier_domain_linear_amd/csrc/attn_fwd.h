@@ -88,4 +88,57 @@ __device__ __forceinline__ void finish_rows(const AttnParams &p, const Seq &sq, 
     if (p.lse && h == 0) p.lse[(sq.q0 + r.tok) * p.Hq + r.hq] = empty ? -INFINITY : st.m * kLn2 + logf(l);
 }
 
+// ---- joining partial results: softmax sums over parts of a row's keys ----
+//
+// Part z of a row: (m, l) at ml[base + z step] and the D unnormalised values of o behind it at o[(base + z step) D]. A
+// wave joins the parts first, first + stride, ... of n, eight at a time with all loads in flight; lane l holds the
+// values 2 l and 2 l + 1.
+struct Joined {
+    float m, l;
+    float2 o;
+};
+__device__ __forceinline__ Joined join_parts(const float2 *ml, const float *o, int64_t base, int64_t step, int first, int stride, int n,
+                                             int D, int lane) {
+    constexpr int N = 8;
+    Joined r = {-INFINITY, 0.0f, make_float2(0.0f, 0.0f)};
+    const bool mine = 2 * lane < D;
+    for (int z0 = first; z0 < n; z0 += N * stride) {
+        float2 st[N], v[N];
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            const int z = z0 + j * stride;
+            const int64_t i = base + min(z, n - 1) * step;
+            st[j] = z < n ? ml[i] : make_float2(-INFINITY, 0.0f);
+            v[j] = z < n && mine ? *(const float2 *)(o + i * D + 2 * lane) : make_float2(0.0f, 0.0f);
+        }
+        float mn = r.m;
+#pragma unroll
+        for (int j = 0; j < N; ++j) mn = fmaxf(mn, st[j].x);
+        const float mm = mn == -INFINITY ? 0.0f : mn, a = __builtin_amdgcn_exp2f(r.m - mm);
+        r.l *= a, r.o.x *= a, r.o.y *= a;
+        r.m = mn;
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            const float w = __builtin_amdgcn_exp2f(st[j].x - mm);
+            r.l = fmaf(w, st[j].y, r.l);
+            r.o.x = fmaf(w, v[j].x, r.o.x);
+            r.o.y = fmaf(w, v[j].y, r.o.y);
+        }
+    }
+    return r;
+}
+
+// A joined row (head hq of query token t), normalised: o and lse.
+template <class E>
+__device__ __forceinline__ void finish_joined(const AttnParams &p, const Joined &r, int64_t t, int hq, bool empty, int lane) {
+    typedef typename ElemOf<E>::type T;
+    const float inv = empty ? 0.0f : 1.0f / r.l;
+    T *dst = (T *)p.o + t * p.ot + hq * p.oh + 2 * lane;
+    if (2 * lane < p.D) {
+        if constexpr (__is_same(E, F32)) *(float2 *)dst = make_float2(r.o.x * inv, r.o.y * inv);
+        else *(uint32_t *)dst = pack2<E>(r.o.x * inv, r.o.y * inv);
+    }
+    if (p.lse && lane == 0) p.lse[t * p.Hq + hq] = empty ? -INFINITY : r.m * kLn2 + logf(r.l);
+}
+
 }  // namespace eqlin

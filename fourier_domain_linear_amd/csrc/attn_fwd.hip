@@ -131,7 +131,7 @@ __global__ void __launch_bounds__(256, (FwdCfg<E, DP, SHORT>::WPE)) k_attn_fwd(c
         if (h == 0) {
             float *ml = p.ws + p.nsplit * rows * p.D + ((int64_t)blockIdx.z * rows + at) * 2;
             ml[0] = st.m;
-            ml[1] = r.last < 0 ? -1.0f : l;  // negative: a row that sees no key
+            ml[1] = l;
         }
         return;
     }
@@ -142,32 +142,16 @@ __global__ void __launch_bounds__(256, (FwdCfg<E, DP, SHORT>::WPE)) k_attn_fwd(c
 
 template <class E>
 __global__ void __launch_bounds__(256) k_attn_join(const AttnParams p) {
-    typedef typename ElemOf<E>::type T;
     const int lane = threadIdx.x & 63;
     const int64_t rows = p.total_q * p.Hq;
     for (int64_t at = (int64_t)blockIdx.x * 4 + uniform((int)(threadIdx.x >> 6)); at < rows; at += (int64_t)gridDim.x * 4) {
+        const Joined r = join_parts((const float2 *)(p.ws + p.nsplit * rows * p.D), p.ws, at, rows, 0, 1, p.nsplit, p.D, lane);
         const int tok = (int)(at / p.Hq), hq = (int)(at - (int64_t)tok * p.Hq);
         int seq;
         const Seq sq = seq_of_row(p, tok, seq);
-        if (tok < sq.q0 || tok >= sq.q0 + sq.lq || sq.lq * p.grp <= p.rcap) continue;
-        const float *ml = p.ws + p.nsplit * rows * p.D;
-        float m = -INFINITY;
-        for (int z = 0; z < p.nsplit; ++z) m = fmaxf(m, ml[(z * rows + at) * 2]);
-        const float mm = m == -INFINITY ? 0.0f : m;
-        float l = 0.0f, o0 = 0.0f, o1 = 0.0f;
-        for (int z = 0; z < p.nsplit; ++z) {
-            const float w = __builtin_amdgcn_exp2f(ml[(z * rows + at) * 2] - mm);
-            const float *o = p.ws + (z * rows + at) * p.D;
-            l = fmaf(w, ml[(z * rows + at) * 2 + 1], l);
-            if (lane < p.D) o0 = fmaf(w, o[lane], o0);
-            if (lane + 64 < p.D) o1 = fmaf(w, o[lane + 64], o1);
-        }
-        T *dst = (T *)p.o + tok * p.ot + hq * p.oh;
-        const bool empty = ml[at * 2 + 1] < 0.0f;  // the same in every range
-        const float inv = empty ? 0.0f : 1.0f / l;
-        if (lane < p.D) dst[lane] = Elem<E>::put(o0 * inv);
-        if (lane + 64 < p.D) dst[lane + 64] = Elem<E>::put(o1 * inv);
-        if (p.lse && lane == 0) p.lse[at] = empty ? -INFINITY : m * kLn2 + logf(l);
+        const int t = tok - (int)sq.q0;
+        if (t < 0 || t >= sq.lq || sq.lq * p.grp <= p.rcap) continue;
+        finish_joined<E>(p, r, tok, hq, sq.lk == 0 || (p.causal && t + sq.lk < sq.lq), lane);
     }
 }
 
@@ -199,22 +183,24 @@ hipError_t run_fwd_e(const AttnParams &p, hipStream_t s) {
     return run_fwd<E, 128, false>(p, s);
 }
 
-// Key ranges a launch is split into: enough workgroups for two a compute unit where the rows alone do not
-// give them, none shorter than 256 keys on average.
-int pick_nsplit(const AttnParams &p) {
+// Key ranges a launch is split into: enough workgroups for two a compute unit where the rows alone do not give them, or
+// four where so many are resident at once (half types up to 64 dims; 7 sequences up to 3102, 3 heads of 40, bf16: 53 us,
+// against 66 us with two), none shorter than 256 keys on average, or 64 in fp32, whose products take eight times as long
+// (9 sequences up to 650, 2 heads on 1 of 32: 19 us, against 38 us with 256).
+int pick_nsplit(const AttnParams &p, bool half) {
     const int64_t wgs = (p.total_q * p.grp / 128 + p.B) * p.Hkv;
-    const int64_t want = 2 * (int64_t)device_num_cus();
-    const int64_t most = std::max<int64_t>(1, p.total_k / p.B / 256);
+    const int64_t want = (half && p.D <= 64 ? 4 : 2) * (int64_t)device_num_cus();
+    const int64_t most = std::max<int64_t>(1, p.total_k / p.B / (half ? 256 : 64));
     return (int)std::min<int64_t>(std::max<int64_t>(1, want / std::max<int64_t>(1, wgs)), std::min<int64_t>(most, 64));
 }
 
 }  // namespace
 
-size_t attention_workspace_bytes(const AttnParams &p0, eqlin_dtype_t) {
+size_t attention_workspace_bytes(const AttnParams &p0, eqlin_dtype_t dtype) {
     AttnParams p = p0;
     if (p.total_q <= 0 || p.B <= 0) return 0;
     const bool step = plan_step(p);
-    const int n = pick_nsplit(p);
+    const int n = pick_nsplit(p, dtype != EQLIN_F32);
     const size_t parts = n <= 1 || (step && !p.tiled) ? 0 : (size_t)n * p.total_q * p.Hq * (p.D + 2) * sizeof(float);
     return parts + (step ? step_workspace_bytes(p) : 0);
 }
@@ -224,7 +210,7 @@ hipError_t launch_attention(const AttnParams &p0, eqlin_dtype_t dtype, hipStream
     const bool step = plan_step(p);
     if (!step || p.tiled) {
         AttnParams t = p;
-        t.nsplit = pick_nsplit(p);
+        t.nsplit = pick_nsplit(p, dtype != EQLIN_F32);
         if (step) t.ws += step_workspace_bytes(p) / sizeof(float);
         const hipError_t e = dtype == EQLIN_F32 ? run_fwd_e<F32>(t, s) : dtype == EQLIN_F16 ? run_fwd_e<F16>(t, s) : run_fwd_e<BF16>(t, s);
         if (e != hipSuccess || !step) return e;

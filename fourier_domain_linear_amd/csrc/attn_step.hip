@@ -122,7 +122,6 @@ __global__ void __launch_bounds__(64, DP > 64 ? 1 : 2) k_attn_step(const AttnPar
 constexpr int kJoinWaves = 16;
 template <class E>
 __global__ void __launch_bounds__(64 * kJoinWaves) k_attn_step_join(const AttnParams p) {
-    typedef typename ElemOf<E>::type T;
     __shared__ float2 so[kJoinWaves][64], sml[kJoinWaves];
     const int lane = threadIdx.x & 63, wave = uniform((int)(threadIdx.x >> 6));
     // (the loop over units: one turn, but for more than a million of them)
@@ -133,64 +132,28 @@ __global__ void __launch_bounds__(64 * kJoinWaves) k_attn_step_join(const AttnPa
         if (nr > p.rcap && p.tiled) continue;                      // the tile kernel's
         if (chunks == 1 || (nr > p.rcap && chunks > 0)) continue;  // written by the step itself
         for (int tok = blockIdx.y; tok < sq.lq; tok += gridDim.y) {
-            const int last = p.causal ? tok + sq.lk - sq.lq : sq.lk - 1;
-            const int64_t at = (sq.q0 + tok) * p.Hq + hq;
             const int64_t slot0 = slot_start(sq.k0, seq, 1, p.chunk);
             const int64_t base = (slot0 * p.Hkv + hk) * p.rcap + tok * p.grp + (hq - hk * p.grp), step = (int64_t)p.Hkv * p.rcap;
             const float2 *ml = (const float2 *)(p.ws + p.slots * p.Hkv * p.rcap * p.D);
             // each wave joins its own chunks (their loads wait for nothing), then the waves join
-            constexpr int N = 8;
-            float m = -INFINITY, l = 0.0f;
-            float2 o = make_float2(0.0f, 0.0f);
-            const bool mine = 2 * lane < p.D;
-            for (int z0 = wave; z0 < chunks; z0 += N * kJoinWaves) {
-                float2 st[N], v[N];
-#pragma unroll
-                for (int j = 0; j < N; ++j) {
-                    const int z = z0 + j * kJoinWaves;
-                    const int64_t i = base + min(z, chunks - 1) * step;
-                    st[j] = z < chunks ? ml[i] : make_float2(-INFINITY, 0.0f);
-                    v[j] = z < chunks && mine ? *(const float2 *)(p.ws + i * p.D + 2 * lane) : make_float2(0.0f, 0.0f);
-                }
-                float mn = m;
-#pragma unroll
-                for (int j = 0; j < N; ++j) mn = fmaxf(mn, st[j].x);
-                const float mm = mn == -INFINITY ? 0.0f : mn, a = __builtin_amdgcn_exp2f(m - mm);
-                l *= a, o.x *= a, o.y *= a;
-                m = mn;
-#pragma unroll
-                for (int j = 0; j < N; ++j) {
-                    const float w = __builtin_amdgcn_exp2f(st[j].x - mm);
-                    l = fmaf(w, st[j].y, l);
-                    o.x = fmaf(w, v[j].x, o.x);
-                    o.y = fmaf(w, v[j].y, o.y);
-                }
-            }
+            const Joined r = join_parts(ml, p.ws, base, step, wave, kJoinWaves, chunks, p.D, lane);
             __syncthreads();
-            so[wave][lane] = o;
-            if (lane == 0) sml[wave] = make_float2(m, l);
+            so[wave][lane] = r.o;
+            if (lane == 0) sml[wave] = make_float2(r.m, r.l);
             __syncthreads();
             if (wave == 0) {
-                float mx = -INFINITY, total = 0.0f;
-                float2 sum = make_float2(0.0f, 0.0f);
+                Joined all = {-INFINITY, 0.0f, make_float2(0.0f, 0.0f)};
 #pragma unroll
-                for (int w = 0; w < kJoinWaves; ++w) mx = fmaxf(mx, sml[w].x);
-                const float mm = mx == -INFINITY ? 0.0f : mx;
+                for (int w = 0; w < kJoinWaves; ++w) all.m = fmaxf(all.m, sml[w].x);
+                const float mm = all.m == -INFINITY ? 0.0f : all.m;
 #pragma unroll
                 for (int w = 0; w < kJoinWaves; ++w) {
                     const float a = __builtin_amdgcn_exp2f(sml[w].x - mm);
-                    total = fmaf(a, sml[w].y, total);
-                    sum.x = fmaf(a, so[w][lane].x, sum.x);
-                    sum.y = fmaf(a, so[w][lane].y, sum.y);
+                    all.l = fmaf(a, sml[w].y, all.l);
+                    all.o.x = fmaf(a, so[w][lane].x, all.o.x);
+                    all.o.y = fmaf(a, so[w][lane].y, all.o.y);
                 }
-                const bool empty = last < 0 || sq.lk == 0;
-                const float inv = empty ? 0.0f : 1.0f / total;
-                T *dst = (T *)p.o + (sq.q0 + tok) * p.ot + hq * p.oh + 2 * lane;
-                if (mine) {
-                    if constexpr (__is_same(E, F32)) *(float2 *)dst = make_float2(sum.x * inv, sum.y * inv);
-                    else *(uint32_t *)dst = pack2<E>(sum.x * inv, sum.y * inv);
-                }
-                if (p.lse && lane == 0) p.lse[at] = empty ? -INFINITY : mx * kLn2 + logf(total);
+                finish_joined<E>(p, all, sq.q0 + tok, hq, sq.lk == 0 || (p.causal && tok + sq.lk < sq.lq), lane);
             }
         }
     }

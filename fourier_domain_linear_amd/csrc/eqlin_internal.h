@@ -204,7 +204,7 @@ struct AttnParams {
     int chunk;   // the step kernel: keys of a chunk
     int rcap;    // rows that a chunk's partial result has room for (0: no step kernel)
     int tiled;   // sequences of more rows than that are the tile kernel's
-    int nsplit;  // key ranges the tile kernel's rows are split into
+    int nsplit;  // key ranges that rows are split into, or shares of the rows of a key tile (gradients)
     int64_t slots;  // tile slots of a launch (a sequence's, then the next one's), and units a run of an XCD
     int run;
 };
@@ -214,7 +214,7 @@ size_t step_workspace_bytes(const AttnParams &p);
 hipError_t launch_step(const AttnParams &p, eqlin_dtype_t dtype, hipStream_t s);
 size_t attention_workspace_bytes(const AttnParams &p, eqlin_dtype_t dtype);
 hipError_t launch_attention(const AttnParams &p, eqlin_dtype_t dtype, hipStream_t s);
-size_t attention_backward_workspace_bytes(const AttnParams &p);
+size_t attention_backward_workspace_bytes(const AttnParams &p, eqlin_dtype_t dtype);
 hipError_t launch_attention_backward(const AttnParams &p, eqlin_dtype_t dtype, hipStream_t s);
 
 }  // namespace eqlin

@@ -263,7 +263,7 @@ eqlin_status_t eqlin_attention(const eqlin_attention_args *a, void *workspace, s
 size_t eqlin_attention_backward_workspace(const eqlin_attention_args *a) {
     eqlin::AttnParams p;
     if (check_attention(a, &p) != EQLIN_OK) return 0;
-    return eqlin::attention_backward_workspace_bytes(p);
+    return eqlin::attention_backward_workspace_bytes(p, a->dtype);
 }
 
 eqlin_status_t eqlin_attention_backward(const eqlin_attention_args *a, const eqlin_attention_grads *g, void *workspace,
@@ -298,7 +298,7 @@ eqlin_status_t eqlin_attention_backward(const eqlin_attention_args *a, const eql
     if (!a->cu_q || !a->cu_k || (a->total_q > 0 && !a->lse)) return api_fail(EQLIN_ERR_INVALID_ARG, "null cu_q, cu_k or lse");
     if (!aligned(a->cu_q, 4) || !aligned(a->cu_k, 4) || !aligned(a->len_k, 4) || !aligned(a->lse, 4))
         return api_fail(EQLIN_ERR_INVALID_ARG, "cu_q, cu_k, len_k or lse misaligned");
-    if ((st = check_workspace(workspace, workspace_bytes, eqlin::attention_backward_workspace_bytes(p))) != EQLIN_OK) return st;
+    if ((st = check_workspace(workspace, workspace_bytes, eqlin::attention_backward_workspace_bytes(p, a->dtype))) != EQLIN_OK) return st;
     // dq, dk and dv may be interleaved parts of one tensor (the gradient of a qkv layer's output), so only an
     // output over an input is refused
     for (const auto &x : t)

@@ -123,3 +123,33 @@ def test_attention_gradients_of_a_causal_sequences_first_rows(cuda_device):
         err = np.linalg.norm(_np(g) - w) / np.linalg.norm(w)
         print(f"[parity] {name}: {err / 2 ** -8:.3f} u", flush=True)
         assert err <= 0.64 * 2 ** -8, name
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+def test_attention_gradients_of_few_rows(dtype, cuda_device):
+    """Few workgroups: dq's keys and dk's and dv's rows are split, with lengths that leave some parts empty."""
+    dev = cuda_device
+    for lq, lk, Hq, Hkv, D in (([40, 0, 7], [900, 30, 700], 4, 2, 64), ([300], [1100], 2, 1, 128), ([70, 500], [70, 20], 1, 1, 40)):
+        label = f"few {lq} {lk} {dtype}"
+        print(f"[case] {label}", flush=True)
+        q, k, v, do, cu_q, cu_k = _inputs(lq, lk, Hq, Hkv, D, dtype, dev, seed=16)
+        o, lse = eq.attention(q, k, v, cu_q, cu_k, causal=True)
+        grads = eq.attention_backward(do, q, k, v, o, lse, cu_q, cu_k, causal=True)
+        torch.cuda.synchronize()
+        _check_forward(o, lse, q, k, v, cu_q, cu_k, dtype, label, causal=True)
+        _check_grads(grads, do, q, k, v, cu_q, cu_k, dtype, label, causal=True)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_attention_gradients_of_rows_before_a_bad_key(dtype, cuda_device):
+    """A causal row's dq has no part of what later keys hold, where its keys are split into ranges too."""
+    q, k, v, do, cu_q, cu_k = _inputs([300], [1100], 4, 2, 64, dtype, cuda_device, seed=17)
+    run = lambda: (lambda o, lse: (o, eq.attention_backward(do, q, k, v, o, lse, cu_q, cu_k, causal=True)[0]))(  # noqa: E731
+        *eq.attention(q, k, v, cu_q, cu_k, causal=True))
+    o, dq = run()
+    k[1050] = float("nan")  # row 250 is the first to see it
+    v[1050] = float("inf")
+    o2, dq2 = run()
+    torch.cuda.synchronize()
+    assert torch.equal(o[:250], o2[:250]) and torch.equal(dq[:250], dq2[:250])
+    assert bool(o2[250:].isnan().all()) and bool(dq2[250:].isnan().all())
