@@ -8,7 +8,8 @@
 // 5, and nothing is added by atomics: the same bits every time, and no fp32 image of dQ in memory. P and dS are rounded to
 // the half types as operands of their products, dS after the subtraction; all else is fp32.
 //
-// Bound by the matrix cores and, at 128 dims, by the LDS reads that feed them. 4 x 4096 tokens, 16 heads, bf16, every key
+// dQ is bound as the forward is; dK and dV at 128 dims by one wave's chain of reads, products and exponentials (below).
+// 4 x 4096 tokens, 16 heads, bf16, every key
 // seen: 2190 us at 128 dims (627 TFLOP/s of the formula's 5 products, 878 of the 7 formed; a large matrix product 1100),
 // 963 us at 64 (713 and 998).
 #include "attn.h"
@@ -197,10 +198,10 @@ __global__ void __launch_bounds__(256, __is_same(E, F32) ? 1 : 2) k_attn_dq(cons
 
 // ---- dK, dV: 32 keys a wave (columns), tiles of packed rows (q and dO) through LDS ----
 //
-// The keys' operands and dk and dv stay in a wave's registers: at 128 dims all of the 512, one wave a SIMD. A block of
-// 32 rows and 32 keys then reads 32 KB of q's and dO's fragments, for the four waves 1024 clocks of LDS, as long as its
-// 32 products of 32 clocks. (Two waves a SIMD with the keys in LDS read 48 KB and take the same time: 2171 us for the
-// backward above, against 2196 us.) The sequences above: 550 us of 890, and 45 us for the sum of the shares.
+// The keys' operands and dk and dv stay in a wave's registers: at 128 dims 384 of the 512, one wave a SIMD, whose
+// exponentials wait for its products and its products for its reads: matrix cores 29 % busy, LDS 19 %, no bank conflicts.
+// (Two waves a SIMD, with the keys in LDS, read half as much again and take the same time: 2171 us for the backward
+// above, against 2196 us.) The sequences above: 550 us of 890, and 45 us for the sum of the shares.
 
 // One group of the products that reduce over the tile's rows: the DP / 32 A fragments of reduction step f.
 template <class E, int DP>
