@@ -3,6 +3,8 @@
 #include <hip/hip_runtime.h>
 #include <math.h>
 
+#include <algorithm>
+
 #include "eqlin_internal.h"
 
 using eqlin::api_fail;
@@ -113,7 +115,7 @@ eqlin_status_t check_tensor(const void *t, int64_t ts, int64_t hs, int64_t token
         return api_fail(EQLIN_ERR_INVALID_ARG, "%s must be 16-byte aligned, its strides multiples of %d elements", name, per);
     // a tile of up to 64 rows is addressed with 32-bit byte offsets from its first
     if (ts < 0 || hs < 0) return api_fail(EQLIN_ERR_INVALID_ARG, "%s: negative strides", name);
-    if (ts > (INT64_C(1) << 23) || hs * heads > (INT64_C(1) << 28))
+    if (ts > (INT64_C(1) << 23) || hs > (INT64_C(1) << 28) / heads)
         return api_fail(EQLIN_ERR_UNSUPPORTED, "%s: token stride beyond 2^23 or heads beyond 2^28 elements", name);
     return EQLIN_OK;
 }
@@ -208,6 +210,8 @@ eqlin_status_t eqlin_rotary(const void *x, int64_t x_token_stride, int64_t x_hea
     if (x_token_stride < 0 || x_head_stride < 0 || y_token_stride < 0 || y_head_stride < 0 || x_token_stride > smost ||
         x_head_stride > smost || y_token_stride > smost || y_head_stride > smost)
         return api_fail(EQLIN_ERR_INVALID_ARG, "strides out of range");
+    if (N > (INT64_C(1) << 56) / std::max<int64_t>(1, std::max(x_token_stride, y_token_stride)))
+        return api_fail(EQLIN_ERR_UNSUPPORTED, "N = %lld tokens of these strides overflow the index range", (long long)N);
     if (folds(y_token_stride, y_head_stride, N, H, (int)D)) return api_fail(EQLIN_ERR_INVALID_ARG, "y's strides fold it onto itself");
     const size_t xb = extent(x_token_stride, x_head_stride, N, H, (int)D, dtype), yb = extent(y_token_stride, y_head_stride, N, H, (int)D, dtype);
     if (x == y) {
