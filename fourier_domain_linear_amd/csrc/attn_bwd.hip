@@ -9,9 +9,9 @@
 // the half types as operands of their products, dS after the subtraction; all else is fp32.
 //
 // dQ is bound as the forward is; dK and dV at 128 dims by one wave's chain of reads, products and exponentials (below).
-// 4 x 4096 tokens, 16 heads, bf16, every key
-// seen: 2190 us at 128 dims (627 TFLOP/s of the formula's 5 products, 878 of the 7 formed; a large matrix product 1100),
-// 963 us at 64 (713 and 998).
+// 4 x 4096 tokens, 16 heads, bf16, every key seen: 2200 us at 128 dims (625 TFLOP/s of the formula's 5 products, 875 of the
+// 7 formed; a large matrix product 1100), 965 us at 64 (712 and 997). Launches that do not fill the card split dq's keys and
+// the rows of dk's and dv's key tiles, as partial sums in fp32 that k_attn_sum adds in order.
 #include "attn.h"
 #include "attn_tile.h"
 

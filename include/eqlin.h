@@ -385,6 +385,7 @@ eqlin_status_t eqlin_rotary(const void *x, int64_t x_token_stride, int64_t x_hea
  *                total_k * heads_kv <= 2^29 (else UNSUPPORTED).
  * Products and sums in fp32; the half types round the unnormalised probabilities (at most 2^8) to the type
  * for the second product.
+ * One call may hold sequences of one new token and whole prompts side by side.
  *   workspace    eqlin_attention_workspace(a) bytes, 256-byte aligned (NULL when that is 0): partial results
  *                where few query rows make it split the keys. Calls sharing it must not overlap.
  */
