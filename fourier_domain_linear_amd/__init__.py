@@ -638,7 +638,7 @@ def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_q: torch.Ten
     heads may be strided views, e.g. of a qkv layer's output), k and v: the same with Hkv heads, Hq a multiple
     of Hkv. cu_q, cu_k: int32 [batch + 1], the sequences' bounds in tokens; len_k: int32 [batch], how many keys
     of each stretch count. causal: token t of lq sees the keys j <= t + lk - lq. scale: 1/sqrt(D) if None.
-    o: like q; lse: float32 [T, Hq]."""
+    o: like q; lse: float32 [T, Hq]. Rows outside every sequence are left as they are."""
     a, out, lse = _attention_args(q, k, v, out, None, cu_q, cu_k, len_k, causal, scale)
     lib, pa = load_library(), ctypes.byref(a)
     need = lib.eqlin_attention_workspace(pa)

@@ -426,9 +426,12 @@ __global__ void __launch_bounds__(256, __is_same(E, F32) || DP > 64 ? 1 : 2) k_a
 }
 
 // out[token][head][.] = sum of the n partial results, in order: four values a thread. The parts of a second tensor lie
-// behind those of the first.
+// behind those of the first. Sequences are stretches one behind the other, so a token in front of the first bound or from
+// the last on is none's: nobody wrote its parts, and it is left as it is.
 struct Sum {
     const float *part;
+    const int *cu;
+    int B;
     int64_t heads;  // tokens * H
     int n, H, D;
     void *out[2];
@@ -437,10 +440,11 @@ struct Sum {
 template <class E>
 __global__ void __launch_bounds__(256) k_attn_sum(const Sum p) {
     typedef typename ElemOf<E>::type T;
-    const int per = p.D / 4, w = blockIdx.y;
+    const int per = p.D / 4, w = blockIdx.y, begin = p.cu[0], end = p.cu[p.B];
     const int64_t n = p.heads * per, part = p.heads * p.D;
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
-        const int64_t at = i / per;
+        const int64_t at = i / per, t = at / p.H;
+        if (t < begin || t >= end) continue;
         const int d = (int)(i - at * per) * 4;
         const float *src = p.part + w * p.n * part + at * p.D + d;
         float4 s = *(const float4 *)src;
@@ -448,7 +452,6 @@ __global__ void __launch_bounds__(256) k_attn_sum(const Sum p) {
             const float4 a = *(const float4 *)(src + z * part);
             s.x += a.x, s.y += a.y, s.z += a.z, s.w += a.w;
         }
-        const int64_t t = at / p.H;
         T *dst = (T *)p.out[w] + t * p.ts[w] + (at - t * p.H) * p.hs[w] + d;
         if constexpr (__is_same(E, F32)) *(float4 *)dst = s;
         else *(uint2 *)dst = make_uint2(pack2<E>(s.x, s.y), pack2<E>(s.z, s.w));
@@ -503,7 +506,7 @@ hipError_t run_bwd(const AttnParams &p0, hipStream_t s) {
         const dim3 grid((unsigned)xcd_grid(p.slots, p.Hkv, p.run), 1, p.nsplit);
         if (p.nsplit > 1) {
             hipLaunchKernelGGL((k_attn_dq<E, DP, true>), grid, dim3(256), CQ::kLds + CQ::kFlags, s, p);
-            run_sum<E>({p.ws + share_offset(p), p.total_q * p.Hq, p.nsplit, p.Hq, p.D, {p.dq}, {p.dqt}, {p.dqh}}, 1, s);
+            run_sum<E>({p.ws + share_offset(p), p.cu_q, p.B, p.total_q * p.Hq, p.nsplit, p.Hq, p.D, {p.dq}, {p.dqt}, {p.dqh}}, 1, s);
         } else {
             hipLaunchKernelGGL((k_attn_dq<E, DP, false>), grid, dim3(256), CQ::kLds + CQ::kFlags, s, p);
         }
@@ -514,7 +517,7 @@ hipError_t run_bwd(const AttnParams &p0, hipStream_t s) {
         p.nsplit = pick_shares(p);
         hipLaunchKernelGGL((k_attn_dkv<E, DP>), dim3((unsigned)xcd_grid(p.slots, p.Hkv * p.nsplit, p.run)), dim3(256), CK::kLds, s, p);
         if (p.nsplit > 1)
-            run_sum<E>({p.ws + share_offset(p), p.total_k * p.Hkv, p.nsplit, p.Hkv, p.D, {p.dk, p.dv}, {p.dkt, p.dvt}, {p.dkh, p.dvh}}, 2, s);
+            run_sum<E>({p.ws + share_offset(p), p.cu_k, p.B, p.total_k * p.Hkv, p.nsplit, p.Hkv, p.D, {p.dk, p.dv}, {p.dkt, p.dvt}, {p.dkh, p.dvh}}, 2, s);
     }
     return hipGetLastError();
 }

@@ -376,8 +376,9 @@ eqlin_status_t eqlin_rotary(const void *x, int64_t x_token_stride, int64_t x_hea
  *                aligned, strides a multiple of 16 bytes (else INVALID_ARG); dim a multiple of 8 (fp32: of 4)
  *                up to 128 (else UNSUPPORTED). Token strides up to 2^23 elements, head stride times heads up to
  *                2^28 (else UNSUPPORTED). o overlaps no input.
- *   cu_q, cu_k   device int32 [batch + 1]: sequence i has the tokens from cu[i] to cu[i + 1]. cu[0] = 0 and
- *                cu[batch] = total; rows outside every sequence are not written.
+ *   cu_q, cu_k   device int32 [batch + 1], not decreasing: sequence i has the tokens from cu[i] to cu[i + 1]. Rows
+ *                outside every sequence (in front of cu[0], from cu[batch] on: tensors of a fixed capacity) are
+ *                neither read for a result nor written, here and in the gradients.
  *   len_k        device int32 [batch] or NULL: how many keys of sequence i's stretch of cu_k count (a cache
  *                with room to grow).
  *   lse          device float [total_q][heads_q] or NULL (the backward needs it).
