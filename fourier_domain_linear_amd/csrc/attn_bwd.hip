@@ -81,8 +81,9 @@ __device__ __forceinline__ float delta_of_tile(const uint4 *qf, const uint4 *gf,
 // Partial sums in fp32 (shares of dq, or of dk and then dv) lie behind delta in the workspace.
 __host__ __device__ __forceinline__ int64_t share_offset(const AttnParams &p) { return (p.total_q * p.Hq + 63) / 64 * 64; }
 
-// SPLIT: a workgroup takes one of p.nsplit ranges of its keys. (Its own instance: the range's registers cost the launches
-// that fill the card without it 8 % at 128 dims.)
+// SPLIT: a workgroup takes one of p.nsplit ranges of its keys; range 0 has the first tile wherever there is one, and so the
+// delta of rows that see few keys. (Its own instance: the range's registers cost the launches that fill the card without it
+// 8 % at 128 dims.)
 template <class E, int DP, bool SPLIT>
 __global__ void __launch_bounds__(256, __is_same(E, F32) ? 1 : 2) k_attn_dq(const AttnParams p) {
     typedef TileCfg<E, DP> C;
@@ -101,8 +102,9 @@ __global__ void __launch_bounds__(256, __is_same(E, F32) ? 1 : 2) k_attn_dq(cons
     int beg = 0, end = r.k_end;
     if constexpr (SPLIT) {
         const int tiles = (end + C::BN - 1) / C::BN, z = blockIdx.z;
-        beg = (int)((int64_t)tiles * z / p.nsplit) * C::BN;
-        end = min(end, (int)((int64_t)tiles * (z + 1) / p.nsplit) * C::BN);
+        auto first_of = [&](int i) { return (int)(((int64_t)tiles * i + p.nsplit - 1) / p.nsplit) * C::BN; };
+        beg = first_of(z);
+        end = min(end, first_of(z + 1));
     }
     const int k_beg = SPLIT ? beg : 0, k_end = SPLIT ? end : r.k_end;
     const T *kg = (const T *)p.k + sq.k0 * p.kt + hk * p.kh;

@@ -1,12 +1,13 @@
 """GPU tests of the attention gradients where a launch too small to fill the card is split (dq's keys into ranges, the rows of
-dk's and dv's key tiles into shares): rows that belong to no sequence. Bars as in test_attention_gpu.py."""
+dk's and dv's key tiles into shares): rows that belong to no sequence, and delta of rows that see few keys. Bars as in
+test_attention_gpu.py."""
 import ctypes
 
 import pytest
 import torch
 
 import fourier_domain_linear_amd as eq
-from test_attention_gpu import _check_grads, _inputs
+from test_attention_gpu import DT, _check_grads, _cu, _inputs
 
 pytestmark = pytest.mark.gpu
 
@@ -53,3 +54,42 @@ def test_rows_outside_every_sequence_are_not_written(name, dtype, causal, cuda_d
             rows = torch.cat([t[:front], t[front + n:]])
             assert bool((rows == 7.0).all()), (what, fill)
         _check_grads([g[front:front + n] for g in grads], do, q, k, v, cu, cu, dtype, f"outside {name} {dtype}", causal=causal)
+
+
+@pytest.mark.parametrize("causal", [False, True], ids=["full", "causal"])
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+def test_one_key_has_no_score_gradient_in_a_split_launch(dtype, causal, cuda_device):
+    """Softmax over one key is 1 whatever the score, so sequences of one key leave dq and dk at zero, to the bit, next to one
+    that splits the launch too; so does a causal sequence whose first row alone has a gradient."""
+    lens = [1, 1, 2600, 1]
+    q, k, v, do, cu, _ = _inputs(lens, lens, 4, 2, 64, dtype, cuda_device, seed=22)
+    o, lse = eq.attention(q, k, v, cu, cu, causal=causal)
+    assert _splits(q, k, v, o, lse, cu, cu, causal)
+    dq, dk, dv = eq.attention_backward(do, q, k, v, o, lse, cu, cu, causal=causal)
+    torch.cuda.synchronize()
+    short = [0, 1, sum(lens) - 1]
+    assert not dq[short].any() and not dk[short].any() and dv[short].any()
+    if causal:
+        do[3:sum(lens) - 1] = 0  # (the long sequence's rows but its first)
+        dq, dk, dv = eq.attention_backward(do, q, k, v, o, lse, cu, cu, causal=True)
+        torch.cuda.synchronize()
+        assert not dq.any() and not dk.any() and dv[2].any()
+
+
+@pytest.mark.parametrize("heads", [(1, 1), (2, 1), (8, 8)], ids=["h1", "h2on1", "h8"])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_delta_of_first_rows_in_a_split_launch(dtype, heads, cuda_device):
+    """The first 64 rows of a causal sequence of 2048 alone have a gradient, and all values have a large common part: dP - delta
+    is then small against delta, and a delta from the rounded o would be off by u |o| |dO|, many times the bars. delta of
+    rows that see no key past the first tile comes from the tile's own probabilities, for dk as well as for dq."""
+    n, D, (Hq, Hkv) = 2048, 128, heads
+    q, k, v, do, cu, _ = _inputs([n], [n], Hq, Hkv, D, dtype, cuda_device, seed=23)
+    v = (8 + v / 4).to(DT[dtype])
+    do[64:] = 0
+    o, lse = eq.attention(q, k, v, cu, cu, causal=True)
+    assert _splits(q, k, v, o, lse, cu, cu, True)
+    grads = eq.attention_backward(do, q, k, v, o, lse, cu, cu, causal=True)
+    torch.cuda.synchronize()
+    assert not any(bool(g[64:].any()) for g in grads)
+    first = _cu([64], cuda_device)
+    _check_grads([g[:64] for g in grads], do[:64], q[:64], k[:64], v[:64], first, first, dtype, f"first rows {dtype} {heads}", causal=True)
