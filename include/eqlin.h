@@ -410,8 +410,8 @@ eqlin_status_t eqlin_attention(const eqlin_attention_args *a, void *workspace, s
 /*
  * eqlin_attention_backward -- dq, dk, dv from d_o (the gradient of o; lse's is zero). a: the forward's
  * arguments, with its o and lse. d_o, dq, dk, dv: as q, o, k, v, with strides; outputs are overwritten (keys
- * beyond len_k get zeros). Probabilities and score gradients are rounded to the half type for their products;
- * everything else is fp32. workspace: eqlin_attention_backward_workspace(a) bytes, 256-byte aligned.
+ * beyond len_k get zeros). Probabilities and score gradients are rounded to the half type for their products, in
+ * fp16 scaled by powers of two so that neither end of the type's range is met; everything else is fp32. workspace: eqlin_attention_backward_workspace(a) bytes, 256-byte aligned.
  */
 typedef struct eqlin_attention_grads {
     const void *d_o;
