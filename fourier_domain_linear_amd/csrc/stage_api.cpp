@@ -14,7 +14,26 @@ namespace {
 bool aligned(const void *p, size_t a) { return ((uintptr_t)p % a) == 0; }
 bool overlap(const void *a, size_t na, const void *b, size_t nb) {
     const char *x = (const char *)a, *y = (const char *)b;
-    return a && b && x < y + nb && y < x + na;
+    return a && b && na && nb && x < y + nb && y < x + na;
+}
+// memory of an argument, from its first byte to its last
+struct Span {
+    const void *at;
+    size_t bytes;
+    const char *name;
+};
+// What is written overlaps neither what is read nor other memory that is written.
+template <size_t NO, size_t NI>
+eqlin_status_t check_apart(const Span (&outs)[NO], const Span (&ins)[NI]) {
+    for (size_t a = 0; a < NO; ++a) {
+        for (const Span &in : ins)
+            if (overlap(outs[a].at, outs[a].bytes, in.at, in.bytes))
+                return api_fail(EQLIN_ERR_INVALID_ARG, "%s overlaps the input %s", outs[a].name, in.name);
+        for (size_t b = 0; b < a; ++b)
+            if (overlap(outs[a].at, outs[a].bytes, outs[b].at, outs[b].bytes))
+                return api_fail(EQLIN_ERR_INVALID_ARG, "%s overlaps %s", outs[a].name, outs[b].name);
+    }
+    return EQLIN_OK;
 }
 size_t elem_bytes(eqlin_dtype_t d) { return d == EQLIN_F32 ? 4 : 2; }
 bool valid_dtype(eqlin_dtype_t d) { return d == EQLIN_F32 || d == EQLIN_BF16 || d == EQLIN_F16; }
@@ -61,16 +80,9 @@ eqlin_status_t rmsnorm(const void *x, const void *residual, const void *gamma, v
         return api_fail(EQLIN_ERR_INVALID_ARG, "x, residual, sum and the output must be 16-byte aligned");
     if (!aligned(gamma, eb) || !aligned(rstd, 4) || !aligned(scale, 4)) return api_fail(EQLIN_ERR_INVALID_ARG, "gamma, rstd or scale misaligned");
     const size_t ob = quant ? n : n * eb;
-    const void *ins[] = {x, residual, gamma};
-    const size_t in_bytes[] = {n * eb, n * eb, (size_t)C * eb};
-    void *outs[] = {sum, const_cast<void *>(out), rstd, scale};
-    const size_t out_bytes[] = {n * eb, ob, (size_t)N * 4, (size_t)N * 4};
-    for (int a = 0; a < 4; ++a) {
-        for (int b = 0; b < 3; ++b)
-            if (overlap(outs[a], out_bytes[a], ins[b], in_bytes[b])) return api_fail(EQLIN_ERR_INVALID_ARG, "an output overlaps an input");
-        for (int b = 0; b < a; ++b)
-            if (overlap(outs[a], out_bytes[a], outs[b], out_bytes[b])) return api_fail(EQLIN_ERR_INVALID_ARG, "outputs overlap");
-    }
+    const Span ins[] = {{x, n * eb, "x"}, {residual, n * eb, "residual"}, {gamma, (size_t)C * eb, "gamma"}};
+    const Span outs[] = {{sum, n * eb, "sum"}, {out, ob, quant ? "q" : "y"}, {rstd, (size_t)N * 4, "rstd"}, {scale, (size_t)N * 4, "scale"}};
+    if ((st = check_apart(outs, ins)) != EQLIN_OK) return st;
     eqlin::NormParams p = {x, residual, gamma, sum, y, q, scale, rstd, N, C, ilog2(G), eps};
     (void)hipGetLastError();
     return done(eqlin::launch_rmsnorm(p, dtype, (hipStream_t)stream), what);
@@ -120,8 +132,32 @@ eqlin_status_t check_tensor(const void *t, int64_t ts, int64_t hs, int64_t token
     return EQLIN_OK;
 }
 
+// Whether heads of two tensors of one layout share elements: head j of token i is the dim elements from i ts + j hs on (and
+// `by` further in the second tensor). Only differences of tokens and heads count; of the two kinds the one with fewer
+// values is gone through, and the other's then lie in a range. self: the second tensor is the first.
+bool heads_meet(int64_t ts, int64_t hs, int64_t dim, int64_t tokens1, int64_t heads1, int64_t tokens2, int64_t heads2, int64_t by, bool self) {
+    if (tokens1 + tokens2 < heads1 + heads2) return heads_meet(hs, ts, dim, heads1, tokens1, heads2, tokens2, by, self);
+    auto floor_div = [](int64_t a, int64_t b) { return a / b - (a % b < 0); };  // b > 0
+    for (int64_t j = -(heads1 - 1); j < heads2; ++j) {
+        const int64_t at = by + j * hs;
+        int64_t lo = -(tokens1 - 1), hi = tokens2 - 1;  // differences i with |at + i ts| < dim
+        if (ts > 0) {
+            lo = std::max(lo, floor_div(-dim - at, ts) + 1);
+            hi = std::min(hi, -floor_div(at - dim, ts) - 1);
+        } else if (at <= -dim || at >= dim) {
+            continue;
+        }
+        if (self && j == 0 ? lo < 0 || hi > 0 : lo <= hi) return true;
+    }
+    return false;
+}
+
 // whether a tensor that is written folds onto itself
-bool folds(int64_t ts, int64_t hs, int64_t tokens, int heads, int dim) { return (heads > 1 && hs < dim) || (tokens > 1 && ts < dim); }
+bool folds(int64_t ts, int64_t hs, int64_t tokens, int heads, int dim) {
+    if ((heads > 1 && hs < dim) || (tokens > 1 && ts < dim)) return true;
+    if (heads <= 1 || tokens <= 1 || ts >= (heads - 1) * hs + dim || hs >= (tokens - 1) * ts + dim) return false;
+    return heads_meet(ts, hs, dim, tokens, heads, tokens, heads, 0, true);
+}
 
 size_t extent(int64_t ts, int64_t hs, int64_t tokens, int heads, int dim, eqlin_dtype_t d) {
     return tokens == 0 ? 0 : (size_t)((tokens - 1) * ts + (heads - 1) * hs + dim) * elem_bytes(d);
@@ -165,12 +201,9 @@ eqlin_status_t eqlin_rmsnorm_backward(const void *sum, const void *gamma, const 
         const size_t need = dgamma ? eqlin::rmsnorm_backward_workspace_bytes(N, C, G) : 0;
         st = check_workspace(workspace, workspace_bytes, need);
         if (st != EQLIN_OK) return st;
-        const void *ins[] = {sum, dy, dsum, gamma, rstd};
-        const size_t in_bytes[] = {n * eb, n * eb, n * eb, (size_t)C * eb, (size_t)N * 4};
-        for (int b = 0; b < 5; ++b)
-            if (overlap(dx, n * eb, ins[b], in_bytes[b]) || overlap(dgamma, (size_t)C * 4, ins[b], in_bytes[b]))
-                return api_fail(EQLIN_ERR_INVALID_ARG, "an output overlaps an input");
-        if (overlap(dx, n * eb, dgamma, (size_t)C * 4)) return api_fail(EQLIN_ERR_INVALID_ARG, "outputs overlap");
+        const Span ins[] = {{sum, n * eb, "sum"}, {dy, n * eb, "dy"}, {dsum, n * eb, "dsum"}, {gamma, (size_t)C * eb, "gamma"}, {rstd, (size_t)N * 4, "rstd"}};
+        const Span outs[] = {{dx, n * eb, "dx"}, {dgamma, (size_t)C * 4, "dgamma"}, {workspace, need, "workspace"}};
+        if ((st = check_apart(outs, ins)) != EQLIN_OK) return st;
     }
     eqlin::NormGradParams p = {sum, gamma, dy, dsum, rstd, dx, dgamma, (float *)workspace, N, C, ilog2(G)};
     (void)hipGetLastError();
@@ -250,15 +283,14 @@ eqlin_status_t eqlin_attention(const eqlin_attention_args *a, void *workspace, s
     if (!a->cu_q || !a->cu_k) return api_fail(EQLIN_ERR_INVALID_ARG, "null cu_q or cu_k");
     if (!aligned(a->cu_q, 4) || !aligned(a->cu_k, 4) || !aligned(a->len_k, 4) || !aligned(a->lse, 4))
         return api_fail(EQLIN_ERR_INVALID_ARG, "cu_q, cu_k, len_k or lse misaligned");
-    if ((st = check_workspace(workspace, workspace_bytes, eqlin::attention_workspace_bytes(p, a->dtype))) != EQLIN_OK) return st;
-    const size_t ob = extent(p.ot, p.oh, a->total_q, p.Hq, p.D, a->dtype), lb = (size_t)a->total_q * p.Hq * 4;
-    const void *ins[] = {a->q, a->k, a->v};
-    const size_t in_bytes[] = {extent(p.qt, p.qh, a->total_q, p.Hq, p.D, a->dtype), extent(p.kt, p.kh, a->total_k, p.Hkv, p.D, a->dtype),
-                               extent(p.vt, p.vh, a->total_k, p.Hkv, p.D, a->dtype)};
-    for (int i = 0; i < 3; ++i)
-        if (overlap(a->o, ob, ins[i], in_bytes[i]) || overlap(a->lse, lb, ins[i], in_bytes[i]))
-            return api_fail(EQLIN_ERR_INVALID_ARG, "an output overlaps an input");
-    if (overlap(a->lse, lb, a->o, ob)) return api_fail(EQLIN_ERR_INVALID_ARG, "o and lse overlap");
+    const size_t need = eqlin::attention_workspace_bytes(p, a->dtype), cu = ((size_t)a->batch + 1) * 4;
+    if ((st = check_workspace(workspace, workspace_bytes, need)) != EQLIN_OK) return st;
+    const Span ins[] = {{a->q, extent(p.qt, p.qh, a->total_q, p.Hq, p.D, a->dtype), "q"}, {a->k, extent(p.kt, p.kh, a->total_k, p.Hkv, p.D, a->dtype), "k"},
+                        {a->v, extent(p.vt, p.vh, a->total_k, p.Hkv, p.D, a->dtype), "v"}, {a->cu_q, cu, "cu_q"}, {a->cu_k, cu, "cu_k"},
+                        {a->len_k, cu - 4, "len_k"}};
+    const Span outs[] = {{a->o, extent(p.ot, p.oh, a->total_q, p.Hq, p.D, a->dtype), "o"}, {a->lse, (size_t)a->total_q * p.Hq * 4, "lse"},
+                         {workspace, need, "workspace"}};
+    if ((st = check_apart(outs, ins)) != EQLIN_OK) return st;
     p.ws = (float *)workspace;
     (void)hipGetLastError();
     return done(eqlin::launch_attention(p, a->dtype, (hipStream_t)stream), "eqlin_attention launch");
@@ -297,19 +329,32 @@ eqlin_status_t eqlin_attention_backward(const eqlin_attention_args *a, const eql
         if (x.out && folds(x.ts, x.hs, x.tokens, x.heads, p.D))
             return api_fail(EQLIN_ERR_INVALID_ARG, "%s's strides fold it onto itself", x.name);
     }
-    if (a->total_k > 0 && (g->dk == g->dv || (a->total_q > 0 && (g->dq == g->dk || g->dq == g->dv))))
-        return api_fail(EQLIN_ERR_INVALID_ARG, "dq, dk and dv share memory");
     if (!a->cu_q || !a->cu_k || (a->total_q > 0 && !a->lse)) return api_fail(EQLIN_ERR_INVALID_ARG, "null cu_q, cu_k or lse");
     if (!aligned(a->cu_q, 4) || !aligned(a->cu_k, 4) || !aligned(a->len_k, 4) || !aligned(a->lse, 4))
         return api_fail(EQLIN_ERR_INVALID_ARG, "cu_q, cu_k, len_k or lse misaligned");
-    if ((st = check_workspace(workspace, workspace_bytes, eqlin::attention_backward_workspace_bytes(p, a->dtype))) != EQLIN_OK) return st;
-    // dq, dk and dv may be interleaved parts of one tensor (the gradient of a qkv layer's output), so only an
-    // output over an input is refused
-    for (const auto &x : t)
-        for (const auto &y : t)
-            if (x.out && !y.out &&
-                overlap(x.t, extent(x.ts, x.hs, x.tokens, x.heads, p.D, a->dtype), y.t, extent(y.ts, y.hs, y.tokens, y.heads, p.D, a->dtype)))
-                return api_fail(EQLIN_ERR_INVALID_ARG, "%s overlaps %s", x.name, y.name);
+    const size_t need = eqlin::attention_backward_workspace_bytes(p, a->dtype), cu = ((size_t)a->batch + 1) * 4;
+    if ((st = check_workspace(workspace, workspace_bytes, need)) != EQLIN_OK) return st;
+    const Span ws[] = {{workspace, need, "workspace"}};
+    const Span more[] = {{a->lse, (size_t)a->total_q * p.Hq * 4, "lse"}, {a->cu_q, cu, "cu_q"}, {a->cu_k, cu, "cu_k"}, {a->len_k, cu - 4, "len_k"}};
+    if ((st = check_apart(ws, more)) != EQLIN_OK) return st;
+    // dq, dk and dv may be interleaved parts of one tensor (the gradient of a qkv layer's output): of two outputs only
+    // shared elements are refused, which strides that differ do not tell in general
+    for (const auto &x : t) {
+        const Span sx[] = {{x.t, extent(x.ts, x.hs, x.tokens, x.heads, p.D, a->dtype), x.name}};
+        if ((st = check_apart(ws, sx)) != EQLIN_OK) return st;
+        if (!x.out) continue;
+        if ((st = check_apart(sx, more)) != EQLIN_OK) return st;
+        for (const auto &y : t) {
+            const Span sy[] = {{y.t, extent(y.ts, y.hs, y.tokens, y.heads, p.D, a->dtype), y.name}};
+            if (!y.out) {
+                if ((st = check_apart(sx, sy)) != EQLIN_OK) return st;
+            } else if (&x < &y && overlap(x.t, sx[0].bytes, y.t, sy[0].bytes)) {
+                const int64_t by = ((const char *)y.t - (const char *)x.t) / (int64_t)elem_bytes(a->dtype);
+                if (by == 0 || (x.ts == y.ts && x.hs == y.hs && heads_meet(x.ts, x.hs, p.D, x.tokens, x.heads, y.tokens, y.heads, by, false)))
+                    return api_fail(EQLIN_ERR_INVALID_ARG, "%s and %s share memory", x.name, y.name);
+            }
+        }
+    }
     p.dout = g->d_o, p.dot = g->do_token_stride, p.doh = g->do_head_stride;
     p.dq = g->dq, p.dqt = g->dq_token_stride, p.dqh = g->dq_head_stride;
     p.dk = g->dk, p.dkt = g->dk_token_stride, p.dkh = g->dk_head_stride;

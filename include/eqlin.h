@@ -327,6 +327,7 @@ eqlin_status_t eqlin_rmsnorm_quant(const void *x, const void *residual, const vo
  *   dx         device [N][C][G] of dtype: the gradient of x and of the residual;  dgamma device float [C] or NULL
  *              (overwritten; zeros for N == 0).
  *   workspace  eqlin_rmsnorm_backward_workspace(N, C, G) bytes, 256-byte aligned (may be NULL without dgamma).
+ * dx, dgamma and the workspace overlap neither the inputs nor each other.
  */
 size_t eqlin_rmsnorm_backward_workspace(int64_t N, int C, int G);
 eqlin_status_t eqlin_rmsnorm_backward(const void *sum, const void *gamma, const float *rstd, const void *dy,
@@ -375,7 +376,8 @@ eqlin_status_t eqlin_rotary(const void *x, int64_t x_token_stride, int64_t x_hea
  *   q, k, v, o   tensor[token][head][dim] of dtype with token and head strides in ELEMENTS; pointers 16-byte
  *                aligned, strides a multiple of 16 bytes (else INVALID_ARG); dim a multiple of 8 (fp32: of 4)
  *                up to 128 (else UNSUPPORTED). Token strides up to 2^23 elements, head stride times heads up to
- *                2^28 (else UNSUPPORTED). o overlaps no input.
+ *                2^28 (else UNSUPPORTED). o, lse and the workspace overlap neither an input (cu_q, cu_k, len_k
+ *                included) nor each other, and no two heads of o share elements.
  *   cu_q, cu_k   device int32 [batch + 1], not decreasing: sequence i has the tokens from cu[i] to cu[i + 1]. Rows
  *                outside every sequence (in front of cu[0], from cu[batch] on: tensors of a fixed capacity) are
  *                neither read for a result nor written, here and in the gradients.
@@ -411,7 +413,10 @@ eqlin_status_t eqlin_attention(const eqlin_attention_args *a, void *workspace, s
  * eqlin_attention_backward -- dq, dk, dv from d_o (the gradient of o; lse's is zero). a: the forward's
  * arguments, with its o and lse. d_o, dq, dk, dv: as q, o, k, v, with strides; outputs are overwritten (keys
  * beyond len_k get zeros). Probabilities and score gradients are rounded to the half type for their products, in
- * fp16 scaled by powers of two so that neither end of the type's range is met; everything else is fp32. workspace: eqlin_attention_backward_workspace(a) bytes, 256-byte aligned.
+ * fp16 scaled by powers of two so that neither end of the type's range is met; everything else is fp32.
+ * dq, dk and dv may be interleaved parts of one tensor, but share no elements (checked where their strides are alike)
+ * and overlap no input.
+ *   workspace  eqlin_attention_backward_workspace(a) bytes, 256-byte aligned, apart from every tensor.
  */
 typedef struct eqlin_attention_grads {
     const void *d_o;
