@@ -88,6 +88,9 @@ eqlin_status_t rmsnorm(const void *x, const void *residual, const void *gamma, v
     return done(eqlin::launch_rmsnorm(p, dtype, (hipStream_t)stream), what);
 }
 
+// a stride over n tokens or heads: of one it means nothing, whatever it is
+int64_t stride_of(int64_t stride, int64_t n) { return n > 1 ? stride : 0; }
+
 // arguments shared by the attention's entry points -> the kernels' parameters
 eqlin_status_t check_attention(const eqlin_attention_args *a, eqlin::AttnParams *p) {
     if (!a) return api_fail(EQLIN_ERR_INVALID_ARG, "null arguments");
@@ -106,8 +109,10 @@ eqlin_status_t check_attention(const eqlin_attention_args *a, eqlin::AttnParams 
         return api_fail(EQLIN_ERR_UNSUPPORTED, "total_q * heads_q or total_k * heads_kv beyond 2^29, or batch * heads_kv beyond 2^21");
     *p = eqlin::AttnParams{};
     p->q = a->q, p->k = a->k, p->v = a->v, p->o = a->o, p->lse = a->lse;
-    p->qt = a->q_token_stride, p->qh = a->q_head_stride, p->kt = a->k_token_stride, p->kh = a->k_head_stride;
-    p->vt = a->v_token_stride, p->vh = a->v_head_stride, p->ot = a->o_token_stride, p->oh = a->o_head_stride;
+    p->qt = stride_of(a->q_token_stride, a->total_q), p->qh = stride_of(a->q_head_stride, a->heads_q);
+    p->kt = stride_of(a->k_token_stride, a->total_k), p->kh = stride_of(a->k_head_stride, a->heads_kv);
+    p->vt = stride_of(a->v_token_stride, a->total_k), p->vh = stride_of(a->v_head_stride, a->heads_kv);
+    p->ot = stride_of(a->o_token_stride, a->total_q), p->oh = stride_of(a->o_head_stride, a->heads_q);
     p->cu_q = a->cu_q, p->cu_k = a->cu_k, p->len_k = a->len_k;
     p->total_q = a->total_q, p->total_k = a->total_k;
     p->B = a->batch, p->Hq = a->heads_q, p->Hkv = a->heads_kv, p->grp = a->heads_q / a->heads_kv, p->D = a->dim;
@@ -240,6 +245,8 @@ eqlin_status_t eqlin_rotary(const void *x, int64_t x_token_stride, int64_t x_hea
     const size_t eb = elem_bytes(dtype);
     if (!aligned(x, eb) || !aligned(y, eb) || !aligned(pos, 4)) return api_fail(EQLIN_ERR_INVALID_ARG, "x, y or pos misaligned");
     const int64_t D = (int64_t)dc * G, smost = INT64_C(1) << 26;
+    x_token_stride = stride_of(x_token_stride, N), y_token_stride = stride_of(y_token_stride, N);
+    x_head_stride = stride_of(x_head_stride, H), y_head_stride = stride_of(y_head_stride, H);
     if (x_token_stride < 0 || x_head_stride < 0 || y_token_stride < 0 || y_head_stride < 0 || x_token_stride > smost ||
         x_head_stride > smost || y_token_stride > smost || y_head_stride > smost)
         return api_fail(EQLIN_ERR_INVALID_ARG, "strides out of range");
@@ -310,6 +317,10 @@ eqlin_status_t eqlin_attention_backward(const eqlin_attention_args *a, const eql
     if (st != EQLIN_OK) return st;
     if (!g) return api_fail(EQLIN_ERR_INVALID_ARG, "null gradients");
     if (a->batch == 0 || (a->total_q == 0 && a->total_k == 0)) return EQLIN_OK;
+    p.dot = stride_of(g->do_token_stride, a->total_q), p.doh = stride_of(g->do_head_stride, p.Hq);
+    p.dqt = stride_of(g->dq_token_stride, a->total_q), p.dqh = stride_of(g->dq_head_stride, p.Hq);
+    p.dkt = stride_of(g->dk_token_stride, a->total_k), p.dkh = stride_of(g->dk_head_stride, p.Hkv);
+    p.dvt = stride_of(g->dv_token_stride, a->total_k), p.dvh = stride_of(g->dv_head_stride, p.Hkv);
     struct {
         const void *t;
         int64_t ts, hs, tokens;
@@ -320,10 +331,10 @@ eqlin_status_t eqlin_attention_backward(const eqlin_attention_args *a, const eql
              {a->k, p.kt, p.kh, a->total_k, p.Hkv, "k", false},
              {a->v, p.vt, p.vh, a->total_k, p.Hkv, "v", false},
              {a->o, p.ot, p.oh, a->total_q, p.Hq, "o", false},
-             {g->d_o, g->do_token_stride, g->do_head_stride, a->total_q, p.Hq, "d_o", false},
-             {g->dq, g->dq_token_stride, g->dq_head_stride, a->total_q, p.Hq, "dq", true},
-             {g->dk, g->dk_token_stride, g->dk_head_stride, a->total_k, p.Hkv, "dk", true},
-             {g->dv, g->dv_token_stride, g->dv_head_stride, a->total_k, p.Hkv, "dv", true}};
+             {g->d_o, p.dot, p.doh, a->total_q, p.Hq, "d_o", false},
+             {g->dq, p.dqt, p.dqh, a->total_q, p.Hq, "dq", true},
+             {g->dk, p.dkt, p.dkh, a->total_k, p.Hkv, "dk", true},
+             {g->dv, p.dvt, p.dvh, a->total_k, p.Hkv, "dv", true}};
     for (const auto &x : t) {
         if ((st = check_tensor(x.t, x.ts, x.hs, x.tokens, x.heads, a->dtype, x.name)) != EQLIN_OK) return st;
         if (x.out && folds(x.ts, x.hs, x.tokens, x.heads, p.D))
@@ -355,10 +366,7 @@ eqlin_status_t eqlin_attention_backward(const eqlin_attention_args *a, const eql
             }
         }
     }
-    p.dout = g->d_o, p.dot = g->do_token_stride, p.doh = g->do_head_stride;
-    p.dq = g->dq, p.dqt = g->dq_token_stride, p.dqh = g->dq_head_stride;
-    p.dk = g->dk, p.dkt = g->dk_token_stride, p.dkh = g->dk_head_stride;
-    p.dv = g->dv, p.dvt = g->dv_token_stride, p.dvh = g->dv_head_stride;
+    p.dout = g->d_o, p.dq = g->dq, p.dk = g->dk, p.dv = g->dv;
     p.ws = (float *)workspace;
     (void)hipGetLastError();
     return done(eqlin::launch_attention_backward(p, a->dtype, (hipStream_t)stream), "eqlin_attention_backward launch");

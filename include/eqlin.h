@@ -376,7 +376,7 @@ eqlin_status_t eqlin_rotary(const void *x, int64_t x_token_stride, int64_t x_hea
  *   q, k, v, o   tensor[token][head][dim] of dtype with token and head strides in ELEMENTS; pointers 16-byte
  *                aligned, strides a multiple of 16 bytes (else INVALID_ARG); dim a multiple of 8 (fp32: of 4)
  *                up to 128 (else UNSUPPORTED). Token strides up to 2^23 elements, head stride times heads up to
- *                2^28 (else UNSUPPORTED). o, lse and the workspace overlap neither an input (cu_q, cu_k, len_k
+ *                2^28 (else UNSUPPORTED); a stride over one token or one head may be anything. o, lse and the workspace overlap neither an input (cu_q, cu_k, len_k
  *                included) nor each other, and no two heads of o share elements.
  *   cu_q, cu_k   device int32 [batch + 1], not decreasing: sequence i has the tokens from cu[i] to cu[i + 1]. Rows
  *                outside every sequence (in front of cu[0], from cu[batch] on: tensors of a fixed capacity) are
