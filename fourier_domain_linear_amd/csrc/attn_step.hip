@@ -184,13 +184,14 @@ bool plan_step(AttnParams &p) {
     // 32768 keys and a prompt of 512, 32 heads on 8: 212 us, against 562 us by the tile kernel alone).
     const bool few = p.total_q * p.grp <= 32 * (int64_t)p.B;
     if (p.grp > 32 || p.total_k <= 256 * (int64_t)p.B || !(few || (p.B > 1 && 8 * p.total_q <= p.total_k))) return false;
-    p.tiled = p.total_q > p.B;
+    const bool several = p.total_q > p.B;  // some sequence has more than one token
+    p.tiled = several && p.total_q * p.grp > 32;  // (fewer rows in all: no sequence has more than the columns hold)
     // Sequences and heads enough to fill the card with a workgroup each are the tile kernel's alone (32 heads on 8; 256 x
     // 1024 keys: 204 us, against 288 us here; 63 steps over 8192 keys and a prompt of 400: 383 us, against 480 us), but
     // not single tokens over many keys, where chunks level out sequences of different lengths (64 of 200 to 8200 keys:
     // 224 us here, against 296 us; the price, 64 of 4096 each: 219 us, against 193 us).
     const int64_t own = (int64_t)p.B * p.Hkv;
-    if (own >= 2 * (int64_t)device_num_cus() && (p.tiled || p.total_k <= 2048 * (int64_t)p.B)) return false;
+    if (own >= 2 * (int64_t)device_num_cus() && (several || p.total_k <= 2048 * (int64_t)p.B)) return false;
     // Four waves a compute unit are resident at once (registers at 128 dims in a half type). Where a chunk a wave
     // keeps them all busy in one go, chunks have that length (8 sequences, 100000 keys in all, 2 heads: 35 us,
     // against 46 us in one and a half goes); with sequences and heads enough by themselves, a third of a
@@ -199,7 +200,7 @@ bool plan_step(AttnParams &p) {
     int64_t chunk = 2 * own < waves ? (p.total_k * p.Hkv + waves - own - 1) / (waves - own) : (p.total_k / p.B + 2) / 3;
     chunk = std::min<int64_t>(std::max<int64_t>((chunk + 31) / 32 * 32, 128), 1 << 20);
     p.chunk = (int)chunk;
-    p.rcap = p.tiled ? 32 : p.grp;
+    p.rcap = several ? 32 : p.grp;
     p.slots = p.total_k / chunk + p.B;
     return true;
 }
