@@ -46,9 +46,10 @@ __device__ __forceinline__ void fwd_block(FwdState<E, DP> &st, const uint4 *qf, 
         for (int v = 0; v < 16; ++v) mx = fmaxf(mx, s[kb][v]);
     mx = half_max(mx) * c;
     // The maximum is only raised when it grew by more than 8 (in log2 units): a stale one keeps every
-    // p <= 2^8, exact in the sums' fp32 and in range of fp16, and saves the pass over the accumulators.
+    // p <= 2^8, exact in the sums' fp32 and in range of fp16, and saves the pass over the accumulators. Each column's own
+    // scores decide, so that its bits depend neither on the columns beside it nor on keys that it does not see.
     if (__any(mx > st.m + 8.0f)) {
-        const float mn = fmaxf(st.m, mx);
+        const float mn = mx > st.m + 8.0f ? mx : st.m;
         const float a = st.m == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(st.m - mn);  // (nothing summed yet: 1)
         st.m = mn;
         st.l *= a;
