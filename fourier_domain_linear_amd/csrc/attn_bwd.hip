@@ -22,15 +22,16 @@ namespace {
 // ---- fp16: where P and dS lie in the type's range ----
 //
 // Over thousands of keys P falls below fp16's normal range (2^-14), dS follows d_o down to nothing, and with a large loss
-// scale it passes 65504. P <= 1 enters its product times 2^15. dS enters times a gain, a power of two of its own for each
-// column (the query of dQ, the key of dK): it starts so high that the first block with a gradient lowers it, to a largest
-// value of 2^8 to 2^9, and is lowered again, the sums so far with it, by a block that passes 2^15. Values down to 2^-23
-// of a column's largest so keep all their bits, and the stores divide by the gain. (bf16 has the range of fp32.) The price,
-// 4 x 4096 tokens, 16 heads, forward and gradients: 2855 us against 2821 us without it at 128 dims, 1415 against 1323 at 64.
+// scale it passes 65504. P enters its product times 2^8: with all its bits down to 2^-22, and in range where lse's rounding
+// leaves it above 1 (scores in the millions). dS enters times a gain, a power of two of its own for each column (the query
+// of dQ, the key of dK): it starts so high that the first block with a gradient lowers it, to a largest value of 2^8 to
+// 2^9, and is lowered again, the sums so far with it, by a block that passes 2^15. Values down to 2^-23 of a column's
+// largest so keep all their bits, and the stores divide by the gain. (bf16 has the range of fp32.) The price, 4 x 4096
+// tokens, 16 heads, forward and gradients: 2907 us against 2866 us without it at 128 dims, 1456 against 1362 at 64.
 template <class E>
 constexpr bool kHasGain = __is_same(E, F16);
 template <class E>
-constexpr float kPGain = kHasGain<E> ? 32768.0f : 1.0f;
+constexpr int kPGain = kHasGain<E> ? 8 : 0;  // (log2)
 constexpr float kTop = 32768.0f;
 constexpr int kAim = 9, kFirstGain = 60;  // (log2; the largest dS of fp16 operands is about 2^40)
 
@@ -391,7 +392,7 @@ __global__ void __launch_bounds__(256, __is_same(E, F32) || DP > 64 ? 1 : 2) k_a
     TileDma<E, DP, C::BR> tq, tg;
     const uint32_t lds0 = lds_offset(lds);
     const typename TL::Lane L = TL::lane_of(lane);
-    float st_lse = INFINITY, st_del = 0.0f, gain = kHasGain<E> ? ldexpf(1.0f, kFirstGain) / kPGain<E> : 1.0f;
+    float st_lse = INFINITY, st_del = 0.0f, gain = kHasGain<E> ? ldexpf(1.0f, kFirstGain - kPGain<E>) : 1.0f;
     int st_last = -1;
     // Row offsets within a tile repeat from tile to tile where the group divides the tile.
     const bool repeats = C::BR % p.grp == 0;
@@ -408,7 +409,7 @@ __global__ void __launch_bounds__(256, __is_same(E, F32) || DP > 64 ? 1 : 2) k_a
             const uint32_t r = (uint32_t)(rem + tid);
             const int tok = tok0 + (int)(r / (uint32_t)p.grp), hh = (int)(r % (uint32_t)p.grp);
             const bool in = tid < valid;
-            st_lse = in ? lse[(int64_t)tok * p.Hq + hh] * kLog2e - (kHasGain<E> ? 15.0f : 0.0f) : INFINITY;
+            st_lse = in ? lse[(int64_t)tok * p.Hq + hh] * kLog2e - kPGain<E> : INFINITY;
             st_del = in ? del[(int64_t)tok * p.Hq + hh] : 0.0f;
             st_last = in ? (p.causal ? min(tok + off, sq.lk - 1) : sq.lk - 1) : -1;
         }
@@ -470,7 +471,7 @@ __global__ void __launch_bounds__(256, __is_same(E, F32) || DP > 64 ? 1 : 2) k_a
 #pragma unroll
         for (int db = 0; db < DP / 32; ++db) dk[db] = zero16(), dv[db] = zero16();
     }
-    const float dk_scale = kHasGain<E> ? p.scale / kPGain<E> / gain : p.scale, dv_scale = 1.0f / kPGain<E>;
+    const float dk_scale = kHasGain<E> ? ldexpf(p.scale, -kPGain<E>) / gain : p.scale, dv_scale = ldexpf(1.0f, -kPGain<E>);
     if (p.nsplit > 1) {  // a share: fp32, for k_attn_sum
         const int64_t heads = p.total_k * p.Hkv, at = (sq.k0 + key) * p.Hkv + hk;
         float *part = p.ws + share_offset(p);

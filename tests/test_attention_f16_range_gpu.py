@@ -88,3 +88,19 @@ def test_infinite_and_nan_rows_stay_where_they_are(cuda_device):
         assert torch.equal(dq[keep], clean[0][keep]) and not bool(dq[100].isfinite().any())
         for a, b in ((dk, clean[1]), (dv, clean[2])):
             assert torch.equal(a[101:], b[101:]) and not bool(a[:101].isfinite().any())
+
+
+@pytest.mark.parametrize("D", [32, 64, 128])
+def test_scores_in_the_millions(D, cuda_device):
+    """Scores up to 2^25 in log2 units, where fp32's step is 2: half a step in the score, in the maximum, in lse and in its way
+    back, and the constants' own roundings, leave exp(score - lse) of the one key that matters anywhere up to 2^5, above 1
+    and still far inside the type's range. Bar: every gradient is finite, and dv within that factor of the sum of |d_o|."""
+    q, k, v, do, cu, _ = _inputs([70], [70], 2, 1, D, "f32", cuda_device, seed=36)
+    q, k, v, do = (100 * q).half(), (100 * k).half(), v.half(), do.half()
+    scale = 600 * D ** -0.5
+    o, lse = eq.attention(q, k, v, cu, cu, scale=scale)
+    assert 1e7 < float(lse.abs().max()) < 2.3e7
+    dq, dk, dv = eq.attention_backward(do, q, k, v, o, lse, cu, cu, scale=scale)
+    torch.cuda.synchronize()
+    assert all(bool(t.isfinite().all()) for t in (o, lse, dv))
+    assert float(dv.float().abs().max()) <= 32 * float(do.float().abs().sum(dim=(0, 1)).max())
