@@ -53,7 +53,8 @@ __device__ __forceinline__ f32x16 zero16() {
 }
 
 // W (a 32x32 product's D layout, 16 values a lane) -> B-operand fragments of the next product: NF = 2
-// (half types, rounded to nearest even) or 4 (fp32, exact).
+// (half types, rounded to nearest even) or 4 (fp32, exact). The rounding is the price of the half types' products, seven
+// times as fast as fp32's: o's error against 64 bits is 1.35 times that of o's own rounding alone.
 template <class E>
 struct WFrags {
     static constexpr int NF = __is_same(E, F32) ? 4 : 2;

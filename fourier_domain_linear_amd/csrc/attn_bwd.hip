@@ -95,7 +95,8 @@ __device__ __forceinline__ void dq_block(f32x16 *dq, const uint4 *qf, const uint
 
 // delta of rows that see no key past the first tile: sum over its keys of P dP, in fp32 throughout. Over a handful of
 // keys (short sequences, a causal sequence's first rows) the sum of dO O carries o's rounding into the gradients about
-// as far as their own rounding; over more it is lost among the terms. A row that sees one key has P = 1 and so dS = 0,
+// as far as their own rounding; over more it is lost among the terms (unless the values share a part many times their spread:
+// it is u |o| |dO|, they are as dP - delta). A row that sees one key has P = 1 and so dS = 0,
 // exactly.
 template <class E, int DP, int NKB>
 __device__ __forceinline__ float delta_of_tile(const uint4 *qf, const uint4 *gf, const typename Tile<E, DP>::Lane &L, uint32_t kt,
@@ -242,7 +243,7 @@ __global__ void __launch_bounds__(256, __is_same(E, F32) ? 1 : 2) k_attn_dq(cons
 
 // ---- dK, dV: 32 keys a wave (columns), tiles of packed rows (q and dO) through LDS ----
 //
-// The keys' operands and dk and dv stay in a wave's registers: at 128 dims 384 of the 512, one wave a SIMD, whose
+// The keys' operands and dk and dv stay in a wave's registers: at 128 dims 192 of the 383 in use, one wave a SIMD, whose
 // exponentials wait for its products and its products for its reads: matrix cores 29 % busy, LDS 19 %, no bank conflicts.
 // (Two waves a SIMD, with the keys in LDS, read half as much again and take the same time: 2171 us for the backward
 // above, against 2196 us.) The sequences above: 550 us of 890, and 45 us for the sum of the shares.

@@ -4,8 +4,10 @@
 // Bound by the matrix cores at 128 dims, and by the vector work beside them below: a 32 x 32 block of scores costs
 // 16 products of 32 clocks at 128 dims and 8 at 64, and at both 16 exponentials of 16 clocks and about 100 other vector
 // instructions of 4. 4 x 4096 tokens, 16 heads, bf16, every key seen: 520 to 600 us at 128 dims (0.92 to 1.05 PFLOP/s, by the
-// card's clock; a large matrix product reaches 1.1), 306 to 335 us at 64 (0.82 to 0.90), 248 us at 32 (0.55). fp32, 4096
-// tokens, 8 heads of 128: 613 us, 112 TFLOP/s (a matrix product: 153).
+// card's clock; a large matrix product reaches 1.1), 306 to 335 us at 64 (0.82 to 0.90), 248 us at 32 (0.55). Sequences of
+// different lengths are started in their packing's order, backwards: 24 of 403 to 3136, 6 heads of 64, 157 us with the
+// longest packed last, 192 us with it first. fp32, 4096 tokens, 8 heads of 128: 607 us, 113 TFLOP/s (a matrix product: 153),
+// matrix cores 68 % busy at one workgroup a compute unit.
 #include "attn.h"
 #include "attn_fwd.h"
 

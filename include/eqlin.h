@@ -308,9 +308,9 @@ eqlin_status_t eqlin_rmsnorm(const void *x, const void *residual, const void *ga
                              int64_t N, int C, int G, float eps, eqlin_dtype_t dtype, eqlin_stream_t stream);
 
 /*
- * eqlin_rmsnorm_quant -- the same with an 8-bit output for a product in e4m3 (OCP: 4 exponent and 3 mantissa
- * bits, largest value 448): q = y / scale rounded to nearest even, with one scale a token, scale = max |y| / 448
- * (1 for a row of zeros; at least the smallest normal fp32 number), so y = q scale.
+ * eqlin_rmsnorm_quant -- the same with an 8-bit output for a product of the caller's in e4m3 (OCP: 4 exponent and 3
+ * mantissa bits, largest value 448; no layer of this library takes it): q = y / scale rounded to nearest even, with one
+ * scale a token, scale = max |y| / 448 (1 for a row of zeros; at least the smallest normal fp32 number), so y = q scale.
  *   q  device [N][C][G] bytes, 16-byte aligned;  scale  device float [N].  Otherwise as eqlin_rmsnorm.
  */
 eqlin_status_t eqlin_rmsnorm_quant(const void *x, const void *residual, const void *gamma, void *sum, uint8_t *q,
@@ -414,6 +414,8 @@ eqlin_status_t eqlin_attention(const eqlin_attention_args *a, void *workspace, s
  * arguments, with its o and lse. d_o, dq, dk, dv: as q, o, k, v, with strides; outputs are overwritten (keys
  * beyond len_k get zeros). Probabilities and score gradients are rounded to the half type for their products, in
  * fp16 scaled by powers of two so that neither end of the type's range is met; everything else is fp32.
+ * (dP - delta takes delta from o as stored where a row sees more than 64 keys: values whose common part is many times
+ * their spread bring o's rounding into dq and dk.)
  * dq, dk and dv may be interleaved parts of one tensor, but share no elements (checked where their strides are alike)
  * and overlap no input.
  *   workspace  eqlin_attention_backward_workspace(a) bytes, 256-byte aligned, apart from every tensor.
