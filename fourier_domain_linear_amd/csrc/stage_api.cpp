@@ -361,7 +361,9 @@ eqlin_status_t eqlin_attention_backward(const eqlin_attention_args *a, const eql
                 if ((st = check_apart(sx, sy)) != EQLIN_OK) return st;
             } else if (&x < &y && overlap(x.t, sx[0].bytes, y.t, sy[0].bytes)) {
                 const int64_t by = ((const char *)y.t - (const char *)x.t) / (int64_t)elem_bytes(a->dtype);
-                if (by == 0 || (x.ts == y.ts && x.hs == y.hs && heads_meet(x.ts, x.hs, p.D, x.tokens, x.heads, y.tokens, y.heads, by, false)))
+                const int64_t ts = x.tokens > 1 ? x.ts : y.ts, hs = x.heads > 1 ? x.hs : y.hs;
+                const bool alike = (y.tokens == 1 || ts == y.ts) && (y.heads == 1 || hs == y.hs);
+                if (by == 0 || (alike && heads_meet(ts, hs, p.D, x.tokens, x.heads, y.tokens, y.heads, by, false)))
                     return api_fail(EQLIN_ERR_INVALID_ARG, "%s and %s share memory", x.name, y.name);
             }
         }

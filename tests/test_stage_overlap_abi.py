@@ -112,6 +112,16 @@ def test_gradients_that_share_elements(lib):
     assert len(seen) == 2
 
 
+def test_gradients_of_one_head_or_token_that_share_elements(lib):
+    """A stride over one head or token means nothing, so the other tensor's decides."""
+    a = _args(heads_q=4, heads_kv=1)
+    g = _grads(dk=_at(8) + 2 * (64 + 8), dq_token_stride=512, dk_token_stride=512)  # dk in dq's second and third head
+    assert _message(lib, lib.eqlin_attention_backward(ctypes.byref(a), ctypes.byref(g), _at(11), 1 << 30, None)) == "dq and dk share memory"
+    a = _args(total_q=1)
+    g = _grads(dk=_at(8) + 2 * 64)  # dk's first heads in dq's only token
+    assert _message(lib, lib.eqlin_attention_backward(ctypes.byref(a), ctypes.byref(g), _at(11), 1 << 30, None)) == "dq and dk share memory"
+
+
 def test_norm_backward_memory_that_is_shared(lib):
     args = [_at(0), _at(1), _at(2), _at(3), _at(4), _at(5), _at(6)]  # sum, gamma, rstd, dy, dsum, dx, dgamma
     for i, name in enumerate(["sum", "gamma", "rstd", "dy", "dsum", "dx", "dgamma"]):
