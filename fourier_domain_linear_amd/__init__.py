@@ -20,6 +20,8 @@ The operators between the layers of a transformer stage (include/eqlin.h has the
     y, s, rstd = eq.rmsnorm(x, gamma, residual=r)              # x, r: [N, C, G]; gamma: [C]
     q, scale, s, rstd = eq.rmsnorm_quant(x, gamma, residual=r) # q: float8_e4m3fn, one scale a token
     dx, dgamma = eq.rmsnorm_backward(dy, s, gamma, rstd, ds=ds)
+    y, s, mean, rstd = eq.layernorm(x, gamma, beta, residual=r)
+    dx, dgamma, dbeta = eq.layernorm_backward(dy, s, gamma, mean, rstd, ds=ds)
     qk = eq.rotary(qk, pos, pairs=(4, 4))                      # qk: [N, H, dc, G]; pos: int32 [N, axes]
     o, lse = eq.attention(q, k, v, cu_q, cu_k, causal=False)   # q: [T, H, D] or [T, H, dc, G]
     dq, dk, dv = eq.attention_backward(do, q, k, v, o, lse, cu_q, cu_k, causal=False)
@@ -65,6 +67,7 @@ EXPORTED = (
     "eqlin_status_string", "eqlin_last_error", "eqlin_version",
     "eqlin_prepare_conv_weights", "eqlin_conv_forward", "eqlin_conv_forward_expanded",
     "eqlin_rmsnorm", "eqlin_rmsnorm_quant", "eqlin_rmsnorm_backward_workspace", "eqlin_rmsnorm_backward",
+    "eqlin_layernorm", "eqlin_layernorm_backward_workspace", "eqlin_layernorm_backward",
     "eqlin_rotary", "eqlin_attention_workspace", "eqlin_attention", "eqlin_attention_backward_workspace",
     "eqlin_attention_backward",
 )
@@ -145,16 +148,20 @@ def load_library() -> ctypes.CDLL:
     lib.eqlin_rmsnorm_quant.argtypes = [vp, vp, vp, vp, vp, vp, vp, i64, i32, i32, f32, i32, vp]
     lib.eqlin_rmsnorm_backward.argtypes = [vp, vp, vp, vp, vp, vp, vp, i64, i32, i32, i32, vp, szt, vp]
     lib.eqlin_rmsnorm_backward_workspace.argtypes = [i64, i32, i32]
+    lib.eqlin_layernorm.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, i64, i32, i32, f32, i32, vp]
+    lib.eqlin_layernorm_backward.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, i64, i32, i32, i32, vp, szt, vp]
+    lib.eqlin_layernorm_backward_workspace.argtypes = [i64, i32, i32]
     lib.eqlin_rotary.argtypes = [vp, i64, i64, vp, i64, i64, vp, i64, i32, i32, i32, i32, ctypes.POINTER(i32),
                                  ctypes.c_double, u32, i32, vp]
     lib.eqlin_attention_workspace.argtypes = [args]
     lib.eqlin_attention.argtypes = [args, vp, szt, vp]
     lib.eqlin_attention_backward_workspace.argtypes = [args]
     lib.eqlin_attention_backward.argtypes = [args, grads, vp, szt, vp]
-    for name in ("eqlin_rmsnorm", "eqlin_rmsnorm_quant", "eqlin_rmsnorm_backward", "eqlin_rotary", "eqlin_attention",
-                 "eqlin_attention_backward"):
+    for name in ("eqlin_rmsnorm", "eqlin_rmsnorm_quant", "eqlin_rmsnorm_backward", "eqlin_layernorm",
+                 "eqlin_layernorm_backward", "eqlin_rotary", "eqlin_attention", "eqlin_attention_backward"):
         getattr(lib, name).restype = i32
-    for name in ("eqlin_rmsnorm_backward_workspace", "eqlin_attention_workspace", "eqlin_attention_backward_workspace"):
+    for name in ("eqlin_rmsnorm_backward_workspace", "eqlin_layernorm_backward_workspace", "eqlin_attention_workspace",
+                 "eqlin_attention_backward_workspace"):
         getattr(lib, name).restype = szt
     _lib = lib
     return lib
@@ -540,6 +547,54 @@ def rmsnorm_backward(dy: torch.Tensor, s: torch.Tensor, gamma: torch.Tensor | No
              _ptr(ds), dx.data_ptr(), _ptr(dgamma), N, C, G, code, _ptr(workspace), need)
     _check(st, "eqlin_rmsnorm_backward")
     return dx, dgamma
+
+
+def layernorm(x: torch.Tensor, gamma: torch.Tensor | None = None, beta: torch.Tensor | None = None,
+              residual: torch.Tensor | None = None, eps: float = 1e-5, y: torch.Tensor | None = None):
+    """eqlin_layernorm -> (y, s, mean, rstd): s = x + residual (x itself without one), mean and rstd [N] float32 over a
+    token's C * G values, y = (s - mean) rstd gamma[c] + beta[c]. x: [N, C, G]; gamma, beta: [C] of x's dtype or None."""
+    code = _norm_args(x, gamma, residual)
+    N, C, G = x.shape
+    if beta is not None:
+        _same(beta, x, "beta", (C,))
+    if y is None:
+        y = torch.empty_like(x)
+    else:
+        _same(y, x, "y")
+    s = x if residual is None else torch.empty_like(x)
+    mean, rstd = x.new_empty((2, N), dtype=torch.float32).unbind()
+    st = _on(x.get_device(), load_library().eqlin_layernorm, x.data_ptr(), _ptr(residual), _ptr(gamma), _ptr(beta),
+             None if residual is None else s.data_ptr(), y.data_ptr(), mean.data_ptr(), rstd.data_ptr(), N, C, G, eps, code)
+    _check(st, "eqlin_layernorm")
+    return y, s, mean, rstd
+
+
+def layernorm_backward_workspace(N: int, C: int, G: int) -> int:
+    """Bytes of device scratch eqlin_layernorm_backward needs (0 without dgamma and dbeta)."""
+    return int(load_library().eqlin_layernorm_backward_workspace(int(N), int(C), int(G)))
+
+
+def layernorm_backward(dy: torch.Tensor, s: torch.Tensor, gamma: torch.Tensor | None, mean: torch.Tensor, rstd: torch.Tensor,
+                       ds: torch.Tensor | None = None, with_params: bool = True, workspace: torch.Tensor | None = None):
+    """eqlin_layernorm_backward -> (dx, dgamma, dbeta): dx [N, C, G], the gradient of x and of the residual (ds: the
+    gradient that reaches s directly), and dgamma, dbeta [C] float32 (None with with_params=False). s, mean, rstd:
+    layernorm's."""
+    code = _norm_args(s, gamma, None)
+    _same(dy, s, "dy")
+    if ds is not None:
+        _same(ds, s, "ds")
+    N, C, G = s.shape
+    _f32_out(mean, (N,), s.device, "mean")
+    _f32_out(rstd, (N,), s.device, "rstd")
+    dx = torch.empty_like(s)
+    dgamma, dbeta = s.new_empty((2, C), dtype=torch.float32).unbind() if with_params else (None, None)
+    need = layernorm_backward_workspace(N, C, G) if with_params else 0
+    workspace = _workspace(workspace, need, s.device)
+    st = _on(s.get_device(), load_library().eqlin_layernorm_backward, s.data_ptr(), _ptr(gamma), mean.data_ptr(),
+             rstd.data_ptr(), dy.data_ptr(), _ptr(ds), dx.data_ptr(), _ptr(dgamma), _ptr(dbeta), N, C, G, code,
+             _ptr(workspace), need)
+    _check(st, "eqlin_layernorm_backward")
+    return dx, dgamma, dbeta
 
 
 def _workspace(workspace: torch.Tensor | None, need: int, device):

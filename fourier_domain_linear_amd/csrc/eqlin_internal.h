@@ -170,6 +170,28 @@ struct NormGradParams {
 size_t rmsnorm_backward_workspace_bytes(int64_t N, int C, int G);
 hipError_t launch_rmsnorm_backward(const NormGradParams &p, eqlin_dtype_t dtype, hipStream_t s);
 
+// ---- layernorm.hip ----
+// The layer norm over rows of C * G values; r, gamma, beta, sum, mean, rstd may be null.
+struct LayerNormParams {
+    const void *x, *r, *gamma, *beta;
+    void *sum, *y;
+    float *mean, *rstd;
+    int64_t N;
+    int C, lg;  // G = 1 << lg
+    float eps;
+};
+hipError_t launch_layernorm(const LayerNormParams &p, eqlin_dtype_t dtype, hipStream_t s);
+struct LayerNormGradParams {
+    const void *s, *gamma, *dy, *ds;
+    const float *mean, *rstd;
+    void *dx;
+    float *dgamma, *dbeta, *part;  // part: partial rows of both, or null where neither is wanted
+    int64_t N;
+    int C, lg;
+};
+size_t layernorm_backward_workspace_bytes(int64_t N, int C, int G);
+hipError_t launch_layernorm_backward(const LayerNormGradParams &p, eqlin_dtype_t dtype, hipStream_t s);
+
 // ---- rotary.hip ----
 constexpr int kRotaryMaxPairs = 256, kRotaryMaxAxes = 4;
 struct RotaryParams {

@@ -11,7 +11,7 @@
 // which reads the row a second time. bf16, 25088 tokens of 96 x 4 with the residual: 14.4 us (77 MB, 5.3 TB/s; a large
 // copy reaches 5.1 from memory, and part of this stays in the last cache); fp16 to 8 bits, 12544 tokens of 256 x 8: 37.8 us
 // (180 MB, 4.8 TB/s). The element loop: 25088 tokens of 97 x 2, 23 us (39 MB, 1.7 TB/s).
-#include "stage.h"
+#include "norm_rows.h"
 
 namespace eqlin {
 
@@ -33,36 +33,6 @@ struct Divisor {
     __device__ __forceinline__ float quotient(float y) const {
         const float t = y * inv;
         return fmaf(fmaf(t, neg, y), inv, t);
-    }
-};
-
-// Sum over the lanes that share a row: a wave, or the whole workgroup (through LDS).
-template <int WAVES>
-struct RowGroup {
-    float *red;
-    __device__ __forceinline__ float sum(float x) {
-        x = wave_sum(x);
-        if constexpr (WAVES > 1) {
-            __syncthreads();
-            if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = x;
-            __syncthreads();
-            x = 0.0f;
-#pragma unroll
-            for (int w = 0; w < WAVES; ++w) x += red[w];
-        }
-        return x;
-    }
-    __device__ __forceinline__ float max(float x) {
-        x = wave_max(x);
-        if constexpr (WAVES > 1) {
-            __syncthreads();
-            if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = x;
-            __syncthreads();
-            x = 0.0f;
-#pragma unroll
-            for (int w = 0; w < WAVES; ++w) x = fmaxf(x, red[w]);
-        }
-        return x;
     }
 };
 
@@ -356,11 +326,6 @@ __global__ void __launch_bounds__(1024) k_norm_dgamma(const float *part, int row
 __global__ void k_zero(float *p, int n) {
     const int i = blockIdx.x * 256 + threadIdx.x;
     if (i < n) p[i] = 0.0f;
-}
-
-unsigned grid_for(int64_t rows, int rows_per_wg, int per_cu) {
-    const int64_t need = (rows + rows_per_wg - 1) / rows_per_wg, most = (int64_t)device_num_cus() * per_cu;
-    return (unsigned)std::max<int64_t>(1, std::min(need, most));
 }
 
 constexpr int kBwdPerCu = 4;  // workgroups of the gradient a compute unit: also bounds the partial rows

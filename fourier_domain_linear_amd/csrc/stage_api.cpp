@@ -1,4 +1,4 @@
-// stage_api.cpp -- the C entry points of the operators between the layers (norm, rotary positions,
+// stage_api.cpp -- the C entry points of the operators between the layers (norms, rotary positions,
 // attention): argument checks and dispatch. Nothing here computes; every step runs in the HIP kernels.
 #include <hip/hip_runtime.h>
 #include <math.h>
@@ -65,13 +65,17 @@ eqlin_status_t check_norm(int64_t N, int C, int G, eqlin_dtype_t dtype) {
     return EQLIN_OK;
 }
 
+eqlin_status_t check_eps(float eps) {
+    return !(eps >= 0.0f) || isinf(eps) ? api_fail(EQLIN_ERR_INVALID_ARG, "eps must be finite and >= 0") : EQLIN_OK;
+}
+
 eqlin_status_t rmsnorm(const void *x, const void *residual, const void *gamma, void *sum, void *y, uint8_t *q,
                        float *scale, float *rstd, int64_t N, int C, int G, float eps, eqlin_dtype_t dtype,
                        eqlin_stream_t stream, bool quant, const char *what) {
     eqlin::api_clear();
     eqlin_status_t st = check_norm(N, C, G, dtype);
     if (st != EQLIN_OK) return st;
-    if (!(eps >= 0.0f) || isinf(eps)) return api_fail(EQLIN_ERR_INVALID_ARG, "eps must be finite and >= 0");
+    if ((st = check_eps(eps)) != EQLIN_OK) return st;
     if (N == 0) return EQLIN_OK;
     const void *out = quant ? (const void *)q : y;
     if (!x || !out || (quant && !scale)) return api_fail(EQLIN_ERR_INVALID_ARG, "null x or output");
@@ -213,6 +217,59 @@ eqlin_status_t eqlin_rmsnorm_backward(const void *sum, const void *gamma, const 
     eqlin::NormGradParams p = {sum, gamma, dy, dsum, rstd, dx, dgamma, (float *)workspace, N, C, ilog2(G)};
     (void)hipGetLastError();
     return done(eqlin::launch_rmsnorm_backward(p, dtype, (hipStream_t)stream), "eqlin_rmsnorm_backward launch");
+}
+
+eqlin_status_t eqlin_layernorm(const void *x, const void *residual, const void *gamma, const void *beta, void *sum, void *y,
+                               float *mean, float *rstd, int64_t N, int C, int G, float eps, eqlin_dtype_t dtype,
+                               eqlin_stream_t stream) {
+    eqlin::api_clear();
+    eqlin_status_t st = check_norm(N, C, G, dtype);
+    if (st != EQLIN_OK) return st;
+    if ((st = check_eps(eps)) != EQLIN_OK) return st;
+    if (N == 0) return EQLIN_OK;
+    if (!x || !y) return api_fail(EQLIN_ERR_INVALID_ARG, "null x or y");
+    const size_t eb = elem_bytes(dtype), n = (size_t)N * C * G * eb, c = (size_t)C * eb, rows = (size_t)N * 4;
+    if (!aligned(x, 16) || !aligned(residual, 16) || !aligned(sum, 16) || !aligned(y, 16))
+        return api_fail(EQLIN_ERR_INVALID_ARG, "x, residual, sum and y must be 16-byte aligned");
+    if (!aligned(gamma, eb) || !aligned(beta, eb) || !aligned(mean, 4) || !aligned(rstd, 4))
+        return api_fail(EQLIN_ERR_INVALID_ARG, "gamma, beta, mean or rstd misaligned");
+    const Span ins[] = {{x, n, "x"}, {residual, n, "residual"}, {gamma, c, "gamma"}, {beta, c, "beta"}};
+    const Span outs[] = {{sum, n, "sum"}, {y, n, "y"}, {mean, rows, "mean"}, {rstd, rows, "rstd"}};
+    if ((st = check_apart(outs, ins)) != EQLIN_OK) return st;
+    eqlin::LayerNormParams p = {x, residual, gamma, beta, sum, y, mean, rstd, N, C, ilog2(G), eps};
+    (void)hipGetLastError();
+    return done(eqlin::launch_layernorm(p, dtype, (hipStream_t)stream), "eqlin_layernorm launch");
+}
+
+size_t eqlin_layernorm_backward_workspace(int64_t N, int C, int G) {
+    return N <= 0 || C < 1 ? 0 : eqlin::layernorm_backward_workspace_bytes(N, C, G);
+}
+
+eqlin_status_t eqlin_layernorm_backward(const void *sum, const void *gamma, const float *mean, const float *rstd,
+                                        const void *dy, const void *dsum, void *dx, float *dgamma, float *dbeta, int64_t N,
+                                        int C, int G, eqlin_dtype_t dtype, void *workspace, size_t workspace_bytes,
+                                        eqlin_stream_t stream) {
+    eqlin::api_clear();
+    eqlin_status_t st = check_norm(N, C, G, dtype);
+    if (st != EQLIN_OK) return st;
+    if (!aligned(dgamma, 4) || !aligned(dbeta, 4)) return api_fail(EQLIN_ERR_INVALID_ARG, "dgamma or dbeta misaligned");
+    const bool params = dgamma || dbeta;
+    if (N == 0 && !params) return EQLIN_OK;
+    const size_t eb = elem_bytes(dtype), n = (size_t)N * C * G * eb, c = (size_t)C * 4, rows = (size_t)N * 4;
+    const size_t need = params && N > 0 ? eqlin::layernorm_backward_workspace_bytes(N, C, G) : 0;
+    if (N > 0) {
+        if (!sum || !mean || !rstd || !dy || !dx) return api_fail(EQLIN_ERR_INVALID_ARG, "null sum, mean, rstd, dy or dx");
+        if (!aligned(sum, 16) || !aligned(dy, 16) || !aligned(dsum, 16) || !aligned(dx, 16))
+            return api_fail(EQLIN_ERR_INVALID_ARG, "sum, dy, dsum and dx must be 16-byte aligned");
+        if (!aligned(gamma, eb) || !aligned(mean, 4) || !aligned(rstd, 4)) return api_fail(EQLIN_ERR_INVALID_ARG, "gamma, mean or rstd misaligned");
+        if ((st = check_workspace(workspace, workspace_bytes, need)) != EQLIN_OK) return st;
+    }
+    const Span ins[] = {{sum, n, "sum"}, {dy, n, "dy"}, {dsum, n, "dsum"}, {gamma, (size_t)C * eb, "gamma"}, {mean, rows, "mean"}, {rstd, rows, "rstd"}};
+    const Span outs[] = {{dx, n, "dx"}, {dgamma, c, "dgamma"}, {dbeta, c, "dbeta"}, {workspace, need, "workspace"}};
+    if ((st = check_apart(outs, ins)) != EQLIN_OK) return st;
+    eqlin::LayerNormGradParams p = {sum, gamma, dy, dsum, mean, rstd, dx, dgamma, dbeta, params ? (float *)workspace : nullptr, N, C, ilog2(G)};
+    (void)hipGetLastError();
+    return done(eqlin::launch_layernorm_backward(p, dtype, (hipStream_t)stream), "eqlin_layernorm_backward launch");
 }
 
 eqlin_status_t eqlin_rotary(const void *x, int64_t x_token_stride, int64_t x_head_stride, void *y,

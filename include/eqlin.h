@@ -336,6 +336,45 @@ eqlin_status_t eqlin_rmsnorm_backward(const void *sum, const void *gamma, const 
                                       eqlin_stream_t stream);
 
 /*
+ * eqlin_layernorm -- layer norm of each token over its C x G values, with the residual's addition:
+ *
+ *     s = x + residual;   mean = mean over (c, g) of s;   rstd = (mean over (c, g) of (s - mean)^2 + eps)^(-1/2)
+ *     y[n, c, g] = (s[n, c, g] - mean[n]) rstd[n] gamma[c] + beta[c]
+ *
+ * Mean and variance run over the group axis too and gamma and beta have one value a channel, so a shift of the group
+ * axis passes through. fp32 throughout, the variance taken about the mean; y is taken from the unrounded sum; s and y are
+ * each rounded once.
+ *   x, residual  device [N][C][G] of dtype (EQLIN_F32, EQLIN_BF16 or EQLIN_F16); residual may be NULL (s = x).
+ *   gamma, beta  device [C] of dtype, or NULL (ones; zeros).
+ *   sum          device [N][C][G], receives s, or NULL;  y device [N][C][G];  mean, rstd device float [N] or NULL.
+ *   N >= 0 (0 enqueues nothing); C >= 1; G in {1, 2, 4, 8}; C * G <= 2^20 (else UNSUPPORTED); eps >= 0, finite.
+ * x, residual, sum and y must be 16-byte aligned; outputs overlap neither the inputs nor each other.
+ * Rows that are no whole number of 16-byte vectors run slower; so do those longer than 16384 values (fp32: 8192; rows of
+ * odd length: 2048, even ones of a half type: 4096), which are read three times.
+ */
+eqlin_status_t eqlin_layernorm(const void *x, const void *residual, const void *gamma, const void *beta, void *sum, void *y,
+                               float *mean, float *rstd, int64_t N, int C, int G, float eps, eqlin_dtype_t dtype,
+                               eqlin_stream_t stream);
+
+/*
+ * eqlin_layernorm_backward -- with xh = (s - mean) rstd and w = dy gamma:
+ *
+ *     dx = dsum + rstd (w - mean(w) - xh mean(w xh));     dgamma[c] = sum over n, g of dy xh;     dbeta[c] = sum over n, g of dy
+ *
+ *   sum, mean, rstd  the forward's;  dy device [N][C][G];  dsum device [N][C][G], the gradient that reaches s from the
+ *              residual stream, or NULL.
+ *   dx         device [N][C][G] of dtype: the gradient of x and of the residual;  dgamma, dbeta device float [C] or NULL
+ *              each (overwritten; zeros for N == 0).
+ *   workspace  eqlin_layernorm_backward_workspace(N, C, G) bytes, 256-byte aligned (may be NULL without dgamma and dbeta).
+ * dx, dgamma, dbeta and the workspace overlap neither the inputs nor each other.
+ */
+size_t eqlin_layernorm_backward_workspace(int64_t N, int C, int G);
+eqlin_status_t eqlin_layernorm_backward(const void *sum, const void *gamma, const float *mean, const float *rstd,
+                                        const void *dy, const void *dsum, void *dx, float *dgamma, float *dbeta, int64_t N,
+                                        int C, int G, eqlin_dtype_t dtype, void *workspace, size_t workspace_bytes,
+                                        eqlin_stream_t stream);
+
+/*
  * eqlin_rotary -- rotary positions over 1 to 4 axes (the last two: row, column) on heads of dc channels x G:
  *
  *     (a, b) = (x[n, h, j, g], x[n, h, j + P, g]) -> (a cos t - b sin t, a sin t + b cos t),  j < P

@@ -1,5 +1,6 @@
-"""fp64 CPU oracle of the operators between the layers of a transformer stage: root-mean-square norm with the
-residual's addition, rotary positions over several axes, attention over packed sequences, and their gradients.
+"""fp64 CPU oracle of the operators between the layers of a transformer or recurrent stage: root-mean-square and layer norm
+with the residual's addition, rotary positions over several axes, attention and the gated recurrence over packed sequences,
+and their gradients.
 
 TEST INFRASTRUCTURE ONLY, written from the formulas in plain numpy loops over tokens' sequences and heads; it
 shares no code with the GPU path. Pinned in ``tests/test_oracle_stage.py`` against central differences,
@@ -49,6 +50,75 @@ def rmsnorm_backward(dy, s, gamma, rstd, ds=None):
     w = dy * g[None, :, None]
     dx = rstd[:, None, None] * (w - xh * (w * xh).mean(axis=(1, 2))[:, None, None])
     return dx + (0 if ds is None else np.asarray(ds, np.float64)), (dy * xh).sum(axis=(0, 2))
+
+
+def layernorm(x, gamma=None, beta=None, residual=None, eps=1e-5):
+    """(y, s, mean, rstd) of x [N, C, G]."""
+    s = np.asarray(x, np.float64) + (0 if residual is None else np.asarray(residual, np.float64))
+    mean = s.mean(axis=(1, 2))
+    d = s - mean[:, None, None]
+    rstd = 1 / np.sqrt((d ** 2).mean(axis=(1, 2)) + eps)
+    g = np.ones(s.shape[1]) if gamma is None else np.asarray(gamma, np.float64)
+    b = np.zeros(s.shape[1]) if beta is None else np.asarray(beta, np.float64)
+    return d * rstd[:, None, None] * g[None, :, None] + b[None, :, None], s, mean, rstd
+
+
+def layernorm_backward(dy, s, gamma, mean, rstd, ds=None):
+    """(dx, dgamma, dbeta) with s, mean and rstd as given."""
+    dy, s, mean, rstd = (np.asarray(t, np.float64) for t in (dy, s, mean, rstd))
+    g = np.ones(s.shape[1]) if gamma is None else np.asarray(gamma, np.float64)
+    xh = (s - mean[:, None, None]) * rstd[:, None, None]
+    w = dy * g[None, :, None]
+    dx = rstd[:, None, None] * (w - w.mean(axis=(1, 2))[:, None, None] - xh * (w * xh).mean(axis=(1, 2))[:, None, None])
+    return dx + (0 if ds is None else np.asarray(ds, np.float64)), (dy * xh).sum(axis=(0, 2)), dy.sum(axis=(0, 2))
+
+
+def _runs(cu, reverse):
+    """The tokens of each sequence in the recurrence's order."""
+    for i in range(len(cu) - 1):
+        t = list(range(cu[i], cu[i + 1]))
+        yield t[::-1] if reverse else t
+
+
+def recurrence(x, forget, cu, gate=None, state=None, reverse=False):
+    """(y, final, h) of h_t = f h_{t-1} + (1 - f) x_t, f = sigmoid(forget), y = h or h silu(gate). x [T, C, G]; rows outside
+    every sequence are NaN in y and h."""
+    x, z = np.asarray(x, np.float64), np.asarray(forget, np.float64)
+    h = np.full(x.shape, np.nan)
+    final = np.zeros((len(cu) - 1,) + x.shape[1:]) if state is None else np.array(state, np.float64)
+    for i, run in enumerate(_runs(cu, reverse)):
+        for t in run:
+            f = 1 / (1 + np.exp(-z[t]))
+            final[i] = f * final[i] + x[t] / (1 + np.exp(z[t]))
+            h[t] = final[i]
+    if gate is None:
+        return h, final, h
+    o = np.asarray(gate, np.float64)
+    return h * o / (1 + np.exp(-o)), final, h
+
+
+def recurrence_backward(dy, x, forget, cu, gate=None, state=None, reverse=False, dfinal=None):
+    """(dx, dforget, dgate, dstate) of the loss sum(dy * y) + sum(dfinal * final)."""
+    dy, x, z = (np.asarray(t, np.float64) for t in (dy, x, forget))
+    _, _, h = recurrence(x, z, cu, None, state, reverse)
+    o = None if gate is None else np.asarray(gate, np.float64)
+    dx, dz, do = (np.full(x.shape, np.nan) for _ in range(3))
+    dstate = np.zeros((len(cu) - 1,) + x.shape[1:]) if dfinal is None else np.array(dfinal, np.float64)
+    for i, run in enumerate(_runs(cu, reverse)):
+        for k in reversed(range(len(run))):
+            t = run[k]
+            before = h[run[k - 1]] if k else (0 if state is None else np.asarray(state, np.float64)[i])
+            direct = dy[t]
+            if o is not None:
+                sig = 1 / (1 + np.exp(-o[t]))
+                do[t] = dy[t] * h[t] * sig * (1 + o[t] * (1 - sig))
+                direct = dy[t] * o[t] * sig
+            dh = direct + dstate[i]
+            f, keep = 1 / (1 + np.exp(-z[t])), 1 / (1 + np.exp(z[t]))
+            dx[t] = keep * dh
+            dz[t] = dh * (before - x[t]) * f * keep
+            dstate[i] = f * dh
+    return dx, dz, None if gate is None else do, dstate
 
 
 def seen_position(pos, g, G, d4=False):
