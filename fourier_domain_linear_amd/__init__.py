@@ -26,6 +26,11 @@ The operators between the layers of a transformer stage (include/eqlin.h has the
     o, lse = eq.attention(q, k, v, cu_q, cu_k, causal=False)   # q: [T, H, D] or [T, H, dc, G]
     dq, dk, dv = eq.attention_backward(do, q, k, v, o, lse, cu_q, cu_k, causal=False)
 
+and of a recurrent one, which mixes tokens by a gated linear recurrence instead of attention:
+
+    y, final, marks = eq.recurrence(x, forget, cu, gate=o, state=h0)   # h = f h + (1 - f) x, y = h silu(o)
+    dx, dforget, dgate, dstate = eq.recurrence_backward(dy, x, forget, cu, marks, gate=o)
+
 Method: "Flash EQ-Linear: Accelerating Equivariant Linear Layers via Group-wise Discrete Fourier
 Transform" (explainer page, gist.science/es/paper/2607.21271).
 """
@@ -70,6 +75,8 @@ EXPORTED = (
     "eqlin_layernorm", "eqlin_layernorm_backward_workspace", "eqlin_layernorm_backward",
     "eqlin_rotary", "eqlin_attention_workspace", "eqlin_attention", "eqlin_attention_backward_workspace",
     "eqlin_attention_backward",
+    "eqlin_recurrence_marks", "eqlin_recurrence_workspace", "eqlin_recurrence", "eqlin_recurrence_backward_workspace",
+    "eqlin_recurrence_backward",
 )
 
 _lib = None
@@ -92,6 +99,20 @@ class AttentionGrads(ctypes.Structure):
     _fields_ = [("d_o", _vp), ("dq", _vp), ("dk", _vp), ("dv", _vp),
                 ("do_token_stride", _i64), ("do_head_stride", _i64), ("dq_token_stride", _i64), ("dq_head_stride", _i64),
                 ("dk_token_stride", _i64), ("dk_head_stride", _i64), ("dv_token_stride", _i64), ("dv_head_stride", _i64)]
+
+
+class RecurrenceArgs(ctypes.Structure):
+    """eqlin_recurrence_args."""
+    _fields_ = [("x", _vp), ("forget", _vp), ("gate", _vp), ("y", _vp), ("state", _vp), ("final", _vp), ("marks", _vp),
+                ("x_token_stride", _i64), ("forget_token_stride", _i64), ("gate_token_stride", _i64), ("y_token_stride", _i64),
+                ("cu", _vp), ("total", _i64), ("longest", _i64), ("batch", _i32), ("C", _i32), ("G", _i32), ("reverse", _i32),
+                ("dtype", _i32)]
+
+
+class RecurrenceGrads(ctypes.Structure):
+    """eqlin_recurrence_grads."""
+    _fields_ = [("dy", _vp), ("dfinal", _vp), ("dx", _vp), ("dforget", _vp), ("dgate", _vp), ("dstate", _vp),
+                ("dy_token_stride", _i64), ("dx_token_stride", _i64), ("dforget_token_stride", _i64), ("dgate_token_stride", _i64)]
 
 
 class EqlinError(RuntimeError):
@@ -157,11 +178,19 @@ def load_library() -> ctypes.CDLL:
     lib.eqlin_attention.argtypes = [args, vp, szt, vp]
     lib.eqlin_attention_backward_workspace.argtypes = [args]
     lib.eqlin_attention_backward.argtypes = [args, grads, vp, szt, vp]
+    rec, rgrads = ctypes.POINTER(RecurrenceArgs), ctypes.POINTER(RecurrenceGrads)
+    lib.eqlin_recurrence_marks.argtypes = [i64, i32]
+    lib.eqlin_recurrence_marks.restype = i64
+    lib.eqlin_recurrence_workspace.argtypes = [rec]
+    lib.eqlin_recurrence.argtypes = [rec, vp, szt, vp]
+    lib.eqlin_recurrence_backward_workspace.argtypes = [rec]
+    lib.eqlin_recurrence_backward.argtypes = [rec, rgrads, vp, szt, vp]
     for name in ("eqlin_rmsnorm", "eqlin_rmsnorm_quant", "eqlin_rmsnorm_backward", "eqlin_layernorm",
-                 "eqlin_layernorm_backward", "eqlin_rotary", "eqlin_attention", "eqlin_attention_backward"):
+                 "eqlin_layernorm_backward", "eqlin_rotary", "eqlin_attention", "eqlin_attention_backward", "eqlin_recurrence",
+                 "eqlin_recurrence_backward"):
         getattr(lib, name).restype = i32
     for name in ("eqlin_rmsnorm_backward_workspace", "eqlin_layernorm_backward_workspace", "eqlin_attention_workspace",
-                 "eqlin_attention_backward_workspace"):
+                 "eqlin_attention_backward_workspace", "eqlin_recurrence_workspace", "eqlin_recurrence_backward_workspace"):
         getattr(lib, name).restype = szt
     _lib = lib
     return lib
@@ -733,6 +762,112 @@ def attention_backward(do: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: to
     _check(_on(q.get_device(), lib.eqlin_attention_backward, pa, ctypes.byref(g), _ptr(workspace), need),
            "eqlin_attention_backward")
     return dq, dk, dv
+
+
+def _rows(t: torch.Tensor, name: str, like: torch.Tensor | None = None):
+    """t: [T, C, G], C * G contiguous; like ``like`` in shape, dtype and device."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA (HIP) tensor")
+    shape, strides = t.shape, t.stride()
+    if len(shape) != 3:
+        raise ValueError(f"{name} must be [T, C, G], got {tuple(shape)}")
+    if (strides[2] != 1 and shape[2] != 1) or (strides[1] != shape[2] and shape[1] != 1):
+        raise ValueError(f"{name}: a token's C * G elements must be contiguous")
+    if like is not None and (shape != like.shape or t.dtype != like.dtype or t.get_device() != like.get_device()):
+        raise ValueError(f"{name} must be {tuple(like.shape)} of {like.dtype} on {like.device}, got {tuple(shape)} {t.dtype} on {t.device}")
+
+
+def recurrence_marks(T: int, batch: int) -> int:
+    """Rows of the marks of T tokens in ``batch`` sequences (eqlin_recurrence_marks)."""
+    return int(load_library().eqlin_recurrence_marks(int(T), int(batch)))
+
+
+def _recurrence_args(x, forget, cu, gate, out, state, final, marks, reverse, longest):
+    _rows(x, "x")
+    _rows(forget, "forget", x)
+    if gate is not None:
+        _rows(gate, "gate", x)
+    if out is not None:
+        _rows(out, "out", x)
+    T, C, G = x.shape
+    _need_cuda(cu, "cu")
+    B = cu.numel() - 1
+    if B < 0:
+        raise ValueError("cu must hold batch + 1 entries")
+    _index(cu, "cu", (B + 1,), x.get_device())
+    if longest is not None and longest < 0:
+        raise ValueError(f"longest = {longest} < 0")
+    args = RecurrenceArgs(x.data_ptr(), forget.data_ptr(), _ptr(gate), _ptr(out), _ptr(state), _ptr(final), _ptr(marks),
+                          x.stride(0), forget.stride(0), 0 if gate is None else gate.stride(0), 0 if out is None else out.stride(0),
+                          cu.data_ptr(), T, longest or 0, B, C, G, 1 if reverse else 0, _dtype_code(x.dtype))
+    return args, B
+
+
+def recurrence(x: torch.Tensor, forget: torch.Tensor, cu: torch.Tensor, gate: torch.Tensor | None = None,
+               state: torch.Tensor | None = None, reverse: bool = False, longest: int | None = None, with_marks: bool = False,
+               final: torch.Tensor | None = None, out: torch.Tensor | None = None, workspace: torch.Tensor | None = None):
+    """eqlin_recurrence -> (y, final, marks): h = f h + (1 - f) x, f = sigmoid(forget), over the tokens of packed sequences;
+    y = h, or h silu(gate). x, forget, gate: [T, C, G] (tokens may be strided: parts of one layer's output); cu: int32
+    [batch + 1], the sequences' bounds; state: float32 [batch, C, G], the state in front of each sequence (None: zeros).
+    reverse: from the last token to the first. longest: tokens of the longest sequence, where the caller knows (a hint).
+    final: float32 [batch, C, G], the states after the last tokens (pass state itself to update it in place). marks: what
+    recurrence_backward needs, float32 [recurrence_marks(T, batch), C, G], None without with_marks. Rows of y outside every sequence are
+    left as they are."""
+    if out is None and isinstance(x, torch.Tensor):
+        out = x.new_empty(x.shape)
+    a, B = _recurrence_args(x, forget, cu, gate, out, None, None, None, reverse, longest)
+    shape = (B, *x.shape[1:])
+    if state is not None:
+        a.state = _f32_out(state, shape, x.device, "state").data_ptr()
+    final = _f32_out(final, shape, x.device, "final")
+    a.final = final.data_ptr()
+    lib, marks, pa = load_library(), None, ctypes.byref(a)
+    if with_marks:
+        marks = x.new_empty((lib.eqlin_recurrence_marks(x.shape[0], B), *x.shape[1:]), dtype=torch.float32)
+        a.marks = marks.data_ptr()
+    need = lib.eqlin_recurrence_workspace(pa)
+    workspace = _workspace(workspace, need, x.device) if need else None
+    st = _on(x.get_device(), lib.eqlin_recurrence, pa, _ptr(workspace), need)
+    if st != EQLIN_OK:
+        _check(st, "eqlin_recurrence")
+    return out, final, marks
+
+
+def recurrence_backward(dy: torch.Tensor, x: torch.Tensor, forget: torch.Tensor, cu: torch.Tensor, marks: torch.Tensor,
+                        gate: torch.Tensor | None = None, reverse: bool = False, dfinal: torch.Tensor | None = None,
+                        longest: int | None = None, with_state: bool = False, dx: torch.Tensor | None = None,
+                        dforget: torch.Tensor | None = None, dgate: torch.Tensor | None = None,
+                        workspace: torch.Tensor | None = None):
+    """eqlin_recurrence_backward -> (dx, dforget, dgate, dstate) from dy, the forward's tensors and its marks. dfinal: the
+    gradient of final (None: zeros). dx, dforget, dgate: tensors to write to (views of one gradient of a layer's output,
+    say), else new ones; dgate is None without a gate, dstate (float32 [batch, C, G]) without with_state."""
+    a, B = _recurrence_args(x, forget, cu, gate, None, None, None, None, reverse, longest)
+    _rows(dy, "dy", x)
+    lib, pa = load_library(), ctypes.byref(a)
+    shape = (B, *x.shape[1:])
+    a.marks = _f32_out(marks, (lib.eqlin_recurrence_marks(x.shape[0], B), *x.shape[1:]), x.device, "marks").data_ptr() \
+        if marks is not None else None
+    if dfinal is not None:
+        _f32_out(dfinal, shape, x.device, "dfinal")
+    grads = []
+    for name, t, like in (("dx", dx, x), ("dforget", dforget, x), ("dgate", dgate, gate)):
+        if like is None:
+            if t is not None:
+                raise ValueError(f"{name} without a gate")
+        elif t is None:
+            t = x.new_empty(x.shape)
+        else:
+            _rows(t, name, x)
+        grads.append(t)
+    dx, dforget, dgate = grads
+    dstate = x.new_empty(shape, dtype=torch.float32) if with_state else None
+    g = RecurrenceGrads(dy.data_ptr(), _ptr(dfinal), dx.data_ptr(), dforget.data_ptr(), _ptr(dgate), _ptr(dstate), dy.stride(0),
+                        dx.stride(0), dforget.stride(0), 0 if dgate is None else dgate.stride(0))
+    need = lib.eqlin_recurrence_backward_workspace(pa)
+    workspace = _workspace(workspace, need, x.device) if need else None
+    _check(_on(x.get_device(), lib.eqlin_recurrence_backward, pa, ctypes.byref(g), _ptr(workspace), need),
+           "eqlin_recurrence_backward")
+    return dx, dforget, dgate, dstate
 
 
 STATIC_SCRATCH_BYTES = 64 << 20  # EQLIN_STATIC_SCRATCH_BYTES

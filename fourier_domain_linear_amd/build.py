@@ -40,7 +40,7 @@ FILE_FLAGS = {f: ["-mllvm", "-amdgpu-mfma-vgpr-form"] for f in ("fwd_res8.hip", 
 REPORT = "-Rpass-analysis=kernel-resource-usage"
 NO_SPILLS = ("attn_fwd.hip", "attn_step.hip", "attn_bwd.hip")
 SOURCES = ["eqlin_api.cpp", "prepare.hip", "fwd_bf16.hip", "fwd_big.hip", "fwd_res.hip", "fwd_res8.hip", "fwd_f32.hip", "bwd.hip", "conv.hip",
-           "stage_api.cpp", "norm.hip", "layernorm.hip", "rotary.hip", "attn_fwd.hip", "attn_step.hip", "attn_bwd.hip"]
+           "stage_api.cpp", "norm.hip", "layernorm.hip", "recurrence.hip", "rotary.hip", "attn_fwd.hip", "attn_step.hip", "attn_bwd.hip"]
 
 
 def spilling_kernels(report: str) -> list[str]:

@@ -192,6 +192,33 @@ struct LayerNormGradParams {
 size_t layernorm_backward_workspace_bytes(int64_t N, int C, int G);
 hipError_t launch_layernorm_backward(const LayerNormGradParams &p, eqlin_dtype_t dtype, hipStream_t s);
 
+// ---- recurrence.hip ----
+constexpr int kRecurrenceChunk = 128;  // tokens between two marks
+struct RecurrenceParams {
+    const void *x, *f, *o;          // values, forget gates, output gates (or null)
+    int64_t xt, ft, ot, yt;         // token strides in elements
+    void *y;
+    const float *state;             // [B][L], L = C << lg, or null
+    float *final;                   // [B][L] or null; may be state
+    float *marks;                   // [slots][L]: the state in front of each chunk (forward: written, or null)
+    const int *cu;
+    int64_t T, slots, longest;
+    int B, C, lg;
+    bool reverse;
+    bool split;                     // chunks side by side, in three launches
+    // gradients
+    const void *dy;
+    const float *dfinal;
+    void *dx, *df, *dgo;
+    float *dstate;
+    int64_t dyt, dxt, dft, dgot;
+    // workspace, [slots][L] each
+    float *ends_a, *ends_b, *carry;
+};
+void plan_recurrence(RecurrenceParams &p);  // fills in slots and split
+size_t recurrence_workspace_bytes(const RecurrenceParams &p);
+hipError_t launch_recurrence(RecurrenceParams p, eqlin_dtype_t dtype, bool back, float *ws, hipStream_t s);
+
 // ---- rotary.hip ----
 constexpr int kRotaryMaxPairs = 256, kRotaryMaxAxes = 4;
 struct RotaryParams {

@@ -15,41 +15,6 @@ namespace eqlin {
 
 namespace {
 
-// W elements at p (aligned to W elements) as fp32, in one load, and back in one store.
-template <class E, int W>
-struct Pack {
-    typedef Elem<E> EL;
-    typedef typename EL::T T;
-    static constexpr int kWords = W * (int)sizeof(T) / 4;  // 0: a single half
-    uint32_t w[kWords ? kWords : 1];
-    __device__ __forceinline__ void clear() {
-#pragma unroll
-        for (int i = 0; i < (kWords ? kWords : 1); ++i) w[i] = 0;
-    }
-    __device__ __forceinline__ void load(const T *p) {
-        if constexpr (kWords == 4) {
-            const uint4 u = *(const uint4 *)p;
-            w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
-        } else if constexpr (kWords == 1) {
-            w[0] = *(const uint32_t *)p;
-        } else {
-            static_assert(kWords == 0, "16 bytes, 4 bytes or a single half");
-            w[0] = *(const uint16_t *)p;
-        }
-    }
-    __device__ __forceinline__ void unpack(float *f) const {
-        if constexpr (kWords == 4) EL::unpack(make_uint4(w[0], w[1], w[2], w[3]), f);
-        else if constexpr (sizeof(T) == 4) f[0] = __uint_as_float(w[0]);
-        else if constexpr (W == 2) f[0] = EL::get((T)(w[0] & 0xffffu)), f[1] = EL::get((T)(w[0] >> 16));
-        else f[0] = EL::get((T)w[0]);
-    }
-    static __device__ __forceinline__ void store(T *p, const float *f) {
-        if constexpr (kWords == 4) *(uint4 *)p = EL::pack(f);
-        else if constexpr (sizeof(T) == 2 && W == 2) *(uint32_t *)p = pack2<E>(f[0], f[1]);
-        else *p = EL::put(f[0]);
-    }
-};
-
 // two sums over the lanes that share a row, in one exchange
 template <int WAVES>
 __device__ __forceinline__ void sum_two(float *red, float &a, float &b) {

@@ -1,5 +1,5 @@
 // stage_api.cpp -- the C entry points of the operators between the layers (norms, rotary positions,
-// attention): argument checks and dispatch. Nothing here computes; every step runs in the HIP kernels.
+// attention, recurrence): argument checks and dispatch. Nothing here computes; every step runs in the HIP kernels.
 #include <hip/hip_runtime.h>
 #include <math.h>
 
@@ -170,6 +170,39 @@ bool folds(int64_t ts, int64_t hs, int64_t tokens, int heads, int dim) {
 
 size_t extent(int64_t ts, int64_t hs, int64_t tokens, int heads, int dim, eqlin_dtype_t d) {
     return tokens == 0 ? 0 : (size_t)((tokens - 1) * ts + (heads - 1) * hs + dim) * elem_bytes(d);
+}
+
+// arguments shared by the recurrence's entry points -> the kernels' parameters
+eqlin_status_t check_recurrence(const eqlin_recurrence_args *a, eqlin::RecurrenceParams *p) {
+    if (!a) return api_fail(EQLIN_ERR_INVALID_ARG, "null arguments");
+    if (!valid_dtype(a->dtype)) return api_fail(EQLIN_ERR_INVALID_ARG, "bad dtype %d", (int)a->dtype);
+    if (a->total < 0 || a->batch < 0 || a->longest < 0)
+        return api_fail(EQLIN_ERR_INVALID_ARG, "total = %lld, batch = %d, longest = %lld", (long long)a->total, a->batch, (long long)a->longest);
+    if (a->C < 1 || !(a->G == 1 || a->G == 2 || a->G == 4 || a->G == 8))
+        return api_fail(EQLIN_ERR_INVALID_ARG, "C = %d must be >= 1, G = %d in {1, 2, 4, 8}", a->C, a->G);
+    const int64_t L = (int64_t)a->C * a->G;
+    if (L > (1 << 20)) return api_fail(EQLIN_ERR_UNSUPPORTED, "C * G = %lld beyond 2^20", (long long)L);
+    if (a->total > (1 << 30) || a->batch > (1 << 24)) return api_fail(EQLIN_ERR_UNSUPPORTED, "total beyond 2^30 or batch beyond 2^24");
+    *p = eqlin::RecurrenceParams{};
+    p->x = a->x, p->f = a->forget, p->o = a->gate, p->y = a->y;
+    p->xt = stride_of(a->x_token_stride, a->total), p->ft = stride_of(a->forget_token_stride, a->total);
+    p->ot = stride_of(a->gate_token_stride, a->total), p->yt = stride_of(a->y_token_stride, a->total);
+    p->state = a->state, p->final = a->final, p->marks = a->marks, p->cu = a->cu;
+    p->T = a->total, p->B = a->batch, p->C = a->C, p->lg = ilog2(a->G);
+    p->longest = a->longest > 0 ? std::min(a->longest, a->total) : a->total;
+    p->reverse = a->reverse != 0;
+    eqlin::plan_recurrence(*p);
+    return EQLIN_OK;
+}
+
+// a [tokens][C * G] tensor's pointer and stride
+eqlin_status_t check_rows(const void *t, int64_t stride, int64_t tokens, int64_t L, eqlin_dtype_t dtype, const char *name, bool out) {
+    if (tokens == 0) return EQLIN_OK;
+    if (!t) return api_fail(EQLIN_ERR_INVALID_ARG, "null %s", name);
+    if (!aligned(t, elem_bytes(dtype))) return api_fail(EQLIN_ERR_INVALID_ARG, "%s misaligned", name);
+    if (stride < 0 || stride > (INT64_C(1) << 28)) return api_fail(EQLIN_ERR_INVALID_ARG, "%s: token stride out of range", name);
+    if (out && tokens > 1 && stride < L) return api_fail(EQLIN_ERR_INVALID_ARG, "%s's token stride folds it onto itself", name);
+    return EQLIN_OK;
 }
 
 }  // namespace
@@ -429,6 +462,94 @@ eqlin_status_t eqlin_attention_backward(const eqlin_attention_args *a, const eql
     p.ws = (float *)workspace;
     (void)hipGetLastError();
     return done(eqlin::launch_attention_backward(p, a->dtype, (hipStream_t)stream), "eqlin_attention_backward launch");
+}
+
+int64_t eqlin_recurrence_marks(int64_t total, int batch) {
+    return total < 0 || batch < 0 ? 0 : total / eqlin::kRecurrenceChunk + batch;
+}
+
+size_t eqlin_recurrence_workspace(const eqlin_recurrence_args *a) {
+    eqlin::RecurrenceParams p;
+    return check_recurrence(a, &p) == EQLIN_OK ? eqlin::recurrence_workspace_bytes(p) : 0;
+}
+
+eqlin_status_t eqlin_recurrence(const eqlin_recurrence_args *a, void *workspace, size_t workspace_bytes, eqlin_stream_t stream) {
+    eqlin::api_clear();
+    eqlin::RecurrenceParams p;
+    eqlin_status_t st = check_recurrence(a, &p);
+    if (st != EQLIN_OK) return st;
+    if (a->batch == 0) return EQLIN_OK;
+    const int64_t T = a->total, L = (int64_t)a->C * a->G;
+    if ((st = check_rows(a->x, p.xt, T, L, a->dtype, "x", false)) != EQLIN_OK) return st;
+    if ((st = check_rows(a->forget, p.ft, T, L, a->dtype, "forget", false)) != EQLIN_OK) return st;
+    if (a->gate && (st = check_rows(a->gate, p.ot, T, L, a->dtype, "gate", false)) != EQLIN_OK) return st;
+    if ((st = check_rows(a->y, p.yt, T, L, a->dtype, "y", true)) != EQLIN_OK) return st;
+    if (!a->cu) return api_fail(EQLIN_ERR_INVALID_ARG, "null cu");
+    if (!aligned(a->cu, 4) || !aligned(a->state, 4) || !aligned(a->final, 4) || !aligned(a->marks, 4))
+        return api_fail(EQLIN_ERR_INVALID_ARG, "cu, state, final or marks misaligned");
+    const size_t need = eqlin::recurrence_workspace_bytes(p), states = (size_t)a->batch * L * 4;
+    if ((st = check_workspace(workspace, workspace_bytes, need)) != EQLIN_OK) return st;
+    auto rows = [&](int64_t stride) { return extent(stride, 0, T, 1, (int)L, a->dtype); };
+    const bool in_place = a->final == a->state;
+    const Span ins[] = {{a->x, rows(p.xt), "x"}, {a->forget, rows(p.ft), "forget"}, {a->gate, rows(p.ot), "gate"},
+                        {in_place ? nullptr : a->state, states, "state"}, {a->cu, ((size_t)a->batch + 1) * 4, "cu"}};
+    const Span outs[] = {{a->y, rows(p.yt), "y"}, {in_place ? a->state : a->final, states, "final"},
+                         {a->marks, (size_t)p.slots * L * 4, "marks"}, {workspace, need, "workspace"}};
+    if ((st = check_apart(outs, ins)) != EQLIN_OK) return st;
+    (void)hipGetLastError();
+    return done(eqlin::launch_recurrence(p, a->dtype, false, (float *)workspace, (hipStream_t)stream), "eqlin_recurrence launch");
+}
+
+size_t eqlin_recurrence_backward_workspace(const eqlin_recurrence_args *a) { return eqlin_recurrence_workspace(a); }
+
+eqlin_status_t eqlin_recurrence_backward(const eqlin_recurrence_args *a, const eqlin_recurrence_grads *g, void *workspace,
+                                         size_t workspace_bytes, eqlin_stream_t stream) {
+    eqlin::api_clear();
+    eqlin::RecurrenceParams p;
+    eqlin_status_t st = check_recurrence(a, &p);
+    if (st != EQLIN_OK) return st;
+    if (!g) return api_fail(EQLIN_ERR_INVALID_ARG, "null gradients");
+    if (a->batch == 0) return EQLIN_OK;
+    const int64_t T = a->total, L = (int64_t)a->C * a->G;
+    p.dy = g->dy, p.dx = g->dx, p.df = g->dforget, p.dgo = g->dgate, p.dfinal = g->dfinal, p.dstate = g->dstate;
+    p.dyt = stride_of(g->dy_token_stride, T), p.dxt = stride_of(g->dx_token_stride, T);
+    p.dft = stride_of(g->dforget_token_stride, T), p.dgot = stride_of(g->dgate_token_stride, T);
+    if (!a->gate && g->dgate) return api_fail(EQLIN_ERR_INVALID_ARG, "dgate without a gate");
+    const struct {
+        const void *t;
+        int64_t stride;
+        const char *name;
+        bool out, may_be_null;
+    } t[] = {{a->x, p.xt, "x", false, false},   {a->forget, p.ft, "forget", false, false}, {a->gate, p.ot, "gate", false, true},
+             {g->dy, p.dyt, "dy", false, false}, {g->dx, p.dxt, "dx", true, false},         {g->dforget, p.dft, "dforget", true, false},
+             {g->dgate, p.dgot, "dgate", true, true}};
+    for (const auto &x : t)
+        if ((x.t || !x.may_be_null) && (st = check_rows(x.t, x.stride, T, L, a->dtype, x.name, x.out)) != EQLIN_OK) return st;
+    if (!a->cu || (T > 0 && !a->marks)) return api_fail(EQLIN_ERR_INVALID_ARG, "null cu or marks");
+    if (!aligned(a->cu, 4) || !aligned(a->marks, 4) || !aligned(g->dfinal, 4) || !aligned(g->dstate, 4))
+        return api_fail(EQLIN_ERR_INVALID_ARG, "cu, marks, dfinal or dstate misaligned");
+    const size_t need = eqlin::recurrence_workspace_bytes(p), states = (size_t)a->batch * L * 4;
+    if ((st = check_workspace(workspace, workspace_bytes, need)) != EQLIN_OK) return st;
+    auto rows = [&](int64_t stride) { return extent(stride, 0, T, 1, (int)L, a->dtype); };
+    const Span ins[] = {{a->x, rows(p.xt), "x"}, {a->forget, rows(p.ft), "forget"}, {a->gate, rows(p.ot), "gate"}, {g->dy, rows(p.dyt), "dy"},
+                        {a->marks, (size_t)p.slots * L * 4, "marks"}, {a->cu, ((size_t)a->batch + 1) * 4, "cu"}, {g->dfinal, states, "dfinal"}};
+    const Span more[] = {{g->dstate, states, "dstate"}, {workspace, need, "workspace"}};
+    if ((st = check_apart(more, ins)) != EQLIN_OK) return st;
+    // dx, dforget and dgate may be interleaved parts of one tensor (the gradient of a layer's output): of one stride, they
+    // are refused where rows share elements, of several where their memory meets
+    for (const auto &x : t) {
+        if (!x.out || !x.t) continue;
+        const Span sx[] = {{x.t, rows(x.stride), x.name}};
+        if ((st = check_apart(sx, ins)) != EQLIN_OK || (st = check_apart(sx, more)) != EQLIN_OK) return st;
+        for (const auto &y : t) {
+            if (!y.out || !y.t || &y >= &x || !overlap(x.t, rows(x.stride), y.t, rows(y.stride))) continue;
+            const int64_t by = ((const char *)y.t - (const char *)x.t) / (int64_t)elem_bytes(a->dtype);
+            if (x.stride != y.stride || heads_meet(x.stride, 0, L, T, 1, T, 1, by, false))
+                return api_fail(EQLIN_ERR_INVALID_ARG, "%s and %s share memory", y.name, x.name);
+        }
+    }
+    (void)hipGetLastError();
+    return done(eqlin::launch_recurrence(p, a->dtype, true, (float *)workspace, (hipStream_t)stream), "eqlin_recurrence_backward launch");
 }
 
 }  // extern "C"

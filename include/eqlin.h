@@ -469,6 +469,71 @@ size_t eqlin_attention_backward_workspace(const eqlin_attention_args *a);
 eqlin_status_t eqlin_attention_backward(const eqlin_attention_args *a, const eqlin_attention_grads *g, void *workspace,
                                         size_t workspace_bytes, eqlin_stream_t stream);
 
+/*
+ * eqlin_recurrence -- gated linear recurrence over packed sequences, a stage's other way to mix tokens (next to attention;
+ * an EQ-VMamba block, "lpnh.cn/news/964151", mixes by a recurrence whose inputs EQ-Linear layers produce). For the
+ * tokens t of a sequence in order (reverse: from the last to the first) and every channel and group element:
+ *
+ *     f = sigmoid(forget[t]);   h = f h + (1 - f) x[t];   y[t] = h,  or  h silu(gate[t]) with an output gate
+ *
+ * h starts from the sequence's state (zeros without one) and its last value is the sequence's final. The operator acts on
+ * each group element alone, so a shift of the group axis passes through. fp32 throughout (states, marks, the exponentials'
+ * results); one rounding of y. A value that is not finite makes later results of its own sequence and column not
+ * finite (infinite or NaN) and has no part in any other.
+ *   x, forget, gate, y   tensor[token][C][G] of dtype with token strides in ELEMENTS (C * G contiguous): parts of one
+ *                layer's output, say. gate may be NULL. Token strides up to 2^28. Odd widths, strides or pointers off two
+ *                elements run a slower kernel.
+ *   cu           device int32 [batch + 1], not decreasing: sequence i has the tokens from cu[i] to cu[i + 1]. Rows outside
+ *                every sequence are left as they are, here and in the gradients. Sequences may be empty: final = state.
+ *   state        device float [batch][C][G] or NULL (zeros).
+ *   final        device float [batch][C][G] or NULL; may be state itself (a step that updates its states in place).
+ *   marks        device float [eqlin_recurrence_marks(total, batch)][C][G] or NULL: the states in front of every 128th
+ *                token of each sequence, which the backward needs.
+ *   longest      the number of tokens of the longest sequence, or more, if known, else 0. It chooses how the work is split and
+ *                nothing else: results are right whatever it says (in the last bits they depend on the split).
+ *   total <= 2^30, batch <= 2^24, C * G <= 2^20 (else UNSUPPORTED).
+ *   workspace    eqlin_recurrence_workspace(a) bytes, 256-byte aligned (NULL when that is 0). Calls sharing it must not overlap.
+ * y, final, marks and the workspace overlap neither an input nor each other (final = state apart).
+ */
+typedef struct eqlin_recurrence_args {
+    const void *x, *forget, *gate;
+    void *y;
+    const float *state;
+    float *final, *marks;
+    int64_t x_token_stride, forget_token_stride, gate_token_stride, y_token_stride;
+    const int32_t *cu;
+    int64_t total, longest;
+    int batch, C, G, reverse;
+    eqlin_dtype_t dtype;
+} eqlin_recurrence_args;
+int64_t eqlin_recurrence_marks(int64_t total, int batch);
+size_t eqlin_recurrence_workspace(const eqlin_recurrence_args *a);
+eqlin_status_t eqlin_recurrence(const eqlin_recurrence_args *a, void *workspace, size_t workspace_bytes,
+                                eqlin_stream_t stream);
+
+/*
+ * eqlin_recurrence_backward -- with dh[t] = dy[t] silu(gate[t]) + f[t+1] dh[t+1] (t + 1: the token after it in the recurrence's
+ * order; dfinal instead at the last):
+ *
+ *     dx = (1 - f) dh;   dforget = dh (h[t-1] - x) f (1 - f);   dgate = dy h silu'(gate);   dstate = f dh of the first token
+ *
+ * a: the forward's arguments, with its marks (y, state and final are not used). dy: as y. dx, dforget, dgate: as x, with strides,
+ * overwritten; they may be interleaved parts of one tensor but share no elements and overlap no input. dgate may be NULL (it
+ * must be without a gate). dfinal, the gradient of final, and dstate: device float [batch][C][G] or NULL each (dfinal: zeros);
+ * dstate of an empty sequence is its dfinal. States and gradients in fp32, each result rounded once.
+ *   workspace  eqlin_recurrence_backward_workspace(a) bytes, 256-byte aligned, apart from every tensor.
+ */
+typedef struct eqlin_recurrence_grads {
+    const void *dy;
+    const float *dfinal;
+    void *dx, *dforget, *dgate;
+    float *dstate;
+    int64_t dy_token_stride, dx_token_stride, dforget_token_stride, dgate_token_stride;
+} eqlin_recurrence_grads;
+size_t eqlin_recurrence_backward_workspace(const eqlin_recurrence_args *a);
+eqlin_status_t eqlin_recurrence_backward(const eqlin_recurrence_args *a, const eqlin_recurrence_grads *g, void *workspace,
+                                         size_t workspace_bytes, eqlin_stream_t stream);
+
 /* Frees the handle's device memory (hipFree, which synchronises the device). NULL is a no-op. */
 eqlin_status_t eqlin_destroy(eqlin_handle_t h);
 
