@@ -193,7 +193,7 @@ size_t layernorm_backward_workspace_bytes(int64_t N, int C, int G);
 hipError_t launch_layernorm_backward(const LayerNormGradParams &p, eqlin_dtype_t dtype, hipStream_t s);
 
 // ---- recurrence.hip ----
-constexpr int kRecurrenceChunk = 128;  // tokens between two marks
+constexpr int kRecurrenceChunk = 64;  // tokens between two marks
 struct RecurrenceParams {
     const void *x, *f, *o;          // values, forget gates, output gates (or null)
     int64_t xt, ft, ot, yt;         // token strides in elements
@@ -205,19 +205,21 @@ struct RecurrenceParams {
     int64_t T, slots, longest;
     int B, C, lg;
     bool reverse;
-    bool split;                     // chunks side by side, in three launches
+    bool split, joined;             // a workgroup a chunk; states in front of chunks by a launch of their own
+    int groups;                     // else: groups of lanes a wave
     // gradients
     const void *dy;
     const float *dfinal;
     void *dx, *df, *dgo;
     float *dstate;
     int64_t dyt, dxt, dft, dgot;
-    // workspace, [slots][L] each
-    float *ends_a, *ends_b, *carry;
+    // workspace, [slots][L] each: (A, B) of the chunks, states in front of them (or null)
+    float2 *ends;
+    float *carry;
 };
-void plan_recurrence(RecurrenceParams &p);  // fills in slots and split
+void plan_recurrence(RecurrenceParams &p, eqlin_dtype_t dtype, bool back);  // fills in slots and form
 size_t recurrence_workspace_bytes(const RecurrenceParams &p);
-hipError_t launch_recurrence(RecurrenceParams p, eqlin_dtype_t dtype, bool back, float *ws, hipStream_t s);
+hipError_t launch_recurrence(RecurrenceParams p, eqlin_dtype_t dtype, bool back, void *ws, hipStream_t s);
 
 // ---- rotary.hip ----
 constexpr int kRotaryMaxPairs = 256, kRotaryMaxAxes = 4;

@@ -173,7 +173,7 @@ size_t extent(int64_t ts, int64_t hs, int64_t tokens, int heads, int dim, eqlin_
 }
 
 // arguments shared by the recurrence's entry points -> the kernels' parameters
-eqlin_status_t check_recurrence(const eqlin_recurrence_args *a, eqlin::RecurrenceParams *p) {
+eqlin_status_t check_recurrence(const eqlin_recurrence_args *a, bool back, eqlin::RecurrenceParams *p) {
     if (!a) return api_fail(EQLIN_ERR_INVALID_ARG, "null arguments");
     if (!valid_dtype(a->dtype)) return api_fail(EQLIN_ERR_INVALID_ARG, "bad dtype %d", (int)a->dtype);
     if (a->total < 0 || a->batch < 0 || a->longest < 0)
@@ -185,23 +185,24 @@ eqlin_status_t check_recurrence(const eqlin_recurrence_args *a, eqlin::Recurrenc
     if (a->total > (1 << 30) || a->batch > (1 << 24)) return api_fail(EQLIN_ERR_UNSUPPORTED, "total beyond 2^30 or batch beyond 2^24");
     *p = eqlin::RecurrenceParams{};
     p->x = a->x, p->f = a->forget, p->o = a->gate, p->y = a->y;
-    p->xt = stride_of(a->x_token_stride, a->total), p->ft = stride_of(a->forget_token_stride, a->total);
-    p->ot = stride_of(a->gate_token_stride, a->total), p->yt = stride_of(a->y_token_stride, a->total);
+    // (of one token a stride means nothing; the kernels tell rows apart by it)
+    auto stride = [&](int64_t s) { return a->total > 1 ? s : L; };
+    p->xt = stride(a->x_token_stride), p->ft = stride(a->forget_token_stride), p->ot = stride(a->gate_token_stride), p->yt = stride(a->y_token_stride);
     p->state = a->state, p->final = a->final, p->marks = a->marks, p->cu = a->cu;
     p->T = a->total, p->B = a->batch, p->C = a->C, p->lg = ilog2(a->G);
     p->longest = a->longest > 0 ? std::min(a->longest, a->total) : a->total;
     p->reverse = a->reverse != 0;
-    eqlin::plan_recurrence(*p);
+    eqlin::plan_recurrence(*p, a->dtype, back);
     return EQLIN_OK;
 }
 
 // a [tokens][C * G] tensor's pointer and stride
-eqlin_status_t check_rows(const void *t, int64_t stride, int64_t tokens, int64_t L, eqlin_dtype_t dtype, const char *name, bool out) {
+eqlin_status_t check_rows(const void *t, int64_t stride, int64_t tokens, int64_t L, eqlin_dtype_t dtype, const char *name) {
     if (tokens == 0) return EQLIN_OK;
     if (!t) return api_fail(EQLIN_ERR_INVALID_ARG, "null %s", name);
     if (!aligned(t, elem_bytes(dtype))) return api_fail(EQLIN_ERR_INVALID_ARG, "%s misaligned", name);
-    if (stride < 0 || stride > (INT64_C(1) << 28)) return api_fail(EQLIN_ERR_INVALID_ARG, "%s: token stride out of range", name);
-    if (out && tokens > 1 && stride < L) return api_fail(EQLIN_ERR_INVALID_ARG, "%s's token stride folds it onto itself", name);
+    if (stride < 0 || stride > (INT64_C(1) << 24)) return api_fail(EQLIN_ERR_INVALID_ARG, "%s: token stride out of range", name);
+    if (tokens > 1 && stride < L) return api_fail(EQLIN_ERR_INVALID_ARG, "%s's token stride folds it onto itself", name);
     return EQLIN_OK;
 }
 
@@ -470,20 +471,20 @@ int64_t eqlin_recurrence_marks(int64_t total, int batch) {
 
 size_t eqlin_recurrence_workspace(const eqlin_recurrence_args *a) {
     eqlin::RecurrenceParams p;
-    return check_recurrence(a, &p) == EQLIN_OK ? eqlin::recurrence_workspace_bytes(p) : 0;
+    return check_recurrence(a, false, &p) == EQLIN_OK ? eqlin::recurrence_workspace_bytes(p) : 0;
 }
 
 eqlin_status_t eqlin_recurrence(const eqlin_recurrence_args *a, void *workspace, size_t workspace_bytes, eqlin_stream_t stream) {
     eqlin::api_clear();
     eqlin::RecurrenceParams p;
-    eqlin_status_t st = check_recurrence(a, &p);
+    eqlin_status_t st = check_recurrence(a, false, &p);
     if (st != EQLIN_OK) return st;
     if (a->batch == 0) return EQLIN_OK;
     const int64_t T = a->total, L = (int64_t)a->C * a->G;
-    if ((st = check_rows(a->x, p.xt, T, L, a->dtype, "x", false)) != EQLIN_OK) return st;
-    if ((st = check_rows(a->forget, p.ft, T, L, a->dtype, "forget", false)) != EQLIN_OK) return st;
-    if (a->gate && (st = check_rows(a->gate, p.ot, T, L, a->dtype, "gate", false)) != EQLIN_OK) return st;
-    if ((st = check_rows(a->y, p.yt, T, L, a->dtype, "y", true)) != EQLIN_OK) return st;
+    if ((st = check_rows(a->x, p.xt, T, L, a->dtype, "x")) != EQLIN_OK) return st;
+    if ((st = check_rows(a->forget, p.ft, T, L, a->dtype, "forget")) != EQLIN_OK) return st;
+    if (a->gate && (st = check_rows(a->gate, p.ot, T, L, a->dtype, "gate")) != EQLIN_OK) return st;
+    if ((st = check_rows(a->y, p.yt, T, L, a->dtype, "y")) != EQLIN_OK) return st;
     if (!a->cu) return api_fail(EQLIN_ERR_INVALID_ARG, "null cu");
     if (!aligned(a->cu, 4) || !aligned(a->state, 4) || !aligned(a->final, 4) || !aligned(a->marks, 4))
         return api_fail(EQLIN_ERR_INVALID_ARG, "cu, state, final or marks misaligned");
@@ -497,23 +498,26 @@ eqlin_status_t eqlin_recurrence(const eqlin_recurrence_args *a, void *workspace,
                          {a->marks, (size_t)p.slots * L * 4, "marks"}, {workspace, need, "workspace"}};
     if ((st = check_apart(outs, ins)) != EQLIN_OK) return st;
     (void)hipGetLastError();
-    return done(eqlin::launch_recurrence(p, a->dtype, false, (float *)workspace, (hipStream_t)stream), "eqlin_recurrence launch");
+    return done(eqlin::launch_recurrence(p, a->dtype, false, workspace, (hipStream_t)stream), "eqlin_recurrence launch");
 }
 
-size_t eqlin_recurrence_backward_workspace(const eqlin_recurrence_args *a) { return eqlin_recurrence_workspace(a); }
+size_t eqlin_recurrence_backward_workspace(const eqlin_recurrence_args *a) {
+    eqlin::RecurrenceParams p;
+    return check_recurrence(a, true, &p) == EQLIN_OK ? eqlin::recurrence_workspace_bytes(p) : 0;
+}
 
 eqlin_status_t eqlin_recurrence_backward(const eqlin_recurrence_args *a, const eqlin_recurrence_grads *g, void *workspace,
                                          size_t workspace_bytes, eqlin_stream_t stream) {
     eqlin::api_clear();
     eqlin::RecurrenceParams p;
-    eqlin_status_t st = check_recurrence(a, &p);
+    eqlin_status_t st = check_recurrence(a, true, &p);
     if (st != EQLIN_OK) return st;
     if (!g) return api_fail(EQLIN_ERR_INVALID_ARG, "null gradients");
     if (a->batch == 0) return EQLIN_OK;
     const int64_t T = a->total, L = (int64_t)a->C * a->G;
     p.dy = g->dy, p.dx = g->dx, p.df = g->dforget, p.dgo = g->dgate, p.dfinal = g->dfinal, p.dstate = g->dstate;
-    p.dyt = stride_of(g->dy_token_stride, T), p.dxt = stride_of(g->dx_token_stride, T);
-    p.dft = stride_of(g->dforget_token_stride, T), p.dgot = stride_of(g->dgate_token_stride, T);
+    auto stride = [&](int64_t s) { return T > 1 ? s : L; };
+    p.dyt = stride(g->dy_token_stride), p.dxt = stride(g->dx_token_stride), p.dft = stride(g->dforget_token_stride), p.dgot = stride(g->dgate_token_stride);
     if (!a->gate && g->dgate) return api_fail(EQLIN_ERR_INVALID_ARG, "dgate without a gate");
     const struct {
         const void *t;
@@ -524,7 +528,7 @@ eqlin_status_t eqlin_recurrence_backward(const eqlin_recurrence_args *a, const e
              {g->dy, p.dyt, "dy", false, false}, {g->dx, p.dxt, "dx", true, false},         {g->dforget, p.dft, "dforget", true, false},
              {g->dgate, p.dgot, "dgate", true, true}};
     for (const auto &x : t)
-        if ((x.t || !x.may_be_null) && (st = check_rows(x.t, x.stride, T, L, a->dtype, x.name, x.out)) != EQLIN_OK) return st;
+        if ((x.t || !x.may_be_null) && (st = check_rows(x.t, x.stride, T, L, a->dtype, x.name)) != EQLIN_OK) return st;
     if (!a->cu || (T > 0 && !a->marks)) return api_fail(EQLIN_ERR_INVALID_ARG, "null cu or marks");
     if (!aligned(a->cu, 4) || !aligned(a->marks, 4) || !aligned(g->dfinal, 4) || !aligned(g->dstate, 4))
         return api_fail(EQLIN_ERR_INVALID_ARG, "cu, marks, dfinal or dstate misaligned");
@@ -549,7 +553,7 @@ eqlin_status_t eqlin_recurrence_backward(const eqlin_recurrence_args *a, const e
         }
     }
     (void)hipGetLastError();
-    return done(eqlin::launch_recurrence(p, a->dtype, true, (float *)workspace, (hipStream_t)stream), "eqlin_recurrence_backward launch");
+    return done(eqlin::launch_recurrence(p, a->dtype, true, workspace, (hipStream_t)stream), "eqlin_recurrence_backward launch");
 }
 
 }  // extern "C"

@@ -481,13 +481,13 @@ eqlin_status_t eqlin_attention_backward(const eqlin_attention_args *a, const eql
  * results); one rounding of y. A value that is not finite makes later results of its own sequence and column not
  * finite (infinite or NaN) and has no part in any other.
  *   x, forget, gate, y   tensor[token][C][G] of dtype with token strides in ELEMENTS (C * G contiguous): parts of one
- *                layer's output, say. gate may be NULL. Token strides up to 2^28. Odd widths, strides or pointers off two
- *                elements run a slower kernel.
+ *                layer's output, say. gate may be NULL. Token strides from C * G to 2^24. Odd widths,
+ *                strides or pointers off two elements run a slower kernel.
  *   cu           device int32 [batch + 1], not decreasing: sequence i has the tokens from cu[i] to cu[i + 1]. Rows outside
  *                every sequence are left as they are, here and in the gradients. Sequences may be empty: final = state.
  *   state        device float [batch][C][G] or NULL (zeros).
  *   final        device float [batch][C][G] or NULL; may be state itself (a step that updates its states in place).
- *   marks        device float [eqlin_recurrence_marks(total, batch)][C][G] or NULL: the states in front of every 128th
+ *   marks        device float [eqlin_recurrence_marks(total, batch)][C][G] or NULL: the states in front of every 64th
  *                token of each sequence, which the backward needs.
  *   longest      the number of tokens of the longest sequence, or more, if known, else 0. It chooses how the work is split and
  *                nothing else: results are right whatever it says (in the last bits they depend on the split).

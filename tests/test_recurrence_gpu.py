@@ -216,7 +216,8 @@ def test_extreme_gates(cuda_device):
     assert y[:, 0].flatten().tolist() == [9] * 4 and y[:, 2].flatten().tolist() == [9] * 4
     assert y[:, 1].flatten().tolist() == [1, 2, 3, 4] and y[:, 3].flatten().tolist() == [1, 2, 3, 4]
     assert dx[:, 0].flatten().tolist() == [0] * 4 and dx[:, 1].flatten().tolist() == [1] * 4 and not dz.any()
-    assert dh.flatten().tolist() == [4, 0, 4, 0]
+    dh = dh.flatten().tolist()
+    assert dh[0] == 4 and dh[2] == 4 and max(abs(dh[1]), abs(dh[3])) <= 4 * 2.0 ** -126  # (half types: f is at least 2^-126)
 
 
 def test_gradients_by_differences(cuda_device):

@@ -59,8 +59,8 @@ def _rec(**change):
     (dict(G=3), INVALID), (dict(C=1 << 19), UNSUPPORTED), (dict(total=(1 << 30) + 1), UNSUPPORTED), (dict(batch=(1 << 24) + 1), UNSUPPORTED),
     (dict(x=None), INVALID), (dict(forget=None), INVALID), (dict(y=None), INVALID), (dict(cu=None), INVALID), (dict(x=_at(0) + 1), INVALID),
     (dict(y=_at(3) + 1), INVALID), (dict(cu=_at(7) + 2), INVALID), (dict(state=_at(4) + 2), INVALID), (dict(final=_at(5) + 1), INVALID),
-    (dict(marks=_at(6) + 2), INVALID), (dict(x_token_stride=-64), INVALID), (dict(y_token_stride=63), INVALID), (dict(y_token_stride=0), INVALID),
-    (dict(gate_token_stride=1 << 29), INVALID), (dict(y=_at(0)), INVALID), (dict(y=_at(2) + 64), INVALID), (dict(final=_at(4) + 64), INVALID),
+    (dict(marks=_at(6) + 2), INVALID), (dict(x_token_stride=-64), INVALID), (dict(forget_token_stride=63), INVALID), (dict(gate_token_stride=0), INVALID), (dict(y_token_stride=63), INVALID), (dict(y_token_stride=0), INVALID),
+    (dict(gate_token_stride=(1 << 24) + 1), INVALID), (dict(y=_at(0)), INVALID), (dict(y=_at(2) + 64), INVALID), (dict(final=_at(4) + 64), INVALID),
     (dict(final=_at(1)), INVALID), (dict(marks=_at(4)), INVALID), (dict(marks=_at(5)), INVALID), (dict(y=_at(7) - 4096), INVALID),
     (dict(marks=_at(7)), INVALID), (dict(total=10000, batch=1), INVALID)])
 def test_recurrence_refusals(lib, change, want):  # noqa: F811
@@ -72,10 +72,10 @@ def test_recurrence_of_nothing_and_sizes(lib):  # noqa: F811
     assert lib.eqlin_recurrence(ctypes.byref(_rec(batch=0, x=None, cu=None)), None, 0, None) == 0
     _refused(lib, lib.eqlin_recurrence(None, None, 0, None), INVALID)
     assert lib.eqlin_recurrence_workspace(None) == 0 and lib.eqlin_recurrence_workspace(ctypes.byref(_rec(G=5))) == 0
-    assert lib.eqlin_recurrence_marks(0, 3) == 3 and lib.eqlin_recurrence_marks(1000, 2) == 9 and lib.eqlin_recurrence_marks(-1, 2) == 0
+    assert lib.eqlin_recurrence_marks(0, 3) == 3 and lib.eqlin_recurrence_marks(1000, 2) == 17 and lib.eqlin_recurrence_marks(-1, 2) == 0
     assert lib.eqlin_recurrence_workspace(ctypes.byref(_rec(total=1 << 20, longest=100))) == 0  # a sequence a workgroup
-    slots = (1 << 20) // 128 + 2
-    assert lib.eqlin_recurrence_workspace(ctypes.byref(_rec(total=1 << 20))) == 3 * slots * 64 * 4  # one that may be long
+    slots = (1 << 20) // 64 + 2
+    assert lib.eqlin_recurrence_workspace(ctypes.byref(_rec(total=1 << 20))) == 12 * slots * 64  # one that may be long
 
 
 @pytest.mark.parametrize("change", [
