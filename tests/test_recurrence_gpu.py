@@ -113,15 +113,18 @@ def _check(i, dtype, reverse, longest, label, with_state=True, with_dfinal=True)
     return y, final
 
 
-# longest: a hint (None: unknown). 1 takes the workgroup of one wave, 17 that of a sequence, None of many tokens the chunks side by side;
-# the results have to be right for each, whatever the lengths are.
-@pytest.mark.parametrize("longest", [None, 17, 1])
+# longest: a hint (None: unknown), which picks the form of the launch: 1 and 8 a wave a sequence, 17, 128 and 256 a workgroup with 1, 2 and 4
+# groups of lanes a wave, 1000 and None of many tokens the chunks side by side, without and with a launch for the states in front of
+# them. The results have to be right for each, whatever the lengths are.
+@pytest.mark.parametrize("longest", [None, 1, 8, 17, 128, 256, 1000])
 @pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
 @pytest.mark.parametrize("name", list(LENS))
 def test_recurrence(name, dtype, longest, cuda_device):
     lens = LENS[name]
-    for k, (C, G) in enumerate(WIDTHS if name != "long" else WIDTHS[2:5]):
-        reverse, gated = bool(k % 2), bool((k + (longest == 17)) % 3)
+    shift = 0 if longest is None else longest % 5  # other widths and options for each hint
+    for k in range(3):
+        (C, G), reverse = WIDTHS[(k + shift) % len(WIDTHS)], bool((k + shift) % 2)
+        gated = bool((k + shift // 2) % 3)
         label = f"recurrence {name} C={C} G={G} {dtype} longest={longest} reverse={reverse} gated={gated}"
         print(f"[case] {label}", flush=True)
         i = _inputs(lens, C, G, dtype, cuda_device, 100 * k + len(lens), lead=3 * (k % 3), tail=5 * (k % 2), gated=gated)
@@ -131,7 +134,7 @@ def test_recurrence(name, dtype, longest, cuda_device):
 def test_chunks_beyond_the_first_rows(cuda_device):
     """A first sequence that begins thousands of rows into the tensor: chunk slots in front of it belong to none."""
     i = _inputs([900, 400], 8, 4, "bf16", cuda_device, 1, lead=3000, tail=700)
-    for longest in (None, 17):
+    for longest in (None, 17, 128, 256):
         _check(i, "bf16", False, longest, f"lead 3000 longest={longest}")
         _check(i, "bf16", True, longest, f"lead 3000 reverse longest={longest}")
 
@@ -140,15 +143,24 @@ def test_many_sequences(cuda_device):
     """More sequences than a wave's search takes in one step (64), and in two (4096), in the chunks' form too."""
     lens = [1, 0, 2, 5] * 1100
     i = _inputs(lens, 2, 1, "f32", cuda_device, 2, lead=1)
-    for longest in (None, 5):
+    for longest in (None, 5, 256):
         _check(i, "f32", False, longest, f"4400 sequences longest={longest}")
+
+
+def test_a_sequence_of_more_chunks_than_a_join_takes_at_once(cuda_device):
+    """66000 tokens (1032 chunks) beside short ones; the states are carried over the join's stages, both ways."""
+    i = _inputs([3, 66000, 0, 70], 1, 2, "f32", cuda_device, 12)
+    _check(i, "f32", False, None, "66000 tokens")
+    _check(i, "f32", True, 20000, "66000 tokens, reverse, said to be 20000")
+    _check(i, "f32", False, 2000, "66000 tokens, said to be 2000")
 
 
 def test_state_in_place_and_in_pieces(cuda_device):
     """A step that updates its states in place, token by token and piece by piece, in every form of the launch; and the same bits
     every time."""
     dev = cuda_device
-    for lens, C, G, longest in [([1] * 300, 24, 4, 1), ([1] * 300, 24, 4, None), ([40, 0, 3, 200], 8, 2, 17), ([700, 0, 900, 5], 33, 1, None)]:
+    for lens, C, G, longest in [([1] * 300, 24, 4, 1), ([1] * 300, 24, 4, None), ([40, 0, 3, 200], 8, 2, 17), ([700, 0, 900, 5], 33, 1, None),
+                                ([700, 0, 300, 5], 32, 1, 128), ([700, 0, 300, 5], 32, 1, 256), ([700, 0, 300, 5], 32, 1, 1000), ([1, 8, 3], 6, 8, 8)]:
         i = _inputs(lens, C, G, "bf16", dev, 5)
         kw = dict(gate=i["gate"], longest=longest)
         y, final, _ = eq.recurrence(i["x"], i["forget"], i["cu"], state=i["state"], **kw)
@@ -175,7 +187,7 @@ def test_state_in_place_and_in_pieces(cuda_device):
 
 def test_what_is_not_finite_stays_in_its_sequence_and_column(cuda_device):
     dev = cuda_device
-    for longest in (None, 17):
+    for longest in (None, 17, 256, 1000):
         i = _inputs([300, 200, 650], 8, 2, "bf16", dev, 7)
         args = dict(gate=i["gate"], longest=longest)
         run = lambda st: (*eq.recurrence(i["x"], i["forget"], i["cu"], state=st["state"], with_marks=True, **args),)  # noqa: E731
@@ -252,7 +264,7 @@ def test_offsets_past_32_bits(cuda_device):
     for k, name in enumerate(("x", "forget", "gate")):
         far[name] = wide[:, (k + 1) * 64:(k + 1) * 64 + C, None]
         far[name].copy_(i[name])
-    for longest in (None, 17):
+    for longest in (None, 17, 128, 256):
         a = eq.recurrence(i["x"], i["forget"], i["cu"], gate=i["gate"], longest=longest, with_marks=True)
         b = eq.recurrence(far["x"], far["forget"], i["cu"], gate=far["gate"], longest=longest, with_marks=True, out=outs[:, :C, None])
         da = eq.recurrence_backward(i["dy"], i["x"], i["forget"], i["cu"], a[2], gate=i["gate"], longest=longest)
@@ -273,7 +285,7 @@ def test_group_shift_streams_and_graphs(cuda_device):
     back = eq.recurrence_backward(i["dy"], i["x"], i["forget"], i["cu"], marks, gate=i["gate"], with_state=True)
     side = torch.cuda.Stream()
     torch.cuda.synchronize()
-    for longest in (None, 130):
+    for longest in (None, 17, 130, 2000):
         with torch.cuda.stream(side):
             graph = torch.cuda.CUDAGraph()
             with torch.cuda.graph(graph, stream=side):
