@@ -764,8 +764,8 @@ def attention_backward(do: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: to
     return dq, dk, dv
 
 
-def _rows(t: torch.Tensor, name: str, like: torch.Tensor | None = None):
-    """t: [T, C, G], C * G contiguous; like ``like`` in shape, dtype and device."""
+def _rows(t: torch.Tensor, name: str, like: torch.Tensor | None = None) -> int:
+    """The token stride of t [T, C, G], C * G contiguous; like ``like`` in shape, dtype and device."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA (HIP) tensor")
     shape, strides = t.shape, t.stride()
@@ -775,6 +775,7 @@ def _rows(t: torch.Tensor, name: str, like: torch.Tensor | None = None):
         raise ValueError(f"{name}: a token's C * G elements must be contiguous")
     if like is not None and (shape != like.shape or t.dtype != like.dtype or t.get_device() != like.get_device()):
         raise ValueError(f"{name} must be {tuple(like.shape)} of {like.dtype} on {like.device}, got {tuple(shape)} {t.dtype} on {t.device}")
+    return strides[0]
 
 
 def recurrence_marks(T: int, batch: int) -> int:
@@ -782,13 +783,11 @@ def recurrence_marks(T: int, batch: int) -> int:
     return int(load_library().eqlin_recurrence_marks(int(T), int(batch)))
 
 
-def _recurrence_args(x, forget, cu, gate, out, state, final, marks, reverse, longest):
-    _rows(x, "x")
-    _rows(forget, "forget", x)
-    if gate is not None:
-        _rows(gate, "gate", x)
-    if out is not None:
-        _rows(out, "out", x)
+def _recurrence_args(x, forget, cu, gate, out, reverse, longest):
+    """The arguments without states and marks, and the shape of the states."""
+    xs, fs = _rows(x, "x"), _rows(forget, "forget", x)
+    gs = 0 if gate is None else _rows(gate, "gate", x)
+    ys = 0 if out is None else _rows(out, "out", x)
     T, C, G = x.shape
     _need_cuda(cu, "cu")
     B = cu.numel() - 1
@@ -797,10 +796,9 @@ def _recurrence_args(x, forget, cu, gate, out, state, final, marks, reverse, lon
     _index(cu, "cu", (B + 1,), x.get_device())
     if longest is not None and longest < 0:
         raise ValueError(f"longest = {longest} < 0")
-    args = RecurrenceArgs(x.data_ptr(), forget.data_ptr(), _ptr(gate), _ptr(out), _ptr(state), _ptr(final), _ptr(marks),
-                          x.stride(0), forget.stride(0), 0 if gate is None else gate.stride(0), 0 if out is None else out.stride(0),
-                          cu.data_ptr(), T, longest or 0, B, C, G, 1 if reverse else 0, _dtype_code(x.dtype))
-    return args, B
+    args = RecurrenceArgs(x.data_ptr(), forget.data_ptr(), _ptr(gate), _ptr(out), None, None, None, xs, fs, gs, ys, cu.data_ptr(), T,
+                          longest or 0, B, C, G, 1 if reverse else 0, _dtype_code(x.dtype))
+    return args, (B, C, G)
 
 
 def recurrence(x: torch.Tensor, forget: torch.Tensor, cu: torch.Tensor, gate: torch.Tensor | None = None,
@@ -815,15 +813,14 @@ def recurrence(x: torch.Tensor, forget: torch.Tensor, cu: torch.Tensor, gate: to
     left as they are."""
     if out is None and isinstance(x, torch.Tensor):
         out = x.new_empty(x.shape)
-    a, B = _recurrence_args(x, forget, cu, gate, out, None, None, None, reverse, longest)
-    shape = (B, *x.shape[1:])
+    a, shape = _recurrence_args(x, forget, cu, gate, out, reverse, longest)
     if state is not None:
         a.state = _f32_out(state, shape, x.device, "state").data_ptr()
-    final = _f32_out(final, shape, x.device, "final")
+    final = x.new_empty(shape, dtype=torch.float32) if final is None else _f32_out(final, shape, x.device, "final")
     a.final = final.data_ptr()
     lib, marks, pa = load_library(), None, ctypes.byref(a)
     if with_marks:
-        marks = x.new_empty((lib.eqlin_recurrence_marks(x.shape[0], B), *x.shape[1:]), dtype=torch.float32)
+        marks = x.new_empty((lib.eqlin_recurrence_marks(a.total, a.batch), *shape[1:]), dtype=torch.float32)
         a.marks = marks.data_ptr()
     need = lib.eqlin_recurrence_workspace(pa)
     workspace = _workspace(workspace, need, x.device) if need else None
@@ -841,12 +838,11 @@ def recurrence_backward(dy: torch.Tensor, x: torch.Tensor, forget: torch.Tensor,
     """eqlin_recurrence_backward -> (dx, dforget, dgate, dstate) from dy, the forward's tensors and its marks. dfinal: the
     gradient of final (None: zeros). dx, dforget, dgate: tensors to write to (views of one gradient of a layer's output,
     say), else new ones; dgate is None without a gate, dstate (float32 [batch, C, G]) without with_state."""
-    a, B = _recurrence_args(x, forget, cu, gate, None, None, None, None, reverse, longest)
+    a, shape = _recurrence_args(x, forget, cu, gate, None, reverse, longest)
     _rows(dy, "dy", x)
     lib, pa = load_library(), ctypes.byref(a)
-    shape = (B, *x.shape[1:])
-    a.marks = _f32_out(marks, (lib.eqlin_recurrence_marks(x.shape[0], B), *x.shape[1:]), x.device, "marks").data_ptr() \
-        if marks is not None else None
+    if marks is not None:
+        a.marks = _f32_out(marks, (lib.eqlin_recurrence_marks(a.total, a.batch), *shape[1:]), x.device, "marks").data_ptr()
     if dfinal is not None:
         _f32_out(dfinal, shape, x.device, "dfinal")
     grads = []
