@@ -278,11 +278,12 @@ eqlin_status_t eqlin_conv_forward_expanded(eqlin_handle_t h, const void *x, cons
                                            int H, int W, eqlin_stream_t stream);
 
 /*
- * ---- The operators around the layer in a transformer stage ----
+ * ---- The operators around the layer in a transformer or recurrent stage ----
  *
  * A stage holds its tokens as x[N][C][G] and runs: norm, EQ-Linear (q, k, v), rotary positions, attention,
- * EQ-Linear, norm with the residual's addition, MLP block. The three operators below are the ones between
- * the layers, forward and backward. They need no handle: everything is an argument, and a call works on the
+ * EQ-Linear, norm with the residual's addition, MLP block; a recurrent one has a gated recurrence in place of
+ * positions and attention. The operators below are the ones between the layers (root-mean-square or layer
+ * norm, rotary positions, attention, recurrence), forward and backward. They need no handle: everything is an argument, and a call works on the
  * current device and on `stream` only. The rules of the head of this file hold (arguments checked on the
  * host before anything is enqueued, no allocation, no synchronisation, no exceptions); contents of device
  * arrays (positions, sequence bounds) cannot be checked there, and no kernel reads or writes outside the
