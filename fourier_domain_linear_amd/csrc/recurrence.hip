@@ -38,15 +38,18 @@ constexpr int kWindow = 16;              // chunks whose ends CHUNK goes over by
 enum Mode { SEQ, ENDS, CHUNK };
 
 // sigmoid(z) and 1 - sigmoid(z), both to a few units of fp32's last place (half types: the hardware's exponential of
-// the product with log2 e, relative error up to |z| 2^-24, far below their rounding; its exponent kept below 126, where 1 + e has
-// a reciprocal, so a gate forgets to 2^-126 at most; the minimum passes NaN on). FORGET: the reciprocal is corrected once by its
-// remainder, since a channel that remembers for hundreds of tokens multiplies as many of them: uncorrected, gradients of
-// initial states over up to 4096 tokens were off by 1.25e-6 of their size instead of 3.5e-7 (states 2.0e-7 and 1.0e-7).
+// the product with log2 e, relative error up to |z| 2^-24, far below their rounding). FORGET: the reciprocal is corrected once by
+// its remainder, since a channel that remembers for hundreds of tokens multiplies as many of them: uncorrected, gradients of
+// initial states over up to 4096 tokens were off by 1.25e-6 of their size instead of 3.5e-7 (states 2.0e-7 and 1.0e-7). In the
+// half types its exponent is kept below 126, where 1 + e has a reciprocal and e / (1 + e) a value, so a gate forgets to 2^-126 at
+// most; the minimum passes NaN on. An output gate is multiplied by its sigmoid, which has to come down to 0 (gates of the type's lowest
+// value): there the exponential may be infinite, and 1 - sigmoid is the difference, since 1 + gate (1 - sigmoid) needs no more.
 template <class E, bool FORGET>
 __device__ __forceinline__ void sigmoid(float z, float &f, float &rest) {
     float e;
     if constexpr (__is_same(E, F32)) e = expf(-fabsf(z));
-    else e = __builtin_amdgcn_exp2f(__builtin_elementwise_minimum(-1.4426950408889634f * z, 126.0f));
+    else if constexpr (FORGET) e = __builtin_amdgcn_exp2f(__builtin_elementwise_minimum(-1.4426950408889634f * z, 126.0f));
+    else e = __builtin_amdgcn_exp2f(-1.4426950408889634f * z);
     const float d = 1.0f + e;
     float r = __builtin_amdgcn_rcpf(d);
     if constexpr (FORGET) r = fmaf(fmaf(-d, r, 1.0f), r, r);
@@ -56,7 +59,7 @@ __device__ __forceinline__ void sigmoid(float z, float &f, float &rest) {
         rest = z >= 0.0f ? s : r;
     } else {
         f = r;
-        rest = e * r;
+        rest = FORGET ? e * r : 1.0f - r;
     }
 }
 

@@ -232,6 +232,27 @@ def test_extreme_gates(cuda_device):
     assert dh[0] == 4 and dh[2] == 4 and max(abs(dh[1]), abs(dh[3])) <= 4 * 2.0 ** -126  # (half types: f is at least 2^-126)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+def test_output_gates_of_the_lowest_and_highest_value(dtype, cuda_device):
+    """silu of the type's lowest value is 0 (whatever the state), of its largest the value itself, of 0 and of large negative ones
+    next to nothing; the gradients follow."""
+    dev, dt = cuda_device, DT[dtype]
+    top = torch.finfo(dt).max
+    o = torch.tensor([-top, -top / 2, -200.0, -88.0, 0.0, 30.0], dtype=dt, device=dev).view(1, 6, 1).repeat(3, 1, 1)
+    x = torch.tensor([100.0, -3.0, 0.25], device=dev).view(3, 1, 1).repeat(1, 6, 1).to(dt)
+    z = torch.zeros_like(x)
+    cu = torch.tensor([0, 3], dtype=torch.int32, device=dev)
+    y, _, marks = eq.recurrence(x, z, cu, gate=o, with_marks=True)
+    dy = torch.ones_like(x)
+    dx, dz, do, _ = eq.recurrence_backward(dy, x, z, cu, marks, gate=o)
+    torch.cuda.synchronize()
+    for t in (y, dx, dz, do):
+        assert bool(t.isfinite().all()) and float(t[:, :4].abs().max()) <= 1e-30
+    h = stage.recurrence(_np(x), _np(z), [0, 3])[0]
+    assert not y[:, 4].any() and np.allclose(_np(do[:, 4]), h[:, 4] / 2, rtol=2 * U[dtype])
+    assert np.allclose(_np(y[:, 5]), 30 * h[:, 5], rtol=2 * U[dtype]) and np.allclose(_np(do[:, 5]), h[:, 5], rtol=2 * U[dtype])
+
+
 def test_gradients_by_differences(cuda_device):
     """Against central differences of the kernel's own forward (fp32, h = 2^-6: third-order terms of size h^2 and rounding of
     2^-24 |sum| / h, both under 1e-3 here)."""
