@@ -528,7 +528,7 @@ __global__ void __launch_bounds__(64 * W) k_recurrence(const RecurrenceParams p,
 //
 // What goes back over a stretch's start, g_t = f_t dh_t, is composed from the last token on with the same A:
 // g -> A g + B'. The states come again from x and forget, exactly as the forward had them, from its marks: the states in
-// front of each chunk. SEQ and CHAIN as above, the chunks taken from the last to the first.
+// front of each chunk. SEQ, ENDS and CHUNK as above, the chunks taken from the last to the first.
 template <class E, int EC, int TW, int W, int GR, bool GATE, Mode MODE>
 __global__ void __launch_bounds__(64 * W) k_recurrence_bwd(const RecurrenceParams p, int strips, int64_t units) {
     typedef Pack<E, EC> PK;

@@ -350,8 +350,8 @@ eqlin_status_t eqlin_rmsnorm_backward(const void *sum, const void *gamma, const 
  *   sum          device [N][C][G], receives s, or NULL;  y device [N][C][G];  mean, rstd device float [N] or NULL.
  *   N >= 0 (0 enqueues nothing); C >= 1; G in {1, 2, 4, 8}; C * G <= 2^20 (else UNSUPPORTED); eps >= 0, finite.
  * x, residual, sum and y must be 16-byte aligned; outputs overlap neither the inputs nor each other.
- * Rows that are no whole number of 16-byte vectors run slower; so do those longer than 16384 values (fp32: 8192; rows of
- * odd length: 2048, even ones of a half type: 4096), which are read three times.
+ * Rows that are no whole number of 16-byte vectors run slower; so do those longer than 16384 values (fp32: 8192; where they
+ * are no whole vectors 2048, an even number of a half type's 4096), which are read three times.
  */
 eqlin_status_t eqlin_layernorm(const void *x, const void *residual, const void *gamma, const void *beta, void *sum, void *y,
                                float *mean, float *rstd, int64_t N, int C, int G, float eps, eqlin_dtype_t dtype,
