@@ -41,9 +41,11 @@ enum Mode { SEQ, ENDS, CHUNK };
 // the product with log2 e, relative error up to |z| 2^-24, far below their rounding). FORGET: the reciprocal is corrected once by
 // its remainder, since a channel that remembers for hundreds of tokens multiplies as many of them: uncorrected, gradients of
 // initial states over up to 4096 tokens were off by 1.25e-6 of their size instead of 3.5e-7 (states 2.0e-7 and 1.0e-7). In the
-// half types its exponent is kept below 126, where 1 + e has a reciprocal and e / (1 + e) a value, so a gate forgets to 2^-126 at
-// most; the minimum passes NaN on. An output gate is multiplied by its sigmoid, which has to come down to 0 (gates of the type's lowest
-// value): there the exponential may be infinite, and 1 - sigmoid is the difference, since 1 + gate (1 - sigmoid) needs no more.
+// half types its exponent is kept below 126, where 1 + e has a reciprocal and e / (1 + e) a value, the minimum passing NaN on; the
+// 2^-126 left there are taken off again: a gate of the type's lowest value or of minus infinity has to forget all of a state
+// however large, and no f from 2^-101 on changes by it. An output gate is multiplied by its sigmoid, which has to come down to 0
+// (gates of the type's lowest value): there the exponential may be infinite, and 1 - sigmoid is the difference, since
+// 1 + gate (1 - sigmoid) needs no more.
 template <class E, bool FORGET>
 __device__ __forceinline__ void sigmoid(float z, float &f, float &rest) {
     float e;
@@ -58,7 +60,7 @@ __device__ __forceinline__ void sigmoid(float z, float &f, float &rest) {
         f = z >= 0.0f ? r : s;
         rest = z >= 0.0f ? s : r;
     } else {
-        f = r;
+        f = FORGET ? r - 0x1p-126f : r;
         rest = FORGET ? e * r : 1.0f - r;
     }
 }

@@ -479,7 +479,7 @@ eqlin_status_t eqlin_attention_backward(const eqlin_attention_args *a, const eql
  *
  * h starts from the sequence's state (zeros without one) and its last value is the sequence's final. The operator acts on
  * each group element alone, so a shift of the group axis passes through. fp32 throughout (states, marks, the exponentials'
- * results); one rounding of y. A value that is not finite makes later results of its own sequence and column not
+ * results; in the half types f is 0 from gates of -87.4 down, elsewhere within 2^-126 and a few units of fp32); one rounding of y. A value that is not finite makes later results of its own sequence and column not
  * finite (infinite or NaN) and has no part in any other.
  *   x, forget, gate, y   tensor[token][C][G] of dtype with token strides in ELEMENTS (C * G contiguous): parts of one
  *                layer's output, say. gate may be NULL. Token strides from C * G to 2^24. Odd widths,

@@ -1,0 +1,50 @@
+"""A forget gate of minus infinity or of the type's lowest value starts a sequence anew: f is exactly 0, so no state in front of it,
+however large, has a part in what comes after, and no gradient behind it in what comes before. Tolerances: none, the same bits."""
+import pytest
+import torch
+
+import fourier_domain_linear_amd as eq
+from test_norm_rotary_gpu import DT
+from test_recurrence_gpu import _inputs
+
+pytestmark = pytest.mark.gpu
+
+LENS = [200, 1, 70]
+RESET = {0: [40, 130], 1: [0], 2: [69]}  # of each sequence, its tokens with such gates
+
+
+def _case(dtype, lowest, reverse, dev):
+    """Inputs whose other gates remember (f = 0.9975), and the rows of the gates in question, by sequence, in the recurrence's order."""
+    i = _inputs(LENS, 6, 4, dtype, dev, 3)
+    i["forget"][:] = 6.0
+    rows = {k: [i["edges"][k + 1] - 1 - t if reverse else i["edges"][k] + t for t in at] for k, at in RESET.items()}
+    for at in rows.values():
+        i["forget"][at] = lowest
+    return i, rows
+
+
+# the launch's forms, by the hint that picks them (test_recurrence_gpu.py)
+@pytest.mark.parametrize("longest", [None, 1, 8, 17, 128, 256, 1000])
+@pytest.mark.parametrize("lowest", ["lowest", "-inf"])
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+def test_nothing_passes_a_gate_of_the_lowest_value(dtype, lowest, longest, cuda_device):
+    low = -float("inf") if lowest == "-inf" else torch.finfo(DT[dtype]).min
+    for reverse in (False, True):
+        i, rows = _case(dtype, low, reverse, cuda_device)
+        kw = dict(gate=i["gate"], reverse=reverse, longest=longest)
+        # states of 3e38 (times 2^-126 still 3.5) in front, and none
+        far, none = (eq.recurrence(i["x"], i["forget"], i["cu"], state=torch.full_like(i["state"], s), with_marks=True, **kw) for s in (3e38, 0.0))
+        # the gradients of final, likewise (1e37 times 2^-126: 0.12)
+        _, _, marks = eq.recurrence(i["x"], i["forget"], i["cu"], state=i["state"], with_marks=True, **kw)
+        back = [eq.recurrence_backward(i["dy"], i["x"], i["forget"], i["cu"], marks, dfinal=torch.full_like(i["dfinal"], s), with_state=True, **kw)
+                for s in (1e37, 0.0)]
+        torch.cuda.synchronize()
+        assert torch.equal(far[1], none[1]), reverse  # final
+        assert torch.equal(back[0][3], back[1][3]) and not back[0][3][1].any(), reverse  # dstate
+        for k, at in rows.items():
+            first, last = i["edges"][k], i["edges"][k + 1]
+            after = slice(first, at[0] + 1) if reverse else slice(at[0], last)
+            before = slice(at[-1] + 1, last) if reverse else slice(first, at[-1])
+            assert bool(none[0][after].isfinite().all()) and torch.equal(far[0][after], none[0][after]), (reverse, k)
+            for a, b in zip(back[0][:3], back[1][:3]):
+                assert bool(b[before].isfinite().all()) and torch.equal(a[before], b[before]), (reverse, k)
