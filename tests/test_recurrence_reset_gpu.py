@@ -1,10 +1,13 @@
 """A forget gate of minus infinity or of the type's lowest value starts a sequence anew: f is exactly 0, so no state in front of it,
-however large, has a part in what comes after, and no gradient behind it in what comes before. Tolerances: none, the same bits."""
+however large, has a part in what comes after, and no gradient behind it in what comes before (tolerances: none, the same bits);
+its own gradient is 0."""
+import numpy as np
 import pytest
 import torch
 
 import fourier_domain_linear_amd as eq
-from test_norm_rotary_gpu import DT
+from oracle import stage as ref
+from test_norm_rotary_gpu import DT, U, _np
 from test_recurrence_gpu import _inputs
 
 pytestmark = pytest.mark.gpu
@@ -48,3 +51,30 @@ def test_nothing_passes_a_gate_of_the_lowest_value(dtype, lowest, longest, cuda_
             assert bool(none[0][after].isfinite().all()) and torch.equal(far[0][after], none[0][after]), (reverse, k)
             for a, b in zip(back[0][:3], back[1][:3]):
                 assert bool(b[before].isfinite().all()) and torch.equal(a[before], b[before]), (reverse, k)
+
+
+@pytest.mark.parametrize("longest", [None, 1, 17, 128, 256, 1000])
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+def test_the_gradient_of_a_gate_behind_masked_values(dtype, longest, cuda_device):
+    """Tokens whose values are masked by the type's lowest value, a gate that forgets them, gradients of some hundreds behind it:
+    dforget = dh (h - x) f (1 - f) is 0 there, though dh (h - x) is beyond fp32, and what it says at the masked token. Bar there: one
+    rounding of the result (u), and 1e-5 for the factors (each within a few units of fp32, sums of two terms of one sign or far apart)."""
+    dev, dt, low = cuda_device, DT[dtype], torch.finfo(DT[dtype]).min
+    for reverse in (False, True):
+        i, rows = _case(dtype, low, reverse, dev)
+        gates = [r for k in (0, 2) for r in rows[k]]
+        masked = [r + 1 if reverse else r - 1 for r in gates]
+        i["x"][masked], i["forget"][masked] = low, 0.0
+        dy = torch.full_like(i["dy"], 8.0)
+        dy[masked] = 0.5
+        kw = dict(reverse=reverse, longest=longest)
+        _, _, marks = eq.recurrence(i["x"], i["forget"], i["cu"], state=i["state"], with_marks=True, **kw)
+        dx, dz, _, dstate = eq.recurrence_backward(dy, i["x"], i["forget"], i["cu"], marks, dfinal=i["dfinal"], with_state=True, **kw)
+        torch.cuda.synchronize()
+        for t in (dx, dz, dstate):
+            assert bool(t.isfinite().all()), reverse
+        assert not dz[gates].any(), reverse
+        with np.errstate(over="ignore"):  # (exp of the lowest gates' size, under a 1 /)
+            want = ref.recurrence_backward(_np(dy), _np(i["x"]), _np(i["forget"]), i["edges"], None, _np(i["state"]), reverse, _np(i["dfinal"]))[1]
+        want = want[masked]
+        assert bool((abs(_np(dz[masked]) - want) <= (U[dtype] + 1e-5) * abs(want)).all()), reverse
