@@ -101,3 +101,27 @@ def test_planted_mistakes_are_seen(slip):
         assert not np.allclose(dy * stage.recurrence(x, z, cu, None, h0)[0] * sig, do)
     else:  # the share of x left out of the gate's gradient
         assert not np.allclose(dz, dz + dx * x / (1 + np.exp(-z)))
+
+
+@pytest.mark.parametrize("slip", ["x left out", "state of the token itself", "the gate's own factor left out"])
+def test_slips_in_the_forget_gates_gradient_are_seen(slip):
+    """dforget = dh (h[t-1] - x) f (1 - f): central differences agree with it and with none of the slips."""
+    x, z, o, dy, h0, df, cu = _case(5)
+    dx, dz, _, _ = stage.recurrence_backward(dy, x, z, cu, o, h0, False, df)
+
+    def loss(b):
+        y, final, _ = stage.recurrence(x, b, cu, o, h0)
+        return (y * dy).sum() + (final * df).sum()
+
+    want = _diff(loss, z)
+    f, keep = 1 / (1 + np.exp(-z)), 1 / (1 + np.exp(z))
+    dh = dx / keep
+    h = stage.recurrence(x, z, cu, None, h0)[0]
+    before = np.concatenate([h[:1], h[:-1]])
+    for i in range(4):
+        if cu[i] < cu[i + 1]:
+            before[cu[i]] = h0[i]
+    assert np.allclose(dz, want, atol=1e-8) and np.allclose(dh * (before - x) * f * keep, want, atol=1e-8)
+    wrong = {"x left out": dh * before * f * keep, "state of the token itself": dh * (h - x) * f * keep,
+             "the gate's own factor left out": dh * (before - x) * keep}[slip]
+    assert not np.allclose(wrong, want, atol=1e-3)
