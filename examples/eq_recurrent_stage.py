@@ -38,8 +38,9 @@ class RecurrentStage:
 
     def forward(self, x: torch.Tensor, cu: torch.Tensor, state: torch.Tensor | None = None, longest: int | None = None,
                 training: bool = False):
-        """x [N, C, G] of sequences packed at the bounds cu, state float32 [batch, C, G] -> (normalised output, residual
-        stream, states after the last tokens, what the gradients need)."""
+        """x [N, C, G] of sequences packed at the bounds cu (from 0 to N: rows of no sequence would come out of the recurrence
+        unwritten), state float32 [batch, C, G] -> (normalised output, residual stream, states after the last tokens, what the
+        gradients need)."""
         C = self.C
         y1, _, m1, r1 = eq.layernorm(x, self.gamma[0], self.beta[0])
         mix = eq.forward(self.layer["mix"], y1, self.b["mix"])

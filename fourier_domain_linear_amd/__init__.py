@@ -810,7 +810,7 @@ def recurrence(x: torch.Tensor, forget: torch.Tensor, cu: torch.Tensor, gate: to
     reverse: from the last token to the first. longest: tokens of the longest sequence, where the caller knows (a hint).
     final: float32 [batch, C, G], the states after the last tokens (pass state itself to update it in place). marks: what
     recurrence_backward needs, float32 [recurrence_marks(T, batch), C, G], None without with_marks. Rows of y outside every sequence are
-    left as they are."""
+    left as they are (of a new y: whatever its memory held; pass a cleared ``out`` where something reads them)."""
     if out is None and isinstance(x, torch.Tensor):
         out = x.new_empty(x.shape)
     a, shape = _recurrence_args(x, forget, cu, gate, out, reverse, longest)
@@ -837,7 +837,8 @@ def recurrence_backward(dy: torch.Tensor, x: torch.Tensor, forget: torch.Tensor,
                         workspace: torch.Tensor | None = None):
     """eqlin_recurrence_backward -> (dx, dforget, dgate, dstate) from dy, the forward's tensors and its marks. dfinal: the
     gradient of final (None: zeros). dx, dforget, dgate: tensors to write to (views of one gradient of a layer's output,
-    say), else new ones; dgate is None without a gate, dstate (float32 [batch, C, G]) without with_state."""
+    say), else new ones, whose rows outside every sequence hold whatever their memory held; dgate is None without a gate, dstate
+    (float32 [batch, C, G]) without with_state."""
     a, shape = _recurrence_args(x, forget, cu, gate, None, reverse, longest)
     _rows(dy, "dy", x)
     lib, pa = load_library(), ctypes.byref(a)

@@ -15,13 +15,13 @@
 // long sequences), a workgroup a chunk of kChunk tokens: ENDS leaves each chunk's (A, B), CHUNK takes the state in front of its
 // chunk through the (A, B) of those before it (JOIN does that between the two for sequences of more than kWindow chunks)
 // and does the rest. x and forget are then read twice. (One launch, in which each chunk waits for what those before it publish, was
-// built and measured: the hops from chunk to chunk through memory took longer than the second reading, 71 to 89 us against 61
+// built and measured: the hops from chunk to chunk through memory took longer than the second reading, 71 to 89 us against the 61 of then
 // for 65536 tokens of 384 columns.)
 //
 // No atomics, every sum in an order that depends on sizes alone: the same bits every time. Bound by memory where the sequences fill
-// the card (bf16, 64 sequences of 196 tokens of 256 x 8 with a gate: 48.9 us, 206 MB, 4.2 TB/s; a large copy reaches 5.0), by a
-// round's latency where they do not (16 of 784 tokens of 192 x 4, gate, forward and gradients 62 us, 46 at the copy's rate),
-// by the second reading in the split form (one of 65536 tokens of 96 x 4 61 us, 30 at the copy's rate).
+// the card (bf16, 64 sequences of 196 tokens of 256 x 8 with a gate: 48.5 us, 206 MB, 4.2 TB/s; a large copy reaches 5.0), by a
+// round's latency where they do not (16 of 784 tokens of 192 x 4, gate, forward and gradients 63 us, 42 at the copy's rate),
+// by the second reading in the split form (one of 65536 tokens of 96 x 4 62 us, 30 at the copy's rate).
 //
 // Everything is held in fp32; 1 - f is computed as sigmoid(-forget), without the cancellation; results are rounded once.
 // Sequences never meet in a sum, so what is not finite in one has no part in another.
@@ -756,8 +756,19 @@ hipError_t run_type(const RecurrenceParams &p, bool back, hipStream_t s) {
 // 64 to 4096 tokens. floor: the bytes that must move, at 5 TB/s. SEQ takes `round` for each 64 tokens a group of lanes of the longest
 // sequence, and a part of the floor beside it; narrower strips (more groups) take longer rounds and more of the memory's time (a row's
 // stretch is 64 bytes of a half type with 4), but more workgroups and fewer rounds. The split form reads twice.
-// In bf16, 1, 2, 4 groups and split: 32 sequences of 1024 tokens of 256 columns 32.0, 19.7, 16.5, 23.7 us; 128 of 1024 41.2, 40.8, 56.9,
-// 79.4; 2 of 4096 113.5, 63.7, 33.8, 15.3.
+// Measured in us, 1, 2, 4 groups, split (the form that is taken in brackets; over 64 such points it is within 6 % of the best):
+//                    32 sequences of 1024 x 256    128 of 1024 x 256          2 of 4096 x 256            64 of 196 x 2048
+//   bf16             34.4 21.4 [16.9] 24.9        41.6 [42.2] 58.3 82.6      120.7 67.5 35.6 [15.8]    [33.1] 36.6 54.5 68.0
+//   bf16 gate        42.1 24.5 [21.5] 27.8        [52.5] 54.9 76.6 94.3      155.9 85.1 45.6 [17.5]    [45.2] 46.9 67.8 80.6
+//   bf16 back        48.2 30.2 [27.3] 28.3        [75.2] 70.3 99.7 103.8     174.4 96.5 54.1 [17.0]    [51.1] 57.0 91.9 85.4
+//   bf16 gate back   62.0 38.1 [36.0] 42.5        [102.6] 107.6 149.1 159.6  233.8 127.9 70.0 [19.2]   [91.9] 88.3 125.6 132.5
+//   fp32             46.2 29.6 [21.9] 36.3        [84.6] 81.4 88.4 134.4     161.7 86.8 45.6 [20.2]    [60.3] 61.8 67.9 111.3
+//   fp32 gate        74.5 45.2 [31.5] 44.3        [113.9] 112.5 123.4 155.0  246.8 128.1 66.5 [23.1]   [87.0] 99.1 115.1 131.6
+//   fp32 back        88.4 49.8 [36.5] 47.9        [140.8] 135.2 148.6 174.9  283.5 133.4 71.7 [23.8]   [107.2] 105.2 109.8 133.7
+//   fp32 gate back   128.8 72.4 [52.6] 72.8       [193.9] 195.9 211.5 282.3  419.8 202.3 106.1 [27.0]  [163.3] 160.7 169.5 224.6
+// The number of sequences has no part in it, and JOIN takes a workgroup a sequence and 16 columns whatever the sequence's length: a long
+// prompt beside many single tokens pays for them (bf16, one of 32768 tokens of 384 columns: 36 us alone, 43 beside 100 single
+// tokens, 75 beside 512, 112 beside 1000, which take 3.4 in a call of their own).
 void plan_recurrence(RecurrenceParams &p, eqlin_dtype_t dtype, bool back) {
     const int64_t L = (int64_t)p.C << p.lg;
     const bool f32 = dtype == EQLIN_F32;

@@ -351,7 +351,9 @@ eqlin_status_t eqlin_rmsnorm_backward(const void *sum, const void *gamma, const 
  *   N >= 0 (0 enqueues nothing); C >= 1; G in {1, 2, 4, 8}; C * G <= 2^20 (else UNSUPPORTED); eps >= 0, finite.
  * x, residual, sum and y must be 16-byte aligned; outputs overlap neither the inputs nor each other.
  * Rows that are no whole number of 16-byte vectors run slower; so do those longer than 16384 values (fp32: 8192; where they
- * are no whole vectors 2048, an even number of a half type's 4096), which are read three times.
+ * are no whole vectors 2048, an even number of a half type's 4096), which are read three times, and in the gradients also
+ * those of more than 8192 channels. Sums are fp32: a row whose values sum beyond its range has y = NaN, one whose
+ * squares about the mean do rstd = 0 and y = beta (rows of values under 1e16 never do; no other row is touched).
  */
 eqlin_status_t eqlin_layernorm(const void *x, const void *residual, const void *gamma, const void *beta, void *sum, void *y,
                                float *mean, float *rstd, int64_t N, int C, int G, float eps, eqlin_dtype_t dtype,
@@ -471,16 +473,20 @@ eqlin_status_t eqlin_attention_backward(const eqlin_attention_args *a, const eql
                                         size_t workspace_bytes, eqlin_stream_t stream);
 
 /*
- * eqlin_recurrence -- gated linear recurrence over packed sequences, a stage's other way to mix tokens (next to attention;
- * an EQ-VMamba block, "lpnh.cn/news/964151", mixes by a recurrence whose inputs EQ-Linear layers produce). For the
- * tokens t of a sequence in order (reverse: from the last to the first) and every channel and group element:
+ * eqlin_recurrence -- gated linear recurrence over packed sequences, a stage's other way to mix tokens (next to attention),
+ * its inputs and gates the outputs of EQ-Linear layers. One state a channel and group element, the input's factor 1 - f:
+ * a simpler recurrence than the state-space block of the EQ-VMamba page ("lpnh.cn/news/964151"), which it does not stand for.
+ * For the tokens t of a sequence in order (reverse: from the last to the first) and every channel and group element:
  *
  *     f = sigmoid(forget[t]);   h = f h + (1 - f) x[t];   y[t] = h,  or  h silu(gate[t]) with an output gate
  *
  * h starts from the sequence's state (zeros without one) and its last value is the sequence's final. The operator acts on
- * each group element alone, so a shift of the group axis passes through. fp32 throughout (states, marks, the exponentials'
- * results; in the half types f is 0 from gates of -87.4 down, elsewhere within 2^-126 and a few units of fp32); one rounding of y. A value that is not finite makes later results of its own sequence and column not
- * finite (infinite or NaN) and has no part in any other.
+ * each group element alone, so a shift of the group axis passes through; all group elements go along the tokens in the same
+ * order, so turning an image passes through only as far as its tokens' order does. fp32 throughout (states, marks, the
+ * exponentials' results; in the half types f is 0 from gates of -87.4 down, elsewhere within 2^-126 and a few units of fp32);
+ * one rounding of y. A forget gate of +-infinity is an f of 1 or 0. Any other value that is not finite can make results of its
+ * own sequence and column not finite (infinite or NaN), from its token on and in the gradients up to it too; it has no part in
+ * any other.
  *   x, forget, gate, y   tensor[token][C][G] of dtype with token strides in ELEMENTS (C * G contiguous): parts of one
  *                layer's output, say. gate may be NULL. Token strides from C * G to 2^24. Odd widths,
  *                strides or pointers off two elements run a slower kernel.
