@@ -665,7 +665,9 @@ __global__ void __launch_bounds__(64 * W) k_recurrence_bwd(const RecurrenceParam
 #pragma unroll
                     for (int j = 0; j < EC; ++j) {
                         const float gx = rest[k][j] * d[k][j];
-                        w[j] = gx * f[k][j] * (h[j] - v[j]);  // (f first: where it is 0, dh (h - x) may be beyond fp32)
+                        // f first and h and x apart: dh (h - x) and h - x may be beyond fp32 where the gradient is not, or is 0
+                        const float t = gx * f[k][j];
+                        w[j] = fmaf(t, h[j], -(t * v[j]));
                         h[j] = fmaf(f[k][j], h[j], rest[k][j] * v[j]);
                         if constexpr (GATE) s[j] = q[k][j] * h[j];
                         v[j] = gx;

@@ -486,7 +486,8 @@ eqlin_status_t eqlin_attention_backward(const eqlin_attention_args *a, const eql
  * exponentials' results; in the half types f is 0 from gates of -87.4 down, elsewhere within 2^-126 and a few units of fp32);
  * one rounding of y. A forget gate of +-infinity is an f of 1 or 0. Any other value that is not finite can make results of its
  * own sequence and column not finite (infinite or NaN), from its token on and in the gradients up to it too; it has no part in
- * any other.
+ * any other. States are rounded sums: x of fp32's largest value token after token can round to infinity (a half type's lowest
+ * value, as a mask, keeps at least 0.4 % away from it); dforget is not finite where dh f (1 - f) times h or x is beyond fp32.
  *   x, forget, gate, y   tensor[token][C][G] of dtype with token strides in ELEMENTS (C * G contiguous): parts of one
  *                layer's output, say. gate may be NULL. Token strides from C * G to 2^24. Odd widths,
  *                strides or pointers off two elements run a slower kernel.

@@ -78,3 +78,18 @@ def test_the_gradient_of_a_gate_behind_masked_values(dtype, longest, cuda_device
             want = ref.recurrence_backward(_np(dy), _np(i["x"]), _np(i["forget"]), i["edges"], None, _np(i["state"]), reverse, _np(i["dfinal"]))[1]
         want = want[masked]
         assert bool((abs(_np(dz[masked]) - want) <= (U[dtype] + 1e-5) * abs(want)).all()), reverse
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_masked_values_under_a_state_of_the_other_sign(dtype, cuda_device):
+    """h - x beyond fp32 (a state of 3e37, a value of the type's lowest), dh (h - x) f (1 - f) not: the bar of the masked tokens above."""
+    dev, dt = cuda_device, DT[dtype]
+    x = torch.zeros((3, 6, 4), dtype=dt, device=dev)
+    x[0] = torch.finfo(dt).min
+    z, dy = torch.full_like(x, 2.0), torch.full_like(x, 0.25)
+    cu, state = torch.tensor([0, 3], dtype=torch.int32, device=dev), torch.full((1, 6, 4), 3e37, device=dev)
+    _, _, marks = eq.recurrence(x, z, cu, state=state, with_marks=True)
+    _, dz, _, _ = eq.recurrence_backward(dy, x, z, cu, marks)
+    torch.cuda.synchronize()
+    want = ref.recurrence_backward(_np(dy), _np(x), _np(z), [0, 3], None, _np(state))[1][0]
+    assert bool((abs(_np(dz[0]) - want) <= (U[dtype] + 1e-5) * abs(want)).all())
